@@ -502,6 +502,135 @@ int i8q_dq_lstm_state_codes(const void* workspace, int64_t T, int64_t batch, int
                             int64_t* row_stride);
 
 /* ========================================================================
+ * Paged key/value cache: what lies between two quantized products when a
+ * model answers one token at a time (not on the pages; the int8 rows follow
+ * [DQIP]'s symmetric quantization, scale = max|x| / 127).
+ *
+ * A cache is two pools of pages, K and V, each [pages, kv_heads, page_size,
+ * head_dim] in any order of the first three axes (strides below).  A
+ * sequence owns the pages that its row of the page table names: its token t
+ * lies in page table[b][t / page_size] at offset t % page_size.
+ *
+ * I8Q_S8 pools hold codes with one fp32 scale per token and head:
+ *   scale = max|x| / 127 (1 when the row is zero),
+ *   code  = saturate(rint(x / scale)),    value = code * scale,
+ * each operation rounded once in fp32.  I8Q_BF16 pools hold the values
+ * rounded to bf16 and have no scales.  A row that holds an infinity or a NaN
+ * gets a scale that is one, so that what attends to it is not finite either.
+ *
+ * Page numbers, sequence numbers, token indices and positions are device
+ * data.  One outside its range is never followed: the token it names is left
+ * out (no read, no write) and i8q_sync_status reports I8Q_ERR_INVALID_ARG.
+ * ====================================================================== */
+#define I8Q_KV_MAX_HEAD_DIM 256
+#define I8Q_ROTARY_MAX_AXES 4
+
+typedef struct i8q_kv_cache {
+  void* k;          /* pools; 16-byte aligned, strides multiples of 16 bytes */
+  void* v;
+  float* k_scale;   /* [pages, kv_heads, page_size]; I8Q_S8 only, else NULL */
+  float* v_scale;
+  float* score;     /* accumulated attention weight per token and head, or NULL */
+  int type;         /* I8Q_S8 | I8Q_BF16 */
+  int64_t pages, kv_heads, page_size;
+  int64_t head_dim; /* a multiple of 16, at most I8Q_KV_MAX_HEAD_DIM */
+  int64_t page_stride, head_stride, token_stride;                   /* elements of k and v; head_dim is contiguous */
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride; /* elements of k_scale, v_scale and score */
+} i8q_kv_cache;
+
+typedef struct i8q_page_table {
+  const int32_t* table; /* [sequences][max_pages], rows `stride` entries apart; */
+  int64_t sequences;    /* entries past a sequence's last token are not read */
+  int64_t max_pages;    /* max_pages * page_size < 2^31 */
+  int64_t stride;
+} i8q_page_table;
+
+/* Rotary positions.  Pair j < pairs of a head is turned by the angle whose
+ * cosine and sine stand at [positions[pair_axis[j]][t]][j] of the tables:
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin   (each operation rounded once),
+ * with (x1, x2) = (x[j], x[j + pairs]), or (x[2j], x[2j+1]) when interleaved.
+ * Elements from 2 * pairs on pass unchanged. */
+typedef struct i8q_rotary {
+  const int32_t* positions;  /* device [axes][tokens], rows position_stride entries apart */
+  int64_t position_stride;
+  int64_t axes;              /* 1 .. I8Q_ROTARY_MAX_AXES, e.g. time, height, width */
+  const float* cos;          /* device [rows][pairs] */
+  const float* sin;
+  int64_t rows;
+  int64_t pairs;             /* 2 * pairs <= head_dim */
+  const uint8_t* pair_axis;  /* host [pairs]: the axis of each pair; NULL: axis 0 */
+  int interleaved;
+} i8q_rotary;
+
+/* Write `tokens` new tokens into the cache.  Token t becomes token index[t]
+ * of sequence seq[t] (device int32; seq < 0: the token is left out, as a
+ * padded batch wants).  k, v: [tokens, kv_heads, head_dim] of `type`
+ * (I8Q_F32 | I8Q_BF16); q: [tokens, q_heads, head_dim] or NULL with q_heads
+ * 0, and q_out of the same type and shape (q itself is allowed).  Strides in
+ * elements (token, head), head_dim contiguous.  rotary (may be NULL) turns q
+ * and k.  The tokens' scores become 0 when the cache keeps scores.  Two
+ * tokens of one call must not name the same place.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq, const int32_t* index,
+                  int64_t tokens, int type, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                  const void* v, int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                  int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, void* q_out,
+                  int64_t q_out_token_stride, int64_t q_out_head_stride, const i8q_rotary* rotary, void* stream);
+
+/* Read tokens back: k_out and v_out [tokens, kv_heads, head_dim] of `type`
+ * (I8Q_F32 | I8Q_BF16) receive the values of token index[t] of sequence
+ * seq[t] (rows with seq < 0 are not written).
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq, const int32_t* index,
+                  int64_t tokens, int type, void* k_out, int64_t k_token_stride, int64_t k_head_stride, void* v_out,
+                  int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* Attention of one new token per sequence.  q and out: [sequences, q_heads,
+ * head_dim] of `type` (I8Q_F32 | I8Q_BF16), strides in elements; query head
+ * h reads key/value head h / (q_heads / kv_heads).  Over the tokens t of
+ * sequence b, from max(0, lengths[b] - window) (window 0: from 0) to
+ * lengths[b] - 1:
+ *   s_t = softmax_scale * (q . k_t),  p = softmax(s),  out = sum_t p_t v_t,
+ *   lse[b][h] = log sum_t exp(s_t)   (device fp32 [sequences, q_heads], or NULL)
+ * and, when accumulate is not 0, score of token t += the sum of p_t over the
+ * query heads that share its key/value head (sequences of one call must then
+ * not share pages).  A sequence of length 0 gives out = 0 and lse =
+ * -infinity.  lengths (device int32) above max_pages * page_size are cut to
+ * that and reported like the other indices.  Nothing past lengths[b] is
+ * read.  Sums, maxima and statistics are fp32.  bf16 queries: the weights
+ * p_t enter the second product in 11 bits (int8 cache) or 16 (bf16 cache);
+ * fp32 queries: q and p_t in at least 22.  workspace: at least
+ * i8q_paged_attention_workspace_size bytes, 256-byte aligned, not shared by
+ * calls that may run at the same time; its contents need not be kept.
+ * Results do not depend on the run: no atomics order the sums.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* lengths, int type,
+                        const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, void* out,
+                        int64_t out_token_stride, int64_t out_head_stride, float* lse, float softmax_scale,
+                        int64_t window, int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* 0 for arguments that i8q_paged_attention refuses. */
+size_t i8q_paged_attention_workspace_size(const i8q_kv_cache* cache, const i8q_page_table* table, int64_t q_heads,
+                                          int accumulate);
+
+/* Evict by accumulated attention weight.  Of each sequence b and key/value
+ * head, n = min(lengths[b], budget) tokens are kept: all of them when
+ * lengths[b] <= budget, else the first `sink`, the last `recent`, and
+ * between those the budget - sink - recent of the largest score (NaN counts
+ * as -infinity, -0 as 0; equal scores: the lowest index first).  The kept
+ * tokens' keys, values, scales and scores are copied, in their order, to
+ * tokens 0 .. n-1 of the pages that new_table names in the same pools.  The
+ * old pages are only read (they may be shared, or go back to the allocator
+ * once this call is done); a new page must not be one of them.
+ * kept: device int32 [sequences, kv_heads, budget], the kept tokens'
+ * indices, -1 from n on.  new_lengths: device int32 [sequences], or NULL.
+ * sink + recent <= budget <= new_table's max_pages * page_size.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* lengths,
+                 const i8q_page_table* new_table, int32_t* kept, int64_t budget, int64_t sink, int64_t recent,
+                 int32_t* new_lengths, void* stream);
+
+/* ========================================================================
  * Measurement (not on the pages)
  * ====================================================================== */
 
@@ -525,8 +654,10 @@ int i8q_profile_entry(int i, const char** name, long long* launches, double* tot
 int i8q_measure_int8_mma_peak(int64_t iters, void* stream, double* tops);
 
 /* Synchronize `stream` and report any error recorded by a device-side
- * bounded wait since the last call (I8Q_ERR_DEVICE_TIMEOUT), or a pending
- * CUDA error (I8Q_ERR_CUDA).  Clears the recorded state. */
+ * bounded wait since the last call (I8Q_ERR_DEVICE_TIMEOUT), an index
+ * outside its range that a key/value cache call met in device data
+ * (I8Q_ERR_INVALID_ARG), or a pending CUDA error (I8Q_ERR_CUDA).  Clears the
+ * recorded state. */
 int i8q_sync_status(void* stream);
 
 /* Failure-detection probe (not on the pages): launch one small kernel on

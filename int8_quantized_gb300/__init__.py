@@ -17,6 +17,7 @@ from ._lib import (ACT_GELU, ACT_IDENTITY, ACT_RELU, BF16, F32, LSTM_BIDIRECTION
 
 __all__ = ["QGemmDyn", "quantize_linear", "dequantize_linear", "qlinearconv", "qlinearconv_workspace_size",
            "dq_lstm_forward", "dq_lstm_forward_ex", "dq_lstm_state_codes", "dq_lstm_workspace_size", "sync_status",
+           "KVCache", "kv_append", "kv_gather", "kv_evict", "paged_attention", "paged_attention_workspace_size",
            "version", "I8QError", "last_error",
            "F32", "BF16", "S8", "U8", "S32", "ACT_IDENTITY", "ACT_RELU", "ACT_GELU", "NO_AXIS",
            "LSTM_FORWARD", "LSTM_REVERSE", "LSTM_BIDIRECTIONAL"]
@@ -385,6 +386,177 @@ def qlinear_unary(op, X, x_scale, x_zero_point, y_scale, y_zero_point, Y, alpha=
                                  X.numel(), _TORCH_TYPE[X.dtype], float(x_scale), int(x_zero_point), float(y_scale),
                                  int(y_zero_point), float(alpha), _dev(Y, "Y"), _stream(stream)), "qlinear_unary")
     return Y
+
+
+class KVCache:
+    """A paged key/value cache: the pools of pages that a serving program
+    keeps (i8q_kv_cache), checked once.
+
+    k, v: [pages, kv_heads, page_size, head_dim] CUDA tensors, int8 (codes,
+    with k_scale, v_scale fp32 [pages, kv_heads, page_size]) or bf16, of the
+    same strides: any order of the first three axes, head_dim contiguous.
+    score: fp32 [pages, kv_heads, page_size], the accumulated attention
+    weight of each token, or None.  The tensors stay the caller's; the object
+    keeps references to them."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, score=None):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+                raise TypeError(f"{name} must be a CUDA tensor of 4 axes")
+        if k.dtype not in (torch.int8, torch.bfloat16) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be int8 or both be bfloat16")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        if k.stride(3) != 1:
+            raise ValueError("head_dim must be contiguous")
+        per = [(t, n) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale"), (score, "score")) if t is not None]
+        for t, name in per:
+            if not isinstance(t, torch.Tensor) or t.device != k.device or t.dtype != torch.float32:
+                raise TypeError(f"{name} must be a float32 tensor beside k")
+            if t.shape != k.shape[:3] or t.stride() != per[0][0].stride():
+                raise ValueError(f"{name} must be [pages, kv_heads, page_size], of the others' strides")
+        if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an int8 cache needs k_scale and v_scale, a bfloat16 cache has none")
+        self.k, self.v, self.k_scale, self.v_scale, self.score = k, v, k_scale, v_scale, score
+        ptr = [None if t is None else t.data_ptr() for t in (k, v, k_scale, v_scale, score)]
+        scale_strides = per[0][0].stride() if per else (0, 0, 0)
+        self._struct = _lib.KVCacheStruct(*ptr, _TORCH_TYPE[k.dtype], *k.shape, *k.stride()[:3], *scale_strides)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _page_table(t, name="page_table"):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2:
+        raise TypeError(f"{name} must be an int32 CUDA tensor of 2 axes")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return _lib.PageTableStruct(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0))
+
+
+def _rows(t, name, n, heads, dim, dtype):
+    """Pointer and (token, head) strides of a [n, heads, dim] CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.shape != (n, heads, dim) or (t.stride(2) != 1 and dim > 1):
+        raise ValueError(f"{name} must be [{n}, {heads}, {dim}] with a contiguous last axis, got {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _i32(t, name, n):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return t.data_ptr()
+
+
+def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions=None, cos=None, sin=None,
+              pair_axis=None, interleaved=False, stream=None):
+    """Write tokens into the cache: token t becomes token index[t] of
+    sequence seq[t] (int32; seq < 0: left out).  k, v [tokens, kv_heads,
+    head_dim] fp32 or bf16, any token and head strides; q, q_out [tokens,
+    q_heads, head_dim] of the same type (q_out may be q).  With cos and sin
+    (fp32 [rows, pairs]) and positions (int32 [axes, tokens], or [tokens])
+    q and k are turned first; pair_axis: the axis of each pair (default 0);
+    interleaved: pairs are (2j, 2j+1) instead of (j, j + pairs).  See
+    i8q_kv_append.  Returns q_out."""
+    T, H, D = k.shape
+    rot = None
+    if (cos is None) != (sin is None) or (cos is None) != (positions is None):
+        raise ValueError("positions, cos and sin come together")
+    if cos is not None:
+        if not (positions.is_cuda and positions.dtype == torch.int32) or positions.dim() > 2:
+            raise TypeError("positions must be an int32 CUDA tensor of 1 or 2 axes")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.shape[-1] != T or (positions.stride(-1) != 1 and T > 1):
+            raise ValueError("positions must be [axes, tokens] with contiguous rows")
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous float32 CUDA tensor")
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must both be [rows, pairs]")
+        if pair_axis is not None and len(pair_axis) != cos.shape[1]:
+            raise ValueError("pair_axis must have an entry for each pair")
+        rot = ctypes.byref(_lib.RotaryStruct(positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0,
+                                             axes, cos.data_ptr(), sin.data_ptr(), *cos.shape,
+                                             None if pair_axis is None else bytes(pair_axis), int(bool(interleaved))))
+    shape = cache.k.shape
+    qs, qo, heads = (None, 0, 0), (None, 0, 0), 0
+    if q is not None:
+        heads = q.shape[1]
+        qs, qo = _rows(q, "q", T, heads, shape[3], k.dtype), _rows(q_out, "q_out", T, heads, shape[3], k.dtype)
+    check(_L().i8q_kv_append(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", T),
+                             _i32(index, "index", T), T, _float_type(k), *_rows(k, "k", T, shape[1], shape[3], k.dtype),
+                             *_rows(v, "v", T, shape[1], shape[3], k.dtype), *qs, heads, *qo, rot, _stream(stream)),
+          "kv_append")
+    return q_out
+
+
+def _float_type(t):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"expected float32 or bfloat16, got {t.dtype}")
+    return _TORCH_TYPE[t.dtype]
+
+
+def kv_gather(cache, page_table, seq, index, k_out, v_out, stream=None):
+    """Read tokens back: k_out, v_out [tokens, kv_heads, head_dim] (fp32 or
+    bf16) receive token index[t] of sequence seq[t] (i8q_kv_gather)."""
+    T, shape = k_out.shape[0], cache.k.shape
+    check(_L().i8q_kv_gather(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", T),
+                             _i32(index, "index", T), T, _float_type(k_out),
+                             *_rows(k_out, "k_out", T, shape[1], shape[3], k_out.dtype),
+                             *_rows(v_out, "v_out", T, shape[1], shape[3], k_out.dtype), _stream(stream)), "kv_gather")
+    return k_out, v_out
+
+
+def paged_attention_workspace_size(cache, page_table, q_heads, accumulate=False):
+    n = int(_L().i8q_paged_attention_workspace_size(cache._ref, ctypes.byref(_page_table(page_table)), q_heads,
+                                                    int(bool(accumulate))))
+    if n == 0:
+        raise I8QError(_lib.ERR_INVALID_ARG, "paged_attention_workspace_size")
+    return n
+
+
+def paged_attention(cache, page_table, lengths, q, out, lse=None, softmax_scale=None, window=0, accumulate=False,
+                    workspace=None, stream=None):
+    """Attention of one new token per sequence over its pages: q, out
+    [sequences, q_heads, head_dim] fp32 or bf16; lengths int32 [sequences];
+    lse fp32 [sequences, q_heads] or None; softmax_scale: default
+    1 / sqrt(head_dim); window: the last `window` tokens only (0: all);
+    accumulate: add each token's weight to cache.score.  See
+    i8q_paged_attention.  Returns out."""
+    shape = cache.k.shape
+    B, heads = page_table.shape[0], q.shape[1]
+    if workspace is None:
+        workspace = torch.empty(paged_attention_workspace_size(cache, page_table, heads, accumulate),
+                                dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)  # allocated on the current stream, used on that one
+    if lse is not None and lse.shape != (B, heads):
+        raise ValueError(f"lse must be [{B}, {heads}]")
+    check(_L().i8q_paged_attention(cache._ref, ctypes.byref(_page_table(page_table)), _i32(lengths, "lengths", B),
+                                   _float_type(q), *_rows(q, "q", B, heads, shape[3], q.dtype), heads,
+                                   *_rows(out, "out", B, heads, shape[3], q.dtype), _dev(lse, "lse", torch.float32),
+                                   shape[3] ** -0.5 if softmax_scale is None else softmax_scale, window,
+                                   int(bool(accumulate)), _dev(workspace, "workspace"),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)), "paged_attention")
+    return out
+
+
+def kv_evict(cache, page_table, lengths, new_table, kept, new_lengths=None, sink=0, recent=0, stream=None):
+    """Keep, of each sequence and head, the first `sink`, the last `recent`
+    and the highest-scored other tokens, budget = kept.shape[2] in all, and
+    copy them in order to the pages of new_table (i8q_kv_evict).  kept int32
+    [sequences, kv_heads, budget] receives their indices (-1 past the end),
+    new_lengths int32 [sequences] the new lengths.  Returns kept."""
+    B, H = page_table.shape[0], cache.k.shape[1]
+    if kept.dim() != 3 or kept.shape[:2] != (B, H):
+        raise ValueError(f"kept must be [{B}, {H}, budget]")
+    check(_L().i8q_kv_evict(cache._ref, ctypes.byref(_page_table(page_table)), _i32(lengths, "lengths", B),
+                            ctypes.byref(_page_table(new_table, "new_table")), _i32(kept, "kept", kept.numel()),
+                            kept.shape[2], sink, recent,
+                            None if new_lengths is None else _i32(new_lengths, "new_lengths", B), _stream(stream)),
+          "kv_evict")
+    return kept
 
 
 def dq_lstm_workspace_size(T, batch, input_size, hidden, direction):

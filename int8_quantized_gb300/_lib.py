@@ -22,6 +22,29 @@ _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
 
+
+
+class KVCacheStruct(ctypes.Structure):
+    """i8q_kv_cache"""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("score", _p), ("type", _i), ("pages", _i64),
+                ("kv_heads", _i64), ("page_size", _i64), ("head_dim", _i64), ("page_stride", _i64),
+                ("head_stride", _i64), ("token_stride", _i64), ("scale_page_stride", _i64),
+                ("scale_head_stride", _i64), ("scale_token_stride", _i64)]
+
+
+class PageTableStruct(ctypes.Structure):
+    """i8q_page_table"""
+    _fields_ = [("table", _p), ("sequences", _i64), ("max_pages", _i64), ("stride", _i64)]
+
+
+class RotaryStruct(ctypes.Structure):
+    """i8q_rotary"""
+    _fields_ = [("positions", _p), ("position_stride", _i64), ("axes", _i64), ("cos", _p), ("sin", _p),
+                ("rows", _i64), ("pairs", _i64), ("pair_axis", ctypes.c_char_p), ("interleaved", _i)]
+
+
+_cache, _table, _rotary = (ctypes.POINTER(c) for c in (KVCacheStruct, PageTableStruct, RotaryStruct))
+
 # name -> (restype, argtypes); mirrors include/i8q.h
 SIGNATURES = {
     "i8q_last_error": (ctypes.c_char_p, []),
@@ -62,6 +85,13 @@ SIGNATURES = {
     "i8q_dq_lstm_forward": (_i, [_p, _i64, _i64, _i64, _i64, _i, _p, _p, _p, _sz, _p, _p, _p, _sz, _p, _p, _p, _p,
                                  _p, _p, _p, _sz, _p]),
     "i8q_dq_lstm_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i]),
+    "i8q_kv_append": (_i, [_cache, _table, _p, _p, _i64, _i, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p,
+                           _i64, _i64, _rotary, _p]),
+    "i8q_kv_gather": (_i, [_cache, _table, _p, _p, _i64, _i, _p, _i64, _i64, _p, _i64, _i64, _p]),
+    "i8q_paged_attention": (_i, [_cache, _table, _p, _i, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, _f, _i64, _i, _p,
+                                 _sz, _p]),
+    "i8q_paged_attention_workspace_size": (_sz, [_cache, _table, _i64, _i]),
+    "i8q_kv_evict": (_i, [_cache, _table, _p, _table, _p, _i64, _i64, _i64, _p, _p]),
     "i8q_sync_status": (_i, [_p]),
     "i8q_debug_wait_timeout": (_i, [_i, _i64, _p]),
     "i8q_profile_enable": (_i, [_i]),

@@ -197,6 +197,9 @@ extern "C" int i8q_sync_status(void* stream) {
   I8Q_CUDA_TRY(cudaMemcpy(&h, w, sizeof(h), cudaMemcpyDeviceToHost));
   if (h) {
     I8Q_CUDA_TRY(cudaMemset(w, 0, sizeof(uint32_t)));
+    if (h == ST_KV_INDEX)
+      return fail(I8Q_ERR_INVALID_ARG,
+                  "a key/value cache call met a page, sequence, token index, length or position outside its range");
     return fail(I8Q_ERR_DEVICE_TIMEOUT, "a device-side bounded wait gave up (status " + std::to_string(h) + ")");
   }
   return I8Q_OK;
