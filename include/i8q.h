@@ -595,11 +595,13 @@ int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* table, const 
  * and, when accumulate is not 0, score of token t += the sum of p_t over the
  * query heads that share its key/value head (sequences of one call must then
  * not share pages).  A sequence of length 0 gives out = 0 and lse =
- * -infinity.  lengths (device int32) above max_pages * page_size are cut to
+ * -infinity, and so do scores that are all -infinity.  A NaN or an infinity
+ * that enters a sequence's sums makes their results NaN or infinite, and no
+ * other sequence's.  lengths (device int32) above max_pages * page_size are cut to
  * that and reported like the other indices.  Nothing past lengths[b] is
  * read.  Sums, maxima and statistics are fp32.  bf16 queries: the weights
- * p_t enter the second product in 11 bits (int8 cache) or 16 (bf16 cache);
- * fp32 queries: q and p_t in at least 22.  workspace: at least
+ * p_t enter the second product in 16 bits; fp32 queries: q and p_t in at
+ * least 22 (q relative to its largest element).  workspace: at least
  * i8q_paged_attention_workspace_size bytes, 256-byte aligned, not shared by
  * calls that may run at the same time; its contents need not be kept.
  * Results do not depend on the run: no atomics order the sums.

@@ -1,5 +1,41 @@
 // kv_attention.cu -- attention of one new token per sequence over a paged
-// key/value cache.
+// key/value cache of int8 codes or bf16 values.
+//
+// For a key/value head, its G query heads and the tokens t of a sequence:
+//   s_t = (q . k_t) softmax_scale log2 e,  o = sum_t 2^(s_t - m) v_t / l,
+//   l = sum_t 2^(s_t - m),
+// in one pass with a running m.  Every key and value is used once for a
+// few heads, so the bound is the memory that holds them: at G = 4, D = 128
+// and int8 a token costs 264 bytes and 4 kFLOP, where the card does 280
+// FLOP per byte.  What a kernel has to do is keep enough reads in flight and
+// spend few instructions per byte:
+//
+//  - a warp takes tiles of 16 tokens.  It forms S^T = K Q^T (tokens as the
+//    16 rows of mma.m16n8k16, heads as its 8 columns) and O^T = V^T P^T (head
+//    elements as rows), so that 8 heads cost no padding of the 16-row side.
+//    tcgen05 wants 128 rows of fp16 operands in shared memory: the codes would
+//    have to be converted and written back there, several times the traffic
+//    of the fragments, for a product that takes a tenth of the time;
+//  - a lane copies the 16-byte pieces that hold its own fragments (the
+//    order of the summation index is free, so both operands use the order in
+//    which a lane's piece lies in memory) into slots of shared memory that
+//    only it reads: an asynchronous copy into what amounts to more registers.
+//    There is no barrier in the loop, and a 16-token tile is 4 KB in flight;
+//  - int8 keys become fp16 by one LOP3 (the byte, sign flipped, as the low
+//    mantissa bits of 1024) and one subtraction per two codes; the query is
+//    scaled by a power of two to at most 2.  Values become bf16, by one LOP3
+//    more, because the weights that multiply them need its range;
+//  - the running maximum moves only when a score exceeds it by 2^8: p stays
+//    below 2^8, and most tiles need no reduction over the lanes;
+//  - value scales multiply p (in fp32) before it is split into bf16 parts.
+//
+// Work split.  Each row (sequence, key/value head, group of query heads) is
+// as long as its number of tiles plus a constant for its start and end;
+// the rows form one line, cut into equal parts, one per warp.  A row that
+// lies in one part is finished by that warp; of the others each warp leaves
+// m, l and o in the workspace, and a second kernel joins them.  The split
+// follows from the lengths alone, so results repeat.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include "kv.cuh"
@@ -15,6 +51,11 @@ struct Heads {  // [sequences][heads][dim], strides in elements
   int64_t token, head;
 };
 
+constexpr int kMaxSequences = 2048;  // of one launch: their line positions lie in shared memory
+constexpr int kRowCost = 2;          // of a row's start and end, in tiles
+constexpr int kMinPart = 8;          // a part is not shorter (in tiles) unless there are that many rows
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 struct Args {
   Cache c;
   Table tab;
@@ -22,114 +63,805 @@ struct Args {
   Heads q, out;
   float* lse;
   float scale;
-  int q_heads, window, accumulate;
-  float* logits;  // [sequences][q_heads][max tokens], accumulate only
-  float* stats;   // [sequences][q_heads] log sum of exponentials
+  int q_heads, group, chunks;  // group: query heads of a key/value head; chunks: rows that share one
+  int window;
+  int aligned_q, aligned_out;  // 16-byte loads of q rows, paired stores of out rows
+  int dp;                      // row pitch of the partial outputs
+  int heads_per_row;           // of a partial: 8 or 16
+  int parts;                   // warps of the first kernel
+  int64_t* line;               // [sequences + 1] start of each sequence on the line
+  float2* part_stats;          // [parts][2][heads_per_row] (m, l)
+  float* part_out;             // [parts][2][heads_per_row][dp]
+  float* logits;               // [sequences][q_heads][logit_pitch], or null
+  int64_t logit_pitch;
+  float* stats;                // [sequences][q_heads] m + log2 l (with logits)
   uint32_t* status;
 };
 
-// One CTA per sequence and query head; each warp takes every eighth token
-// and keeps a running maximum, sum and weighted value, joined at the end.
-template <class T, bool S8>
-__global__ void __launch_bounds__(256) attend_kernel(Args a) {
-  constexpr int E = I8Q_KV_MAX_HEAD_DIM / 32;
-  __shared__ float sm[8], sl[8], so[8][I8Q_KV_MAX_HEAD_DIM];
+__device__ __forceinline__ int first_token(const Args& a, int len) {
+  return a.window && len > a.window ? len - a.window : 0;
+}
+__device__ __forceinline__ int tile_count(const Args& a, int len) {
+  return len > 0 ? (len + 15) / 16 - first_token(a, len) / 16 : 0;
+}
+// Parts that a line of n units over `rows` rows is cut into.
+__device__ __forceinline__ int part_count(const Args& a, int64_t n, int64_t rows) {
+  const int64_t want = max(rows, (n + kMinPart - 1) / kMinPart);
+  return (int)min(want, (int64_t)a.parts);
+}
+__device__ __forceinline__ int64_t part_begin(int64_t n, int parts, int w) { return n * w / parts; }
+__device__ __forceinline__ int part_of(int64_t n, int parts, int64_t x) {
+  int w = (int)(x * parts / n);
+  while (part_begin(n, parts, w + 1) <= x) ++w;
+  while (part_begin(n, parts, w) > x) --w;
+  return w;
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+template <bool HALF>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (HALF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 transpose of 16-bit values over the warp (a lane holds two
+// neighbours of row lane / 4).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Codes in bytes 0 and 2 of w as two fp16: a byte with its
+// sign bit flipped is code + 128; under 0x64 it is the fp16 number 1024 +
+// (code + 128), from which 1152 is taken (exactly).
+__device__ __forceinline__ uint32_t even_codes(uint32_t w) {
+  const uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u;
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
+  return r;
+}
+// The same as bf16, whose 8 bits hold a code too: its low 7 bits under 0x43
+// are the bf16 number 128 + (code mod 128), its sign bit there makes 128 or
+// 256, and the difference is the code.
+__device__ __forceinline__ uint32_t even_codes_bf16(uint32_t w) {
+  const uint32_t u = (w & 0x007f007fu) | 0x43004300u, z = (w & 0x00800080u) | 0x43004300u;
+  uint32_t r;
+  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(z));
+  return r;
+}
+
+// x as the sum of `N` 16-bit floats, the largest first; two values a word.
+template <bool HALF, int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (HALF) {
+      const __half2 h = __floats2half2_rn(x, y);
+      r[i] = *reinterpret_cast<const uint32_t*>(&h);
+      if (i + 1 < N) x -= __low2float(h), y -= __high2float(h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      r[i] = *reinterpret_cast<const uint32_t*>(&h);
+      if (i + 1 < N) x -= __low2float(h), y -= __high2float(h);
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ float as_float(T x) {
+  if constexpr (std::is_same<T, float>::value) return x;
+  else return __bfloat162float(x);
+}
+
+// N consecutive elements of a q row, in fp32.
+template <class T, int N>
+__device__ __forceinline__ void load_row(const T* p, bool aligned, float (&x)[N]) {
+  if (aligned) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < N / V; ++i) {
+      const uint4 w = *reinterpret_cast<const uint4*>(p + i * V);
+      const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[i * V + j] = as_float(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = as_float(p[i]);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_pair(T* p, float x, float y, bool paired) {
+  if constexpr (std::is_same<T, float>::value) {
+    if (paired) *reinterpret_cast<float2*>(p) = make_float2(x, y);
+    else p[0] = x, p[1] = y;
+  } else {
+    if (paired) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+    else p[0] = __float2bfloat16_rn(x), p[1] = __float2bfloat16_rn(y);
+  }
+}
+
+// What a kernel is made for.  QT: type of q and out; S8: int8 cache, else
+// bf16; DP: head_dim rounded up to 64, 128 or 256; NT: groups of 8 heads.
+template <class QT_, bool S8_, int DP_, int NT_>
+struct Form {
+  using QT = QT_;
+  static constexpr bool S8 = S8_;
+  static constexpr int DP = DP_, NT = NT_;
+  static constexpr bool WIDE = std::is_same<QT, float>::value;
+  // 16-bit parts of q (fp16 of 11 bits, or bf16 of 8) and of the weights
+  // (bf16).  A bf16 query is exact in one; of the weights a bf16 output gets
+  // 16 bits, far below its own rounding, since one part's 2^-9 is not.
+  static constexpr int NQ = WIDE ? (S8 ? 2 : 3) : 1;
+  static constexpr int NP = WIDE ? 3 : 2;
+  static constexpr int ES = S8 ? 1 : 2;
+  static constexpr int KS = DP / 16;           // steps of the first product
+  static constexpr int MT = DP / 16;           // row blocks of the second
+  static constexpr int PK = DP * ES / 64;      // 16-byte pieces of a key row per lane
+  static constexpr int VB = S8 && DP == 64 ? 8 : 16;
+  static constexpr int PV = DP * ES / 8 / VB;  // pieces of a value row per lane
+  static constexpr int SLOT = 16 * DP * ES + 80;  // half a tile: pieces, 16 scales, the mask of its tokens
+  static constexpr int Q_WORDS = NQ * NT * KS * 2;
+  static constexpr bool MANY = S8 && DP <= 128 && NT == 1;     // 16 warps of 128 registers, else 8 or 4 of 255
+  static constexpr bool Q_REG = Q_WORDS <= (MANY ? 16 : 32);   // q fragments in registers
+  static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
+  static constexpr int W = MANY ? 16 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
+  static constexpr int AHEAD = ROOM >= 7 ? 3 : ROOM >= 5 ? 2 : 1;  // tiles in flight
+  static constexpr int SLOTS = 2 * AHEAD + 1;
+  static constexpr int WARP_BYTES = SLOTS * SLOT + Q_BYTES;
+  static constexpr int SMEM = W * WARP_BYTES + (kMaxSequences + 1) * 8 + 512;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // Head element that lane group g holds in row g of block mt (row g + 8: the next one).
+  __device__ static int row_element(int mt, int g) {
+    if constexpr (S8) return DP == 64 ? g * 8 + mt * 2 : mt / 8 * 128 + g * 16 + mt % 8 * 2;
+    else return mt / 4 * 64 + g * 8 + mt % 4 * 2;
+  }
+};
+
+template <class F>
+__global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_constant__ Args a) {
+  using QT = typename F::QT;
+  constexpr bool S8 = F::S8;
+  constexpr int NT = F::NT;
+  extern __shared__ __align__(16) unsigned char smem[];
+  int64_t* line = reinterpret_cast<int64_t*>(smem + F::W * F::WARP_BYTES);
+  int64_t* sums = line + kMaxSequences + 1;
   const Cache& c = a.c;
-  const int b = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads, kvh = h / (a.q_heads / c.heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
-  const int first = a.window && len > a.window ? len - a.window : 0;
-  const T* q = static_cast<const T*>(a.q.p) + b * a.q.token + h * a.q.head;
-  float x[E], acc[E];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
+  const int B = a.tab.sequences, R = c.heads * a.chunks;
+
+  next_kernel_may_start();
+
+  // ---- the line: where each sequence starts ----
+  {
+    int64_t run = 0;
+    for (int b0 = 0; b0 < B; b0 += F::W * 32) {
+      const int b = b0 + threadIdx.x;
+      int64_t v = 0;
+      if (b < B) v = (int64_t)(tile_count(a, kv::cut_length(c, a.tab, a.lengths[b], a.status)) + kRowCost) * R;
+      int64_t x = v;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int d = lane + 32 * e;
-    x[e] = d < c.dim ? (float)q[d] * a.scale : 0.0f;
-    acc[e] = 0.0f;
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, x, i);
+        if (lane >= i) x += u;
+      }
+      if (lane == 31) sums[warp] = x;
+      __syncthreads();
+      int64_t before = 0, all = 0;
+      for (int w = 0; w < F::W; ++w) {
+        const int64_t u = sums[w];
+        before += w < warp ? u : 0;
+        all += u;
+      }
+      if (b < B) line[b] = run + before + x - v;
+      run += all;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) line[B] = run;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b <= B; b += F::W * 32) a.line[b] = line[b];
   }
-  float m = -INFINITY, l = 0.0f;
-  float* logit = a.accumulate ? a.logits + (int64_t)blockIdx.x * a.tab.max_pages * c.page_size : nullptr;
-  for (int t = first + warp; t < len; t += 8) {
-    int page, off;
-    if (!kv::find(c, a.tab, b, t, page, off, a.status)) {
-      if (logit && lane == 0) logit[t] = -INFINITY;
-      continue;
-    }
-    const int64_t row = kv::row_at(c, page, kvh, off), sc = S8 ? kv::scale_at(c, page, kvh, off) : 0;
-    float s = 0.0f;
+  const int64_t n = line[B];
+  const int parts = part_count(a, n, (int64_t)B * R);
+  const int w = warp * gridDim.x + blockIdx.x;  // neighbouring parts on different SMs
+  if (w >= parts) return;
+  int64_t x = part_begin(n, parts, w);
+  const int64_t x_end = part_begin(n, parts, w + 1);
+  int b = 0;
+  for (int lo = 0, hi = B; lo < hi;) {  // last b with line[b] <= x
+    const int mid = (lo + hi) / 2;
+    if (line[mid] <= x) b = mid, lo = mid + 1;
+    else hi = mid;
+  }
+
+  unsigned char* ring = smem + warp * F::WARP_BYTES;
+  const uint32_t ring_u = smem_u32(ring);
+  uint2* q_smem = reinterpret_cast<uint2*>(ring + F::SLOTS * F::SLOT) + lane;
+  int put = 0, use = 0;                            // byte offsets of slots
+  const bool whole_pages = c.page_size % 16 == 0;  // a tile lies in one page
+  const int per_page = c.page_size / 16;
+  const int D = c.dim;
+
+  for (; x < x_end; ++b) {
+    const int64_t b_end = min(line[b + 1], x_end);
+    const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
+    const int first = first_token(a, len), tile0 = first / 16;
+    const int cost = tile_count(a, len) + kRowCost;
+    const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
+    while (x < b_end) {
+      const int row = (int)((x - line[b]) / cost);
+      const int64_t row_at = line[b] + (int64_t)row * cost;
+      const int in = (int)(x - row_at);
+      const int64_t seg_end = min(row_at + cost, x_end);
+      const int begin = max(in - kRowCost, 0), end = max((int)(seg_end - row_at) - kRowCost, 0);
+      const bool starts = in == 0, whole = starts && seg_end == row_at + cost;
+      const int kvh = row / a.chunks, h0 = kvh * a.group + (row % a.chunks) * (8 * NT);
+      const int heads = min(8 * NT, (kvh + 1) * a.group - h0);
+      x = seg_end;
+
+      // ---- copies: a tile is located once, then its keys, then its values are sent for ----
+      int64_t at = 0, scale_at = 0;  // of the tile's first row (whole pages) or of row lane % 16; of row lane % 16
+      uint32_t mask = 0;             // tokens of the tile that take part
+      int pg = 0, pg_off = 0, pg_next = -1, off_next = 0;
+      auto look_up = [&](int i) {  // the page of tile i + lane
+        pg_next = -1, off_next = 0;
+        if (i + lane < end) {
+          const int t = tile0 + i + lane, p = t / per_page;
+          off_next = (t - p * per_page) * 16;
+          pg_next = pages[p];
+        }
+      };
+      auto locate = [&](int i) {
+        const int r = lane & 15, t = (tile0 + i) * 16 + r;
+        bool ok = t >= first && t < len;
+        if (whole_pages) {
+          const int l = (i - begin) & 31;
+          if (l == 0) {
+            pg = pg_next, pg_off = off_next;
+            look_up(i + 32);
+          }
+          const int page = __shfl_sync(0xffffffffu, pg, l), off = __shfl_sync(0xffffffffu, pg_off, l);
+          if ((unsigned)page >= (unsigned)c.pages) {
+            ok = false;
+            if (lane == 0) kv::report_index(a.status);
+          }
+          at = kv::row_at(c, page, kvh, off);
+          scale_at = kv::scale_at(c, page, kvh, off + r);
+        } else {
+          int page = 0, off = 0;
+          if (ok) ok = kv::find(c, a.tab, b, t, page, off, a.status);
+          at = kv::row_at(c, page, kvh, off);
+          scale_at = kv::scale_at(c, page, kvh, off);
+        }
+        mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      };
+      auto row_of = [&](int r) {  // element offset of token r of the tile
+        return whole_pages ? at + r * c.token_stride : __shfl_sync(0xffffffffu, at, r);
+      };
+      auto send_scales = [&](uint32_t dst, const float* scale) {
+        if (lane < 16) {
+          const bool ok = mask >> lane & 1;
+          copy4(dst + 16 * F::DP * F::ES + lane * 4, ok ? scale + scale_at : scale, ok ? 4 : 0);
+        }
+      };
+      auto send_keys = [&](int i) {
+        if (i < end) {
+          locate(i);
+          const uint32_t dst = ring_u + put;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane + 32 * e;
-      if (d < c.dim)
-        s = fmaf(x[e], S8 ? (float)static_cast<const int8_t*>(c.k)[row + d]
-                          : (float)static_cast<const __nv_bfloat16*>(c.k)[row + d], s);
-    }
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    if (S8) s *= c.ks[sc];
-    if (logit && lane == 0) logit[t] = s;
-    const float mn = s > m ? s : m;
-    const float ref = mn == -INFINITY ? 0.0f : mn;  // no finite score yet: no weight either
-    const float keep = m == -INFINITY ? 0.0f : expf(m - ref), p = expf(s - ref);
-    m = mn;
-    l = l * keep + p;
-    const float pv = S8 ? p * c.vs[sc] : p;
+          for (int r = 0; r < 2; ++r) {
+            const int64_t src = row_of(g + 8 * r);
+            const bool ok = mask >> (g + 8 * r) & 1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane + 32 * e;
-      if (d < c.dim)
-        acc[e] = fmaf(pv, S8 ? (float)static_cast<const int8_t*>(c.v)[row + d]
-                             : (float)static_cast<const __nv_bfloat16*>(c.v)[row + d], acc[e] * keep);
+            for (int j = 0; j < F::PK; ++j) {
+              const int d = S8 ? j * 64 + tig * 16 : j * 32 + tig * 8;
+              const bool in_row = ok && d < D;
+              copy16(dst + ((r * F::PK + j) * 32 + lane) * 16,
+                     static_cast<const char*>(c.k) + (in_row ? (src + d) * F::ES : 0), in_row ? 16 : 0);
+            }
+          }
+          if constexpr (S8) send_scales(dst, c.ks);
+          if (lane == 0) *reinterpret_cast<uint32_t*>(ring + put + 16 * F::DP * F::ES + 64) = mask;
+        }
+        copy_commit();
+        put = put + F::SLOT == F::SLOTS * F::SLOT ? 0 : put + F::SLOT;
+      };
+      auto send_values = [&](int i) {  // of the tile located last
+        if (i < end) {
+          const uint32_t dst = ring_u + put;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 2 * tig + (r & 1) + (r & 2) * 4;
+            const int64_t src = row_of(t);
+            const bool ok = mask >> t & 1;
+#pragma unroll
+            for (int j = 0; j < F::PV; ++j) {
+              const int d = S8 ? j * 128 + g * F::VB : j * 64 + g * 8;
+              const bool in_row = ok && d < D;
+              const char* p = static_cast<const char*>(c.v) + (in_row ? (src + d) * F::ES : 0);
+              const uint32_t to = dst + ((r * F::PV + j) * 32 + lane) * F::VB;
+              if constexpr (F::VB == 16) copy16(to, p, in_row ? 16 : 0);
+              else copy8(to, p, in_row ? 8 : 0);
+            }
+          }
+          if constexpr (S8) send_scales(dst, c.vs);
+        }
+        copy_commit();
+        put = put + F::SLOT == F::SLOTS * F::SLOT ? 0 : put + F::SLOT;
+      };
+      use = put;  // the last row's copies have all been used
+      if (whole_pages) look_up(begin);
+#pragma unroll
+      for (int i = 0; i < F::AHEAD; ++i) {
+        send_keys(begin + i);
+        send_values(begin + i);
+      }
+
+      // ---- the query heads, as the columns of the first product ----
+      uint2 q_reg[F::Q_REG ? F::NQ * NT * F::KS : 1];
+      float factor[NT][2];  // of the scores of heads 2 tig and 2 tig + 1
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        constexpr int N = S8 ? 16 : 8;  // elements of a piece
+        float v[F::PK][N];
+        const bool live = nt * 8 + g < heads;
+        const QT* src = static_cast<const QT*>(a.q.p) + b * a.q.token + (int64_t)(h0 + nt * 8 + g) * a.q.head;
+#pragma unroll
+        for (int j = 0; j < F::PK; ++j) {
+          const int d = (j * 4 + tig) * N;
+          if (live && d < D) {
+            load_row<QT, N>(src + d, a.aligned_q, v[j]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[j][i] = 0.0f;
+          }
+        }
+        float f = a.scale * kLog2e;
+        if constexpr (S8) {
+          // by a power of two to [1, 2): fp16 then holds every element to
+          // 2^-25 of the largest
+          uint32_t most = 0;
+#pragma unroll
+          for (int j = 0; j < F::PK; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(fabsf(v[j][i])));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          most = min(most & 0x7f800000u, 0x7e800000u);
+          const float down = most ? __uint_as_float(0x7f000000u - most) : 1.0f;
+          if (most) f *= __uint_as_float(most);
+#pragma unroll
+          for (int j = 0; j < F::PK; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[j][i] *= down;
+        }
+        factor[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
+        factor[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+#pragma unroll
+        for (int ks = 0; ks < F::KS; ++ks) {
+          const float* e = S8 ? &v[ks / 4][ks % 4 * 4] : &v[ks / 2][ks % 2 * 4];
+          uint32_t r0[F::NQ], r1[F::NQ];
+          // int8 codes come as (0, 2) and (1, 3) of a word
+          split2<S8, F::NQ>(e[0], S8 ? e[2] : e[1], r0);
+          split2<S8, F::NQ>(S8 ? e[1] : e[2], e[3], r1);
+#pragma unroll
+          for (int i = 0; i < F::NQ; ++i) {
+            const int at_q = (i * NT + nt) * F::KS + ks;
+            if constexpr (F::Q_REG) q_reg[at_q] = make_uint2(r0[i], r1[i]);
+            else q_smem[at_q * 32] = make_uint2(r0[i], r1[i]);
+          }
+        }
+      }
+
+      // ---- the tiles ----
+      float o[F::MT][NT][4], m[NT][2], ref[NT][2], l[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int mt = 0; mt < F::MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.0f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        ref[nt][0] = ref[nt][1] = 0.0f;
+        l[nt][0] = l[nt][1] = 0.0f;
+      }
+      for (int i = begin; i < end; ++i) {
+        send_keys(i + F::AHEAD);
+        copy_wait<2 * F::AHEAD>();
+        __syncwarp();
+        const unsigned char* slot = ring + use;
+        use = use + F::SLOT == F::SLOTS * F::SLOT ? 0 : use + F::SLOT;
+        // bf16 keys may be infinite, and infinity times a later part of q (0, or
+        // of the other sign) is NaN: the first part's sum is kept apart
+        constexpr bool APART = !S8 && F::NQ > 1;
+        float s[NT][4], rest[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][j] = rest[nt][j] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < F::PK; ++j) {
+          const uint4 r0 = *reinterpret_cast<const uint4*>(slot + (j * 32 + lane) * 16);
+          const uint4 r1 = *reinterpret_cast<const uint4*>(slot + ((F::PK + j) * 32 + lane) * 16);
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+          for (int k = 0; k < (S8 ? 4 : 2); ++k) {
+            const int ks = j * (S8 ? 4 : 2) + k;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (S8) {
+              a0 = even_codes(w0[k]), a2 = even_codes(w0[k] >> 8);
+              a1 = even_codes(w1[k]), a3 = even_codes(w1[k] >> 8);
+            } else {
+              a0 = w0[2 * k], a2 = w0[2 * k + 1];
+              a1 = w1[2 * k], a3 = w1[2 * k + 1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int p = 0; p < F::NQ; ++p) {
+                const int at_q = (p * NT + nt) * F::KS + ks;
+                uint2 bq;
+                if constexpr (F::Q_REG) bq = q_reg[at_q];
+                else bq = q_smem[at_q * 32];
+                mma<S8>(APART && p ? rest[nt] : s[nt], a0, a1, a2, a3, bq.x, bq.y);
+              }
+          }
+        }
+        if constexpr (APART) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (fabsf(rest[nt][j]) < INFINITY) s[nt][j] += rest[nt][j];
+        }
+        const float* scales = reinterpret_cast<const float*>(slot + 16 * F::DP * F::ES);
+        const uint32_t taken = reinterpret_cast<const uint32_t*>(scales)[16];
+        const bool in0 = taken >> g & 1, in1 = taken >> (g + 8) & 1;
+        float k0 = 1.0f, k1 = 1.0f;
+        if constexpr (S8) k0 = scales[g], k1 = scales[g + 8];
+        bool rise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s[nt][j] = in0 ? s[nt][j] * k0 * factor[nt][j] : -INFINITY;
+            s[nt][2 + j] = in1 ? s[nt][2 + j] * k1 * factor[nt][j] : -INFINITY;
+            rise |= fmaxf(s[nt][j], s[nt][2 + j]) > m[nt][j] + 8.0f;
+          }
+        if (a.logits) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (nt * 8 + 2 * tig + j < heads) {
+                float* to = a.logits + ((int64_t)b * a.q_heads + h0 + nt * 8 + 2 * tig + j) * a.logit_pitch +
+                            (int64_t)(tile0 + i) * 16 + g;
+                to[0] = s[nt][j], to[8] = s[nt][2 + j];
+              }
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(m[nt][j], fmaxf(s[nt][j], s[nt][2 + j]));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              // no score above -infinity so far: nothing to keep, and s - 0 = -infinity
+              const float next = top == -INFINITY ? 0.0f : top;
+              const float keep = m[nt][j] == -INFINITY ? 0.0f : ex2_approx(m[nt][j] - next);
+              m[nt][j] = top, ref[nt][j] = next;
+              l[nt][j] *= keep;
+#pragma unroll
+              for (int mt = 0; mt < F::MT; ++mt) o[mt][nt][j] *= keep, o[mt][nt][2 + j] *= keep;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s[nt][j] = ex2_approx(s[nt][j] - ref[nt][j]);
+            s[nt][2 + j] = ex2_approx(s[nt][2 + j] - ref[nt][j]);
+            l[nt][j] += s[nt][j] + s[nt][2 + j];
+          }
+
+        send_values(i + F::AHEAD);
+        copy_wait<2 * F::AHEAD>();
+        __syncwarp();
+        slot = ring + use;
+        use = use + F::SLOT == F::SLOTS * F::SLOT ? 0 : use + F::SLOT;
+        float f0 = 1.0f, f1 = 1.0f;
+        if constexpr (S8) {
+          const float* vs = reinterpret_cast<const float*>(slot + 16 * F::DP * F::ES);
+          f0 = vs[g], f1 = vs[g + 8];
+        }
+        uint32_t b0[NT][F::NP], b1[NT][F::NP];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          split2<false, F::NP>(s[nt][0] * f0, s[nt][1] * f0, b0[nt]);
+          split2<false, F::NP>(s[nt][2] * f1, s[nt][3] * f1, b1[nt]);
+#pragma unroll
+          for (int p = 0; p < F::NP; ++p) b0[nt][p] = transpose8(b0[nt][p]), b1[nt][p] = transpose8(b1[nt][p]);
+        }
+        auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int p = 0; p < F::NP; ++p) mma<false>(o[mt][nt], a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
+        };
+#pragma unroll
+        for (int j = 0; j < F::PV; ++j) {
+          constexpr int N = F::VB / 4;  // words of a piece
+          uint32_t v[4][N];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const unsigned char* p = slot + ((r * F::PV + j) * 32 + lane) * F::VB;
+            if constexpr (F::VB == 16) {
+              const uint4 u = *reinterpret_cast<const uint4*>(p);
+              v[r][0] = u.x, v[r][1] = u.y, v[r][N - 2] = u.z, v[r][N - 1] = u.w;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(p);
+              v[r][0] = u.x, v[r][1] = u.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            // elements of two neighbouring tokens side by side
+            const uint32_t x0 = __byte_perm(v[0][k], v[1][k], 0x5410), x1 = __byte_perm(v[0][k], v[1][k], 0x7632);
+            const uint32_t y0 = __byte_perm(v[2][k], v[3][k], 0x5410), y1 = __byte_perm(v[2][k], v[3][k], 0x7632);
+            if constexpr (S8) {
+              product((j * N + k) * 2, even_codes_bf16(x0), even_codes_bf16(x0 >> 8), even_codes_bf16(y0),
+                      even_codes_bf16(y0 >> 8));
+              product((j * N + k) * 2 + 1, even_codes_bf16(x1), even_codes_bf16(x1 >> 8), even_codes_bf16(y1),
+                      even_codes_bf16(y1 >> 8));
+            } else {
+              product(j * N + k, x0, x1, y0, y1);
+            }
+          }
+        }
+        __syncwarp();
+      }
+
+      // ---- the row, or this part of it ----
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float sum = l[nt][j];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int hh = nt * 8 + 2 * tig + j;
+          if (hh >= heads) continue;
+          if (whole) {
+            const int64_t h = (int64_t)b * a.q_heads + h0 + hh;
+            const bool none = sum == 0.0f;
+            const float z = none ? -INFINITY : m[nt][j] + log2f(sum);
+            if (g == 0) {
+              if (a.lse) a.lse[h] = z * kLn2;
+              if (a.stats) a.stats[h] = z;
+            }
+            QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)(h0 + hh) * a.out.head;
+            const float inv = none ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int mt = 0; mt < F::MT; ++mt) {
+              const int d = F::row_element(mt, g);
+              if (d < D) store_pair(out + d, o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv, a.aligned_out);
+            }
+          } else {
+            const int64_t p = ((int64_t)w * 2 + (starts ? 1 : 0)) * (8 * NT) + hh;
+            if (g == 0) a.part_stats[p] = make_float2(m[nt][j], sum);
+            float* out = a.part_out + p * F::DP;
+#pragma unroll
+            for (int mt = 0; mt < F::MT; ++mt)
+              *reinterpret_cast<float2*>(out + F::row_element(mt, g)) =
+                  make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
+          }
+        }
     }
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
+}
+
+// Rows that lie in several parts: one CTA per sequence and query head.
+template <class QT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  __shared__ float s_max[8], s_slice[16];
+  __shared__ float4 s_out[256];
+  const Cache& c = a.c;
+  const int b = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads;
+  const int gi = h % a.group, row = h / a.group * a.chunks + gi / a.heads_per_row, hh = gi % a.heads_per_row;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  next_kernel_may_start();
+  wait_previous_kernel();
+  const int R = c.heads * a.chunks;
+  const int64_t n = a.line[a.tab.sequences], at = a.line[b], cost = (a.line[b + 1] - at) / R;
+  const int parts = part_count(a, n, (int64_t)a.tab.sequences * R);
+  const int64_t row_at = at + row * cost;
+  const int w0 = part_of(n, parts, row_at), count = part_of(n, parts, row_at + cost - 1) - w0 + 1;
+  if (count == 1) return;
+  // part k: the tail of warp w0's range, then the heads of the next warps'
+  auto part = [&](int k) { return ((int64_t)(w0 + k) * 2 + (k == 0)) * a.heads_per_row + hh; };
+  float top = -INFINITY;
+  for (int k = threadIdx.x; k < count; k += 256) top = fmaxf(top, a.part_stats[part(k)].x);
+  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+  if (lane == 0) s_max[warp] = top;
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f, o = 0.0f;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w]);
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, s_max[i]);
   const float ref = top == -INFINITY ? 0.0f : top;
-  for (int w = 0; w < 8; ++w) {
-    const float f = sm[w] == -INFINITY ? (sl[w] == sl[w] ? 0.0f : sl[w]) : expf(sm[w] - ref);
-    sum += sl[w] * f;
-    o += so[w][threadIdx.x] * f;
+  const int quads = a.dp / 4, slices = 256 / quads, e = threadIdx.x % quads, slice = threadIdx.x / quads;
+  float sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = slice; k < count; k += slices) {
+    const int64_t p = part(k);
+    const float2 st = a.part_stats[p];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_out + p * a.dp + 4 * e);
+    const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
+    sum = fmaf(st.y, f, sum);
+    acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
   }
-  if ((int)threadIdx.x < c.dim) {
-    T* out = static_cast<T*>(a.out.p) + b * a.out.token + h * a.out.head + threadIdx.x;
-    const float y = len > first ? o / sum : 0.0f;
-    if constexpr (std::is_same<T, float>::value) *out = y;
-    else *out = __float2bfloat16_rn(y);
+  s_out[threadIdx.x] = acc;
+  if (e == 0) s_slice[slice] = sum;
+  __syncthreads();
+  if ((int)threadIdx.x >= quads) return;
+  sum = 0.0f;
+  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < slices; ++i) {
+    const float4 v = s_out[i * quads + e];
+    sum += s_slice[i];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
   }
+  const bool none = sum == 0.0f;
   if (threadIdx.x == 0) {
-    const float z = len > first ? ref + logf(sum) : -INFINITY;
-    if (a.lse) a.lse[blockIdx.x] = z;
+    const float z = none ? -INFINITY : top + log2f(sum);
+    if (a.lse) a.lse[blockIdx.x] = z * kLn2;
     if (a.stats) a.stats[blockIdx.x] = z;
+  }
+  if (4 * e < c.dim) {
+    QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)h * a.out.head + 4 * e;
+    const float inv = none ? 0.0f : 1.0f / sum;
+    store_pair(out, acc.x * inv, acc.y * inv, a.aligned_out);
+    store_pair(out + 2, acc.z * inv, acc.w * inv, a.aligned_out);
   }
 }
 
 // score of each token += its weights, summed over the query heads that share
-// its key/value head
-__global__ void __launch_bounds__(256) score_kernel(Args a) {
+// its key/value head.  The line again, with one row per key/value head.
+__global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
   const Cache& c = a.c;
-  const int b = blockIdx.x / c.heads, kvh = blockIdx.x % c.heads, group = a.q_heads / c.heads;
-  const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
-  const int first = a.window && len > a.window ? len - a.window : 0;
-  const int64_t most = (int64_t)a.tab.max_pages * c.page_size;
-  for (int t = first + threadIdx.x; t < len; t += 256) {
-    int page, off;
-    if (!kv::find(c, a.tab, b, t, page, off, a.status)) continue;
-    float p = 0.0f;
-    for (int g = 0; g < group; ++g) {
-      const int64_t r = (int64_t)b * a.q_heads + kvh * group + g;
-      p += expf(a.logits[r * most + t] - a.stats[r]);
+  const int lane = threadIdx.x & 31, B = a.tab.sequences;
+  const int warps = gridDim.x * 8, w = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  wait_previous_kernel();
+  const int64_t n = a.line[B] / a.chunks;
+  int64_t x = part_begin(n, warps, w);
+  const int64_t x_end = part_begin(n, warps, w + 1);
+  if (x >= x_end) return;
+  int b = 0;
+  for (int lo = 0, hi = B; lo < hi;) {
+    const int mid = (lo + hi) / 2;
+    if (a.line[mid] / a.chunks <= x) b = mid, lo = mid + 1;
+    else hi = mid;
+  }
+  for (; x < x_end; ++b) {
+    const int64_t at = a.line[b] / a.chunks, b_end = min(a.line[b + 1] / a.chunks, x_end);
+    const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
+    const int first = first_token(a, len), tile0 = first / 16, cost = tile_count(a, len) + kRowCost;
+    while (x < b_end) {
+      const int kvh = (int)((x - at) / cost);
+      const int64_t row_at = at + (int64_t)kvh * cost, seg_end = min(row_at + cost, x_end);
+      const int begin = max((int)(x - row_at) - kRowCost, 0), end = max((int)(seg_end - row_at) - kRowCost, 0);
+      x = seg_end;
+      const int64_t h0 = (int64_t)b * a.q_heads + kvh * a.group;
+      for (int t = max((tile0 + begin) * 16, first) + lane; t < min((tile0 + end) * 16, len); t += 32) {
+        int page, off;
+        if (!kv::find(c, a.tab, b, t, page, off, a.status)) continue;
+        float p = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < a.group; ++i) {
+          const float z = a.stats[h0 + i], s = a.logits[(h0 + i) * a.logit_pitch + t];
+          p += z == -INFINITY ? 0.0f : ex2_approx(s - z);
+        }
+        c.score[kv::scale_at(c, page, kvh, off)] += p;
+      }
     }
-    c.score[kv::scale_at(c, page, kvh, off)] += p;
   }
 }
 
-size_t workspace_bytes(const Cache& c, const Table& tab, int64_t q_heads, int accumulate) {
-  if (!accumulate) return 256;
-  const int64_t rows = (int64_t)tab.sequences * q_heads;
-  return (size_t)round_up(rows * 4, 256) + (size_t)rows * tab.max_pages * c.page_size * 4;
+int width_of(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+int groups_of(int group) { return group <= 8 ? 1 : 2; }
+int most_warps(bool s8, int dp, int nt) { return s8 && dp <= 128 && nt == 1 ? 16 : 8; }
+
+struct Layout {
+  int64_t line, part_stats, part_out, stats, logits, bytes, pitch;
+  int heads_per_row, dp;
+};
+
+Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int accumulate) {
+  Layout l{};
+  const int nt = groups_of((int)(q_heads / c.heads));
+  l.dp = width_of(c.dim);
+  l.heads_per_row = 8 * nt;
+  const int64_t B = std::min(tab.sequences, kMaxSequences);
+  const int64_t slots = (int64_t)sm_count() * most_warps(s8, l.dp, nt) * 2 * l.heads_per_row;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t p = at;
+    at += round_up(bytes, 256);
+    return p;
+  };
+  l.line = take((B + 1) * 8);
+  l.part_stats = take(slots * 8);
+  l.part_out = take(slots * l.dp * 4);
+  l.pitch = round_up((int64_t)tab.max_pages * c.page_size, 16);
+  if (accumulate) {
+    l.stats = take(B * q_heads * 4);
+    l.logits = take(B * q_heads * l.pitch * 4);
+  }
+  l.bytes = at;
+  return l;
+}
+
+template <class F>
+int launch_attend(Args& a, cudaStream_t s) {
+  a.parts = sm_count() * F::W;
+  const int rc = smem_attr((const void*)attend_kernel<F>, F::SMEM);
+  if (rc != I8Q_OK) return rc;
+  I8Q_PROF("paged_attention", s);
+  attend_kernel<F><<<(unsigned)sm_count(), F::W * 32, F::SMEM, s>>>(a);
+  I8Q_LAUNCH_CHECK("paged_attention");
+  return I8Q_OK;
+}
+
+template <class QT, bool S8, int DP>
+int launch_groups(Args& a, cudaStream_t s) {
+  return a.heads_per_row == 8 ? launch_attend<Form<QT, S8, DP, 1>>(a, s) : launch_attend<Form<QT, S8, DP, 2>>(a, s);
+}
+
+template <class QT, bool S8>
+int launch_width(Args& a, cudaStream_t s) {
+  return a.dp == 64 ? launch_groups<QT, S8, 64>(a, s)
+                    : a.dp == 128 ? launch_groups<QT, S8, 128>(a, s) : launch_groups<QT, S8, 256>(a, s);
+}
+
+// A launch that may begin while the kernel before it ends (it waits for that
+// one's results itself).
+template <class... P, class... V>
+int launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t s, const char* what, V... v) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.stream = s;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, v...);
+  return e == cudaSuccess ? I8Q_OK : cuda_fail(e, what);
 }
 
 }  // namespace
@@ -148,7 +880,7 @@ extern "C" size_t i8q_paged_attention_workspace_size(const i8q_kv_cache* cache, 
     fail(I8Q_ERR_INVALID_ARG, "paged_attention_workspace_size: q_heads must be a multiple of kv_heads, in range");
     return 0;
   }
-  return workspace_bytes(c, tab, q_heads, accumulate);
+  return (size_t)layout_of(c, tab, cache->type == I8Q_S8, q_heads, accumulate).bytes;
 }
 
 extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* lengths,
@@ -171,40 +903,52 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   if (!(softmax_scale == softmax_scale)) return fail(I8Q_ERR_INVALID_ARG, "paged_attention: softmax_scale is NaN");
   if (accumulate && !a.c.score)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: accumulate needs a cache that keeps scores");
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
-      ws_bytes < workspace_bytes(a.c, a.tab, q_heads, accumulate))
+  const bool s8 = cache->type == I8Q_S8;
+  const Layout l = layout_of(a.c, a.tab, s8, q_heads, accumulate);
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < (size_t)l.bytes)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: workspace is NULL, unaligned or too small");
-  a.lengths = lengths;
-  a.q = Heads{const_cast<void*>(q), q_token_stride, q_head_stride};
-  a.out = Heads{out, out_token_stride, out_head_stride};
-  a.lse = lse;
   a.scale = softmax_scale;
   a.q_heads = (int)q_heads;
+  a.group = a.q_heads / a.c.heads;
   a.window = (int)std::min<int64_t>(window, INT32_MAX);
-  a.accumulate = accumulate != 0;
+  a.dp = l.dp, a.heads_per_row = l.heads_per_row;
+  a.chunks = (int)ceil_div(a.group, a.heads_per_row);
+  char* ws = static_cast<char*>(workspace);
+  a.line = reinterpret_cast<int64_t*>(ws + l.line);
+  a.part_stats = reinterpret_cast<float2*>(ws + l.part_stats);
+  a.part_out = reinterpret_cast<float*>(ws + l.part_out);
   if (accumulate) {
-    a.stats = static_cast<float*>(workspace);
-    a.logits = a.stats + round_up((int64_t)a.tab.sequences * q_heads * 4, 256) / 4;
+    a.stats = reinterpret_cast<float*>(ws + l.stats);
+    a.logits = reinterpret_cast<float*>(ws + l.logits);
+    a.logit_pitch = l.pitch;
   }
+  const int64_t es = type == I8Q_F32 ? 4 : 2;
+  a.aligned_q = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_token_stride * es % 16 == 0 && q_head_stride * es % 16 == 0;
+  a.aligned_out = reinterpret_cast<uintptr_t>(out) % (2 * es) == 0 && out_token_stride % 2 == 0 && out_head_stride % 2 == 0;
   a.status = device_status_word();
   if (!a.status) return fail(I8Q_ERR_CUDA, "paged_attention: no status word");
   cudaStream_t s = as_stream(stream);
-  const unsigned blocks = (unsigned)(a.tab.sequences * q_heads);
-  {
-    I8Q_PROF("paged_attention", s);
-    if (type == I8Q_F32) {
-      if (cache->type == I8Q_S8) attend_kernel<float, true><<<blocks, 256, 0, s>>>(a);
-      else attend_kernel<float, false><<<blocks, 256, 0, s>>>(a);
-    } else {
-      if (cache->type == I8Q_S8) attend_kernel<__nv_bfloat16, true><<<blocks, 256, 0, s>>>(a);
-      else attend_kernel<__nv_bfloat16, false><<<blocks, 256, 0, s>>>(a);
+  const Table all = a.tab;
+  for (int b0 = 0; b0 < all.sequences; b0 += kMaxSequences) {
+    a.tab = Table{all.page + b0 * all.stride, all.stride, std::min(kMaxSequences, all.sequences - b0), all.max_pages};
+    a.lengths = lengths + b0;
+    a.q = Heads{const_cast<char*>(static_cast<const char*>(q)) + b0 * q_token_stride * es, q_token_stride, q_head_stride};
+    a.out = Heads{static_cast<char*>(out) + b0 * out_token_stride * es, out_token_stride, out_head_stride};
+    a.lse = lse ? lse + b0 * q_heads : nullptr;
+    if (type == I8Q_F32) rc = s8 ? launch_width<float, true>(a, s) : launch_width<float, false>(a, s);
+    else rc = s8 ? launch_width<__nv_bfloat16, true>(a, s) : launch_width<__nv_bfloat16, false>(a, s);
+    if (rc != I8Q_OK) return rc;
+    {
+      I8Q_PROF("paged_attention_join", s);
+      rc = launch_after(type == I8Q_F32 ? join_kernel<float> : join_kernel<__nv_bfloat16>,
+                        (unsigned)(a.tab.sequences * a.q_heads), 256, s, "paged_attention_join", a);
+      if (rc != I8Q_OK) return rc;
     }
-    I8Q_LAUNCH_CHECK("paged_attention");
-  }
-  if (accumulate) {
-    I8Q_PROF("paged_attention_scores", s);
-    score_kernel<<<(unsigned)a.tab.sequences * (unsigned)a.c.heads, 256, 0, s>>>(a);
-    I8Q_LAUNCH_CHECK("paged_attention_scores");
+    if (accumulate) {
+      I8Q_PROF("paged_attention_scores", s);
+      rc = launch_after(score_kernel, (unsigned)sm_count() * 8, 256, s, "paged_attention_scores", a);
+      if (rc != I8Q_OK) return rc;
+    }
   }
   return I8Q_OK;
 }
