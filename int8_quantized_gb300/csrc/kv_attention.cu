@@ -16,15 +16,18 @@
 //    tcgen05 wants 128 rows of fp16 operands in shared memory: the codes would
 //    have to be converted and written back there, several times the traffic
 //    of the fragments, for a product that takes a tenth of the time;
-//  - a lane copies the 16-byte pieces that hold its own fragments (the
-//    order of the summation index is free, so both operands use the order in
-//    which a lane's piece lies in memory) into slots of shared memory that
-//    only it reads: an asynchronous copy into what amounts to more registers.
-//    There is no barrier in the loop, and a 16-token tile is 4 KB in flight;
-//  - int8 keys become fp16 by one LOP3 (the byte, sign flipped, as the low
-//    mantissa bits of 1024) and one subtraction per two codes; the query is
-//    scaled by a power of two to at most 2.  Values become bf16, by one LOP3
-//    more, because the weights that multiply them need its range;
+//  - each warp copies its tiles asynchronously into slots of shared memory of
+//    its own, so there is no barrier in the loop, and a 16-token tile is 4 KB
+//    in flight.  Eight lanes read 128 bytes in a row (reading rows in pieces
+//    of 32 bytes, as the fragments lie, held the kernel to 4.3 TB/s);
+//  - the order of the summation index is free, so both operands use the one
+//    in which 16-byte pieces hold a lane's fragments;
+//  - a byte with its sign bit flipped, code + 128, is a subnormal number of
+//    fp16 and of bf16 as it lies: one LOP3 makes two of them.  Keys enter so,
+//    and the sum starts at what the 128s add up to (fp32 queries subtract
+//    them exactly); the query is scaled by a power of two to at most 2.  A
+//    bf16 fma turns two values into exact codes; bf16 because the weights that
+//    multiply them need its range;
 //  - the running maximum moves only when a score exceeds it by 2^8: p stays
 //    below 2^8, and most tiles need no reduction over the lanes;
 //  - value scales multiply p (in fp32) before it is split into bf16 parts.
@@ -63,6 +66,7 @@ struct Args {
   Heads q, out;
   float* lse;
   float scale;
+  int64_t page_bytes, head_bytes, token_bytes, step_bytes;  // the pools' strides; of the rows that 32 lanes copy at once
   int q_heads, group, chunks;  // group: query heads of a key/value head; chunks: rows that share one
   int window;
   int aligned_q, aligned_out;  // 16-byte loads of q rows, paired stores of out rows
@@ -101,9 +105,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)_
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -119,11 +120,11 @@ template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (HALF)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -135,22 +136,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Codes in bytes 0 and 2 of w as two fp16: a byte with its
-// sign bit flipped is code + 128; under 0x64 it is the fp16 number 1024 +
-// (code + 128), from which 1152 is taken (exactly).
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) {
+// Two codes in bytes 0 and 2 of w.  A byte with its sign bit flipped is the
+// unsigned number u = code + 128.
+//  as fp16 numbers: under 0x64 u stands for 1024 + u, and 1152 is taken;
+__device__ __forceinline__ uint32_t codes_fp16(uint32_t w) {
   const uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u;
   uint32_t r;
   asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
   return r;
 }
-// The same as bf16, whose 8 bits hold a code too: its low 7 bits under 0x43
-// are the bf16 number 128 + (code mod 128), its sign bit there makes 128 or
-// 256, and the difference is the code.
-__device__ __forceinline__ uint32_t even_codes_bf16(uint32_t w) {
-  const uint32_t u = (w & 0x007f007fu) | 0x43004300u, z = (w & 0x00800080u) | 0x43004300u;
+//  as fp16 numbers u 2^-24: u alone, the mantissa of a subnormal;
+__device__ __forceinline__ uint32_t codes_raised(uint32_t w) { return (w & 0x00ff00ffu) ^ 0x00800080u; }
+//  as bf16 numbers code 2^-6: u alone is u 2^-133 there (7 bits of mantissa,
+//  the eighth the lowest of the exponent), times 2^127, minus 128 2^-6.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t u = (w & 0x00ff00ffu) ^ 0x00800080u;
   uint32_t r;
-  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(z));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
   return r;
 }
 
@@ -175,6 +177,11 @@ template <class T>
 __device__ __forceinline__ float as_float(T x) {
   if constexpr (std::is_same<T, float>::value) return x;
   else return __bfloat162float(x);
+}
+
+__device__ __forceinline__ float fp16_sum(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f.x + f.y;
 }
 
 // N consecutive elements of a q row, in fp32.
@@ -219,13 +226,19 @@ struct Form {
   // 16 bits, far below its own rounding, since one part's 2^-9 is not.
   static constexpr int NQ = WIDE ? (S8 ? 2 : 3) : 1;
   static constexpr int NP = WIDE ? 3 : 2;
+  // int8 keys as code + 128, the 128 taken from the sum: half the work of
+  // exact codes, for sums rounded at four times their size
+  static constexpr bool RAISED = S8 && !WIDE;
   static constexpr int ES = S8 ? 1 : 2;
   static constexpr int KS = DP / 16;           // steps of the first product
   static constexpr int MT = DP / 16;           // row blocks of the second
-  static constexpr int PK = DP * ES / 64;      // 16-byte pieces of a key row per lane
-  static constexpr int VB = S8 && DP == 64 ? 8 : 16;
-  static constexpr int PV = DP * ES / 8 / VB;  // pieces of a value row per lane
-  static constexpr int SLOT = 16 * DP * ES + 80;  // half a tile: pieces, 16 scales, the mask of its tokens
+  static constexpr int ROW = DP * ES;          // bytes of a token's keys
+  static constexpr int PK = ROW / 64;          // 16-byte pieces of a key row per lane
+  static constexpr int VB = ROW == 64 ? 8 : 16;
+  static constexpr int PV = ROW / 8 / VB;      // pieces of a value row per lane
+  static constexpr int CR = ROW / 16;          // pieces of a row
+  static constexpr int CT = ROW / 32;          // pieces of half a tile that a lane copies
+  static constexpr int SLOT = 16 * ROW + 80;  // half a tile: pieces, 16 scales, the mask of its tokens
   static constexpr int Q_WORDS = NQ * NT * KS * 2;
   static constexpr bool MANY = S8 && DP <= 128 && NT == 1;     // 16 warps of 128 registers, else 8 or 4 of 255
   static constexpr bool Q_REG = Q_WORDS <= (MANY ? 16 : 32);   // q fragments in registers
@@ -237,6 +250,15 @@ struct Form {
   static constexpr int WARP_BYTES = SLOTS * SLOT + Q_BYTES;
   static constexpr int SMEM = W * WARP_BYTES + (kMaxSequences + 1) * 8 + 512;
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  // Where piece p of token t lies in a slot.  Copies go by rows (8 lanes read
+  // 128 bytes in a row of memory; four lanes a row of 64), and the exclusive
+  // or spreads what 8 lanes read at once, be it 4 pieces of tokens t and t +
+  // 1 (keys) or 2 pieces of tokens t, t + 2, t + 4 and t + 6 (values), over
+  // all banks.
+  __device__ static int place(int t, int p) {
+    if constexpr (ROW == 64) return t / 2 * 128 + ((((t & 1) * 4 + p) ^ (t & 6)) * 16);
+    else return t * ROW + ((p ^ (t & 6) ^ ((t & 1) * 4)) * 16);
+  }
   // Head element that lane group g holds in row g of block mt (row g + 8: the next one).
   __device__ static int row_element(int mt, int g) {
     if constexpr (S8) return DP == 64 ? g * 8 + mt * 2 : mt / 8 * 128 + g * 16 + mt % 8 * 2;
@@ -304,7 +326,6 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   unsigned char* ring = smem + warp * F::WARP_BYTES;
   const uint32_t ring_u = smem_u32(ring);
   uint2* q_smem = reinterpret_cast<uint2*>(ring + F::SLOTS * F::SLOT) + lane;
-  int put = 0, use = 0;                            // byte offsets of slots
   const bool whole_pages = c.page_size % 16 == 0;  // a tile lies in one page
   const int per_page = c.page_size / 16;
   const int D = c.dim;
@@ -327,106 +348,111 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       x = seg_end;
 
       // ---- copies: a tile is located once, then its keys, then its values are sent for ----
-      int64_t at = 0, scale_at = 0;  // of the tile's first row (whole pages) or of row lane % 16; of row lane % 16
+      // Addresses are a lane's own: its piece of the key/value head's first
+      // rows, and the scale of token lane % 16.  A tile adds where its first
+      // row lies.
+      const int64_t head_at = kvh * a.head_bytes;
+      const int64_t lane_at = head_at + lane / F::CR * a.token_bytes + lane % F::CR * 16;
+      const char* const k_lane = static_cast<const char*>(c.k) + lane_at;
+      const char* const v_lane = static_cast<const char*>(c.v) + lane_at;
+      const int64_t s_lane = kvh * c.s_head + (lane & 15) * c.s_token;
+      int64_t at = 0, scale_at = 0;  // of the tile: bytes (-1: no such page), and elements of the scales
+      int64_t at32 = 0, scale_at32 = 0;  // of the 32 tiles from the last multiple of 32 on, one a lane
+      int page_next = 0, off_next = 0;   // of the 32 after those
       uint32_t mask = 0;             // tokens of the tile that take part
-      int pg = 0, pg_off = 0, pg_next = -1, off_next = 0;
-      auto look_up = [&](int i) {  // the page of tile i + lane
-        pg_next = -1, off_next = 0;
+      uint32_t odd_tiles = 0;        // bit j: of the tile sent for j tiles ago, not all of them do
+      auto look_up = [&](int i) {
         if (i + lane < end) {
           const int t = tile0 + i + lane, p = t / per_page;
           off_next = (t - p * per_page) * 16;
-          pg_next = pages[p];
+          page_next = pages[p];
         }
       };
       auto locate = [&](int i) {
-        const int r = lane & 15, t = (tile0 + i) * 16 + r;
-        bool ok = t >= first && t < len;
+        const int t0 = (tile0 + i) * 16;
+        mask = 0xffffu;
         if (whole_pages) {
           const int l = (i - begin) & 31;
           if (l == 0) {
-            pg = pg_next, pg_off = off_next;
+            const bool bad = (unsigned)page_next >= (unsigned)c.pages;
+            if (bad) kv::report_index(a.status);
+            at32 = bad ? -1 : page_next * a.page_bytes + off_next * a.token_bytes;
+            scale_at32 = page_next * c.s_page + off_next * c.s_token;
             look_up(i + 32);
           }
-          const int page = __shfl_sync(0xffffffffu, pg, l), off = __shfl_sync(0xffffffffu, pg_off, l);
-          if ((unsigned)page >= (unsigned)c.pages) {
-            ok = false;
-            if (lane == 0) kv::report_index(a.status);
-          }
-          at = kv::row_at(c, page, kvh, off);
-          scale_at = kv::scale_at(c, page, kvh, off + r);
-        } else {
+          at = __shfl_sync(0xffffffffu, at32, l);
+          if constexpr (S8) scale_at = __shfl_sync(0xffffffffu, scale_at32, l) + s_lane;
+          if (t0 < first) mask = 0xffffu << (first - t0) & 0xffffu;
+          if (len - t0 < 16) mask &= 0xffffu >> (16 - (len - t0));
+          if (at < 0) mask = 0;
+        } else {  // at and scale_at: of token lane % 16
+          const int t = t0 + (lane & 15);
           int page = 0, off = 0;
+          bool ok = t >= first && t < len;
           if (ok) ok = kv::find(c, a.tab, b, t, page, off, a.status);
-          at = kv::row_at(c, page, kvh, off);
-          scale_at = kv::scale_at(c, page, kvh, off);
-        }
-        mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      };
-      auto row_of = [&](int r) {  // element offset of token r of the tile
-        return whole_pages ? at + r * c.token_stride : __shfl_sync(0xffffffffu, at, r);
-      };
-      auto send_scales = [&](uint32_t dst, const float* scale) {
-        if (lane < 16) {
-          const bool ok = mask >> lane & 1;
-          copy4(dst + 16 * F::DP * F::ES + lane * 4, ok ? scale + scale_at : scale, ok ? 4 : 0);
+          at = page * a.page_bytes + off * a.token_bytes;
+          scale_at = page * c.s_page + off * c.s_token + kvh * c.s_head;
+          mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
         }
       };
-      auto send_keys = [&](int i) {
+      // every token there, in one page, and every piece inside the row
+      auto plain = [&]() { return whole_pages && mask == 0xffffu && D == F::DP; };
+      auto send = [&](int put, const char* from, const void* pool, const float* scale) {
+        const uint32_t dst = ring_u + put;
+        if (plain()) {
+          const char* src = from + at;
+#pragma unroll
+          for (int r = 0; r < F::CT; ++r, src += a.step_bytes)
+            copy16(dst + F::place(r * 32 / F::CR + lane / F::CR, lane % F::CR), src, 16);
+          if constexpr (S8)
+            if (lane < 16) copy4(dst + 16 * F::ROW + lane * 4, scale + scale_at, 4);
+        } else {  // some pieces are zeros
+#pragma unroll 1
+          for (int r = 0; r < F::CT; ++r) {
+            const int t = (r * 32 + lane) / F::CR, p = lane % F::CR;
+            const int64_t row = whole_pages ? at + t * a.token_bytes : __shfl_sync(0xffffffffu, at, t);
+            const bool ok = (mask >> t & 1) && p * 16 < D * F::ES;
+            copy16(dst + F::place(t, p), static_cast<const char*>(pool) + (ok ? head_at + row + p * 16 : 0), ok ? 16 : 0);
+          }
+          if constexpr (S8)
+            if (lane < 16) {
+              const bool ok = mask >> lane & 1;
+              copy4(dst + 16 * F::ROW + lane * 4, ok ? scale + scale_at : scale, ok ? 4 : 0);
+            }
+          if (lane == 0) *reinterpret_cast<uint32_t*>(ring + put + 16 * F::ROW + 64) = mask;
+        }
+      };
+      auto send_keys = [&](int i, int put) {
+        odd_tiles <<= 1;
         if (i < end) {
           locate(i);
-          const uint32_t dst = ring_u + put;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int64_t src = row_of(g + 8 * r);
-            const bool ok = mask >> (g + 8 * r) & 1;
-#pragma unroll
-            for (int j = 0; j < F::PK; ++j) {
-              const int d = S8 ? j * 64 + tig * 16 : j * 32 + tig * 8;
-              const bool in_row = ok && d < D;
-              copy16(dst + ((r * F::PK + j) * 32 + lane) * 16,
-                     static_cast<const char*>(c.k) + (in_row ? (src + d) * F::ES : 0), in_row ? 16 : 0);
-            }
-          }
-          if constexpr (S8) send_scales(dst, c.ks);
-          if (lane == 0) *reinterpret_cast<uint32_t*>(ring + put + 16 * F::DP * F::ES + 64) = mask;
+          odd_tiles |= mask != 0xffffu;
+          send(put, k_lane, c.k, c.ks);
         }
         copy_commit();
-        put = put + F::SLOT == F::SLOTS * F::SLOT ? 0 : put + F::SLOT;
       };
-      auto send_values = [&](int i) {  // of the tile located last
-        if (i < end) {
-          const uint32_t dst = ring_u + put;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int t = 2 * tig + (r & 1) + (r & 2) * 4;
-            const int64_t src = row_of(t);
-            const bool ok = mask >> t & 1;
-#pragma unroll
-            for (int j = 0; j < F::PV; ++j) {
-              const int d = S8 ? j * 128 + g * F::VB : j * 64 + g * 8;
-              const bool in_row = ok && d < D;
-              const char* p = static_cast<const char*>(c.v) + (in_row ? (src + d) * F::ES : 0);
-              const uint32_t to = dst + ((r * F::PV + j) * 32 + lane) * F::VB;
-              if constexpr (F::VB == 16) copy16(to, p, in_row ? 16 : 0);
-              else copy8(to, p, in_row ? 8 : 0);
-            }
-          }
-          if constexpr (S8) send_scales(dst, c.vs);
-        }
+      auto send_values = [&](int i, int put) {  // of the tile located last
+        if (i < end) send(put, v_lane, c.v, c.vs);
         copy_commit();
-        put = put + F::SLOT == F::SLOTS * F::SLOT ? 0 : put + F::SLOT;
       };
-      use = put;  // the last row's copies have all been used
+      // The copy for AHEAD tiles on goes where the half used last lay.
+      int use = 0, free_slot = (F::SLOTS - 1) * F::SLOT;
+      auto advance = [&]() {
+        free_slot = use;
+        use = use == (F::SLOTS - 1) * F::SLOT ? 0 : use + F::SLOT;
+      };
+      __syncwarp();
       if (whole_pages) look_up(begin);
 #pragma unroll
       for (int i = 0; i < F::AHEAD; ++i) {
-        send_keys(begin + i);
-        send_values(begin + i);
+        send_keys(begin + i, 2 * i * F::SLOT);
+        send_values(begin + i, (2 * i + 1) * F::SLOT);
       }
 
       // ---- the query heads, as the columns of the first product ----
       uint2 q_reg[F::Q_REG ? F::NQ * NT * F::KS : 1];
       float factor[NT][2];  // of the scores of heads 2 tig and 2 tig + 1
+      float base[NT][2];    // where their sums start: what the codes' 128 add up to, subtracted
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         constexpr int N = S8 ? 16 : 8;  // elements of a piece
@@ -462,8 +488,10 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < N; ++i) v[j][i] *= down;
         }
+        if constexpr (F::RAISED) f *= 0x1p24f;
         factor[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
         factor[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+        float total = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < F::KS; ++ks) {
           const float* e = S8 ? &v[ks / 4][ks % 4 * 4] : &v[ks / 2][ks % 2 * 4];
@@ -471,6 +499,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           // int8 codes come as (0, 2) and (1, 3) of a word
           split2<S8, F::NQ>(e[0], S8 ? e[2] : e[1], r0);
           split2<S8, F::NQ>(S8 ? e[1] : e[2], e[3], r1);
+          if constexpr (F::RAISED) total += fp16_sum(r0[0]) + fp16_sum(r1[0]);
 #pragma unroll
           for (int i = 0; i < F::NQ; ++i) {
             const int at_q = (i * NT + nt) * F::KS + ks;
@@ -478,10 +507,17 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             else q_smem[at_q * 32] = make_uint2(r0[i], r1[i]);
           }
         }
+        if constexpr (F::RAISED) {
+          total += __shfl_xor_sync(0xffffffffu, total, 1);
+          total += __shfl_xor_sync(0xffffffffu, total, 2);
+          total *= -0x1p-17f;  // -128 2^-24
+        }
+        base[nt][0] = __shfl_sync(0xffffffffu, total, 8 * tig);
+        base[nt][1] = __shfl_sync(0xffffffffu, total, 8 * tig + 4);
       }
 
       // ---- the tiles ----
-      float o[F::MT][NT][4], m[NT][2], ref[NT][2], l[NT][2];
+      float o[F::MT][NT][4], m[NT][2], ref[NT][2], l[NT][2];  // ref: m, or 0 while m is -infinity
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -490,12 +526,14 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         ref[nt][0] = ref[nt][1] = 0.0f;
         l[nt][0] = l[nt][1] = 0.0f;
       }
+      bool unset = true;  // some m is -infinity
+#pragma unroll 1
       for (int i = begin; i < end; ++i) {
-        send_keys(i + F::AHEAD);
+        send_keys(i + F::AHEAD, free_slot);
         copy_wait<2 * F::AHEAD>();
         __syncwarp();
         const unsigned char* slot = ring + use;
-        use = use + F::SLOT == F::SLOTS * F::SLOT ? 0 : use + F::SLOT;
+        advance();
         // bf16 keys may be infinite, and infinity times a later part of q (0, or
         // of the other sign) is NaN: the first part's sum is kept apart
         constexpr bool APART = !S8 && F::NQ > 1;
@@ -503,19 +541,22 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = rest[nt][j] = 0.0f;
+          for (int j = 0; j < 4; ++j) s[nt][j] = F::RAISED ? base[nt][j & 1] : 0.0f, rest[nt][j] = 0.0f;
 #pragma unroll
         for (int j = 0; j < F::PK; ++j) {
-          const uint4 r0 = *reinterpret_cast<const uint4*>(slot + (j * 32 + lane) * 16);
-          const uint4 r1 = *reinterpret_cast<const uint4*>(slot + ((F::PK + j) * 32 + lane) * 16);
+          const uint4 r0 = *reinterpret_cast<const uint4*>(slot + F::place(g, j * 4 + tig));
+          const uint4 r1 = *reinterpret_cast<const uint4*>(slot + F::place(g + 8, j * 4 + tig));
           const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
           for (int k = 0; k < (S8 ? 4 : 2); ++k) {
             const int ks = j * (S8 ? 4 : 2) + k;
             uint32_t a0, a1, a2, a3;
-            if constexpr (S8) {
-              a0 = even_codes(w0[k]), a2 = even_codes(w0[k] >> 8);
-              a1 = even_codes(w1[k]), a3 = even_codes(w1[k] >> 8);
+            if constexpr (F::RAISED) {
+              a0 = codes_raised(w0[k]), a2 = codes_raised(w0[k] >> 8);
+              a1 = codes_raised(w1[k]), a3 = codes_raised(w1[k] >> 8);
+            } else if constexpr (S8) {
+              a0 = codes_fp16(w0[k]), a2 = codes_fp16(w0[k] >> 8);
+              a1 = codes_fp16(w1[k]), a3 = codes_fp16(w1[k] >> 8);
             } else {
               a0 = w0[2 * k], a2 = w0[2 * k + 1];
               a1 = w1[2 * k], a3 = w1[2 * k + 1];
@@ -539,20 +580,21 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             for (int j = 0; j < 4; ++j)
               if (fabsf(rest[nt][j]) < INFINITY) s[nt][j] += rest[nt][j];
         }
-        const float* scales = reinterpret_cast<const float*>(slot + 16 * F::DP * F::ES);
-        const uint32_t taken = reinterpret_cast<const uint32_t*>(scales)[16];
-        const bool in0 = taken >> g & 1, in1 = taken >> (g + 8) & 1;
+        const float* scales = reinterpret_cast<const float*>(slot + 16 * F::ROW);
         float k0 = 1.0f, k1 = 1.0f;
         if constexpr (S8) k0 = scales[g], k1 = scales[g + 8];
-        bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            s[nt][j] = in0 ? s[nt][j] * k0 * factor[nt][j] : -INFINITY;
-            s[nt][2 + j] = in1 ? s[nt][2 + j] * k1 * factor[nt][j] : -INFINITY;
-            rise |= fmaxf(s[nt][j], s[nt][2 + j]) > m[nt][j] + 8.0f;
-          }
+          for (int j = 0; j < 4; ++j) s[nt][j] = s[nt][j] * (j < 2 ? k0 : k1) * factor[nt][j & 1];
+        if (odd_tiles >> F::AHEAD & 1) {
+          const uint32_t taken = reinterpret_cast<const uint32_t*>(scales)[16];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!(taken >> (g + (j & 2) * 4) & 1)) s[nt][j] = -INFINITY;
+        }
         if (a.logits) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -564,23 +606,32 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
                 to[0] = s[nt][j], to[8] = s[nt][2 + j];
               }
         }
+        // a new reference where an exponent exceeds 8
+        bool rise = unset;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) rise |= fmaxf(s[nt][j], s[nt][2 + j]) > ref[nt][j] + 8.0f;
         if (__any_sync(0xffffffffu, rise)) {
+          unset = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(m[nt][j], fmaxf(s[nt][j], s[nt][2 + j]));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              float most = fmaxf(m[nt][j], fmaxf(s[nt][j], s[nt][2 + j]));
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
               // no score above -infinity so far: nothing to keep, and s - 0 = -infinity
-              const float next = top == -INFINITY ? 0.0f : top;
+              const float next = most == -INFINITY ? 0.0f : most;
               const float keep = m[nt][j] == -INFINITY ? 0.0f : ex2_approx(m[nt][j] - next);
-              m[nt][j] = top, ref[nt][j] = next;
+              unset |= most == -INFINITY;
+              m[nt][j] = most, ref[nt][j] = next;
               l[nt][j] *= keep;
 #pragma unroll
               for (int mt = 0; mt < F::MT; ++mt) o[mt][nt][j] *= keep, o[mt][nt][2 + j] *= keep;
             }
+          unset = __any_sync(0xffffffffu, unset);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -591,14 +642,14 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             l[nt][j] += s[nt][j] + s[nt][2 + j];
           }
 
-        send_values(i + F::AHEAD);
+        send_values(i + F::AHEAD, free_slot);
         copy_wait<2 * F::AHEAD>();
         __syncwarp();
         slot = ring + use;
-        use = use + F::SLOT == F::SLOTS * F::SLOT ? 0 : use + F::SLOT;
+        advance();
         float f0 = 1.0f, f1 = 1.0f;
         if constexpr (S8) {
-          const float* vs = reinterpret_cast<const float*>(slot + 16 * F::DP * F::ES);
+          const float* vs = reinterpret_cast<const float*>(slot + 16 * F::ROW);
           f0 = vs[g], f1 = vs[g + 8];
         }
         uint32_t b0[NT][F::NP], b1[NT][F::NP];
@@ -621,12 +672,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           uint32_t v[4][N];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const unsigned char* p = slot + ((r * F::PV + j) * 32 + lane) * F::VB;
+            const int t = 2 * tig + (r & 1) + (r & 2) * 4;
             if constexpr (F::VB == 16) {
-              const uint4 u = *reinterpret_cast<const uint4*>(p);
+              const uint4 u = *reinterpret_cast<const uint4*>(slot + F::place(t, j * 8 + g));
               v[r][0] = u.x, v[r][1] = u.y, v[r][N - 2] = u.z, v[r][N - 1] = u.w;
             } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(p);
+              const uint2 u = *reinterpret_cast<const uint2*>(slot + F::place(t, g / 2) + g % 2 * 8);
               v[r][0] = u.x, v[r][1] = u.y;
             }
           }
@@ -636,10 +687,10 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             const uint32_t x0 = __byte_perm(v[0][k], v[1][k], 0x5410), x1 = __byte_perm(v[0][k], v[1][k], 0x7632);
             const uint32_t y0 = __byte_perm(v[2][k], v[3][k], 0x5410), y1 = __byte_perm(v[2][k], v[3][k], 0x7632);
             if constexpr (S8) {
-              product((j * N + k) * 2, even_codes_bf16(x0), even_codes_bf16(x0 >> 8), even_codes_bf16(y0),
-                      even_codes_bf16(y0 >> 8));
-              product((j * N + k) * 2 + 1, even_codes_bf16(x1), even_codes_bf16(x1 >> 8), even_codes_bf16(y1),
-                      even_codes_bf16(y1 >> 8));
+              product((j * N + k) * 2, codes_bf16(x0), codes_bf16(x0 >> 8), codes_bf16(y0),
+                      codes_bf16(y0 >> 8));
+              product((j * N + k) * 2 + 1, codes_bf16(x1), codes_bf16(x1 >> 8), codes_bf16(y1),
+                      codes_bf16(y1 >> 8));
             } else {
               product(j * N + k, x0, x1, y0, y1);
             }
@@ -649,6 +700,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       }
 
       // ---- the row, or this part of it ----
+      constexpr float unit = S8 ? 64.0f : 1.0f;  // of codes_bf16
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -668,7 +720,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
               if (a.stats) a.stats[h] = z;
             }
             QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)(h0 + hh) * a.out.head;
-            const float inv = none ? 0.0f : 1.0f / sum;
+            const float inv = none ? 0.0f : unit / sum;
 #pragma unroll
             for (int mt = 0; mt < F::MT; ++mt) {
               const int d = F::row_element(mt, g);
@@ -681,7 +733,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
             for (int mt = 0; mt < F::MT; ++mt)
               *reinterpret_cast<float2*>(out + F::row_element(mt, g)) =
-                  make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
+                  make_float2(o[mt][nt][j] * unit, o[mt][nt][2 + j] * unit);
           }
         }
     }
@@ -831,6 +883,7 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
 template <class F>
 int launch_attend(Args& a, cudaStream_t s) {
   a.parts = sm_count() * F::W;
+  a.step_bytes = a.token_bytes * 32 / F::CR;
   const int rc = smem_attr((const void*)attend_kernel<F>, F::SMEM);
   if (rc != I8Q_OK) return rc;
   I8Q_PROF("paged_attention", s);
@@ -907,6 +960,9 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   const Layout l = layout_of(a.c, a.tab, s8, q_heads, accumulate);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < (size_t)l.bytes)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: workspace is NULL, unaligned or too small");
+  const int64_t ces = s8 ? 1 : 2;
+  a.page_bytes = a.c.page_stride * ces, a.head_bytes = a.c.head_stride * ces;
+  a.token_bytes = a.c.token_stride * ces;
   a.scale = softmax_scale;
   a.q_heads = (int)q_heads;
   a.group = a.q_heads / a.c.heads;
