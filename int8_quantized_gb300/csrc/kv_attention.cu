@@ -35,9 +35,10 @@
 // Work split.  Each row (sequence, key/value head, group of query heads) is
 // as long as its number of tiles plus a constant for its start and end;
 // the rows form one line, cut into equal parts, one per warp.  A row that
-// lies in one part is finished by that warp; of the others each warp leaves
-// m, l and o in the workspace, and a second kernel joins them.  The split
-// follows from the lengths alone, so results repeat.
+// lies in one part is finished by that warp.  Of the others the warps of a
+// CTA join what they have in shared memory, leave m, l and o in the
+// workspace, and a second kernel joins those.  The split follows from the
+// lengths alone, so results repeat.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -56,7 +57,7 @@ struct Heads {  // [sequences][heads][dim], strides in elements
 
 constexpr int kMaxSequences = 2048;  // of one launch: their line positions lie in shared memory
 constexpr int kRowCost = 2;          // of a row's start and end, in tiles
-constexpr int kMinPart = 8;          // a part is not shorter (in tiles) unless there are that many rows
+constexpr int kMinPart = 8;          // a part is not shorter unless there are that many rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -72,10 +73,10 @@ struct Args {
   int aligned_q, aligned_out;  // 16-byte loads of q rows, paired stores of out rows
   int dp;                      // row pitch of the partial outputs
   int heads_per_row;           // of a partial: 8 or 16
-  int parts;                   // warps of the first kernel
-  int64_t* line;               // [sequences + 1] start of each sequence on the line
-  float2* part_stats;          // [parts][2][heads_per_row] (m, l)
-  float* part_out;             // [parts][2][heads_per_row][dp]
+  int ctas, warps;             // of the first kernel
+  int* line;                   // [sequences + 1] start of each sequence on the line
+  float2* part_stats;          // [ctas * warps][2][heads_per_row] (m, l)
+  float* part_out;             // [ctas * warps][2][heads_per_row][dp]
   float* logits;               // [sequences][q_heads][logit_pitch], or null
   int64_t logit_pitch;
   float* stats;                // [sequences][q_heads] m + log2 l (with logits)
@@ -88,17 +89,23 @@ __device__ __forceinline__ int first_token(const Args& a, int len) {
 __device__ __forceinline__ int tile_count(const Args& a, int len) {
   return len > 0 ? (len + 15) / 16 - first_token(a, len) / 16 : 0;
 }
-// Parts that a line of n units over `rows` rows is cut into.
-__device__ __forceinline__ int part_count(const Args& a, int64_t n, int64_t rows) {
-  const int64_t want = max(rows, (n + kMinPart - 1) / kMinPart);
-  return (int)min(want, (int64_t)a.parts);
-}
-__device__ __forceinline__ int64_t part_begin(int64_t n, int parts, int w) { return n * w / parts; }
-__device__ __forceinline__ int part_of(int64_t n, int parts, int64_t x) {
-  int w = (int)(x * parts / n);
-  while (part_begin(n, parts, w + 1) <= x) ++w;
-  while (part_begin(n, parts, w) > x) --w;
-  return w;
+// The line of n units cut into parts whose lengths differ by one at most,
+// the longer ones first; each CTA takes `per_cta` neighbours.
+struct Cut {
+  int parts, per_cta, q, longer;  // `longer` parts of q + 1 units, then parts of q
+  __device__ int begin(int w) const { return w * q + min(w, longer); }
+  __device__ int of(int x) const {
+    const int split = longer * (q + 1);
+    return x < split ? x / (q + 1) : longer + (x - split) / q;
+  }
+};
+__device__ __forceinline__ Cut cut_line(const Args& a, int n, int rows) {
+  Cut c;
+  c.parts = min(max(rows, (n + kMinPart - 1) / kMinPart), a.ctas * a.warps);
+  c.per_cta = (c.parts + a.ctas - 1) / a.ctas;
+  c.q = n / c.parts;
+  c.longer = n - c.q * c.parts;
+  return c;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -240,15 +247,17 @@ struct Form {
   static constexpr int CT = ROW / 32;          // pieces of half a tile that a lane copies
   static constexpr int SLOT = 16 * ROW + 80;  // half a tile: pieces, 16 scales, the mask of its tokens
   static constexpr int Q_WORDS = NQ * NT * KS * 2;
-  static constexpr bool MANY = S8 && DP <= 128 && NT == 1;     // 16 warps of 128 registers, else 8 or 4 of 255
-  static constexpr bool Q_REG = Q_WORDS <= (MANY ? 16 : 32);   // q fragments in registers
+  static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
-  static constexpr int W = MANY ? 16 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  // warps: 12 of 168 registers where they suffice, else 8 or 4 of 255 (at
+  // 128 registers 16 warps spent a fifth more instructions on addresses)
+  static constexpr int W = S8 && DP <= 128 && NT == 1 ? 12 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
   static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
   static constexpr int AHEAD = ROOM >= 7 ? 3 : ROOM >= 5 ? 2 : 1;  // tiles in flight
   static constexpr int SLOTS = 2 * AHEAD + 1;
   static constexpr int WARP_BYTES = SLOTS * SLOT + Q_BYTES;
-  static constexpr int SMEM = W * WARP_BYTES + (kMaxSequences + 1) * 8 + 512;
+  static constexpr int SMEM = W * WARP_BYTES + (kMaxSequences + 1) * 4 + 12 + W * (8 * NT * 8 + 16);
+  static_assert(8 * NT * DP * 4 <= WARP_BYTES, "a part's result lies in its ring");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // Where piece p of token t lies in a slot.  Copies go by rows (8 lanes read
   // 128 bytes in a row of memory; four lanes a row of 64), and the exclusive
@@ -272,8 +281,11 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   constexpr bool S8 = F::S8;
   constexpr int NT = F::NT;
   extern __shared__ __align__(16) unsigned char smem[];
-  int64_t* line = reinterpret_cast<int64_t*>(smem + F::W * F::WARP_BYTES);
-  int64_t* sums = line + kMaxSequences + 1;
+  int* line = reinterpret_cast<int*>(smem + F::W * F::WARP_BYTES);
+  float2* open_stats = reinterpret_cast<float2*>(line + kMaxSequences + 4);  // [W][8 NT], 16-byte aligned
+  int* open_row = reinterpret_cast<int*>(open_stats + F::W * 8 * NT);        // [W] row left open by a warp, or -1
+  int* open_head = open_row + F::W;                                          // [W] that warp began the row
+  int* sums = open_head + F::W;                                              // [W]
   const Cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
   const int B = a.tab.sequences, R = c.heads * a.chunks;
@@ -282,22 +294,22 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 
   // ---- the line: where each sequence starts ----
   {
-    int64_t run = 0;
+    int run = 0;
     for (int b0 = 0; b0 < B; b0 += F::W * 32) {
       const int b = b0 + threadIdx.x;
-      int64_t v = 0;
-      if (b < B) v = (int64_t)(tile_count(a, kv::cut_length(c, a.tab, a.lengths[b], a.status)) + kRowCost) * R;
-      int64_t x = v;
+      int v = 0;
+      if (b < B) v = (tile_count(a, kv::cut_length(c, a.tab, a.lengths[b], a.status)) + kRowCost) * R;
+      int x = v;
 #pragma unroll
       for (int i = 1; i < 32; i <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, x, i);
+        const int u = __shfl_up_sync(0xffffffffu, x, i);
         if (lane >= i) x += u;
       }
       if (lane == 31) sums[warp] = x;
       __syncthreads();
-      int64_t before = 0, all = 0;
+      int before = 0, all = 0;
       for (int w = 0; w < F::W; ++w) {
-        const int64_t u = sums[w];
+        const int u = sums[w];
         before += w < warp ? u : 0;
         all += u;
       }
@@ -306,16 +318,16 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       __syncthreads();
     }
     if (threadIdx.x == 0) line[B] = run;
+    if (lane == 0) open_row[warp] = -1;
     __syncthreads();
     if (blockIdx.x == 0)
       for (int b = threadIdx.x; b <= B; b += F::W * 32) a.line[b] = line[b];
   }
-  const int64_t n = line[B];
-  const int parts = part_count(a, n, (int64_t)B * R);
-  const int w = warp * gridDim.x + blockIdx.x;  // neighbouring parts on different SMs
-  if (w >= parts) return;
-  int64_t x = part_begin(n, parts, w);
-  const int64_t x_end = part_begin(n, parts, w + 1);
+  const Cut cut = cut_line(a, line[B], B * R);
+  const int w = blockIdx.x * cut.per_cta + warp;
+  const bool idle = warp >= cut.per_cta || w >= cut.parts;
+  int x = idle ? 0 : cut.begin(w);
+  const int x_end = idle ? 0 : cut.begin(w + 1);
   int b = 0;
   for (int lo = 0, hi = B; lo < hi;) {  // last b with line[b] <= x
     const int mid = (lo + hi) / 2;
@@ -331,18 +343,16 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   const int D = c.dim;
 
   for (; x < x_end; ++b) {
-    const int64_t b_end = min(line[b + 1], x_end);
+    const int b_end = min(line[b + 1], x_end);
     const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
     const int first = first_token(a, len), tile0 = first / 16;
     const int cost = tile_count(a, len) + kRowCost;
     const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
     while (x < b_end) {
-      const int row = (int)((x - line[b]) / cost);
-      const int64_t row_at = line[b] + (int64_t)row * cost;
-      const int in = (int)(x - row_at);
-      const int64_t seg_end = min(row_at + cost, x_end);
-      const int begin = max(in - kRowCost, 0), end = max((int)(seg_end - row_at) - kRowCost, 0);
-      const bool starts = in == 0, whole = starts && seg_end == row_at + cost;
+      const int row = (x - line[b]) / cost, row_at = line[b] + row * cost, in = x - row_at;
+      const int seg_end = min(row_at + cost, x_end);
+      const int begin = max(in - kRowCost, 0), end = max(seg_end - row_at - kRowCost, 0);
+      const bool starts = in == 0, ends = seg_end == row_at + cost;
       const int kvh = row / a.chunks, h0 = kvh * a.group + (row % a.chunks) * (8 * NT);
       const int heads = min(8 * NT, (kvh + 1) * a.group - h0);
       x = seg_end;
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
           const int hh = nt * 8 + 2 * tig + j;
           if (hh >= heads) continue;
-          if (whole) {
+          if (starts && ends) {
             const int64_t h = (int64_t)b * a.q_heads + h0 + hh;
             const bool none = sum == 0.0f;
             const float z = none ? -INFINITY : m[nt][j] + log2f(sum);
@@ -727,93 +737,133 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
               if (d < D) store_pair(out + d, o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv, a.aligned_out);
             }
           } else {
-            const int64_t p = ((int64_t)w * 2 + (starts ? 1 : 0)) * (8 * NT) + hh;
-            if (g == 0) a.part_stats[p] = make_float2(m[nt][j], sum);
-            float* out = a.part_out + p * F::DP;
+            // a part that ends a row goes to the workspace; one that leaves it open is
+            // this warp's last: into its ring, to be joined with its neighbours'
+            const int64_t p = (int64_t)w * 2 * (8 * NT) + hh;
+            if (g == 0) (ends ? a.part_stats[p] : open_stats[warp * 8 * NT + hh]) = make_float2(m[nt][j], sum);
+            float* out = ends ? a.part_out + p * F::DP : reinterpret_cast<float*>(ring) + hh * F::DP;
 #pragma unroll
             for (int mt = 0; mt < F::MT; ++mt)
               *reinterpret_cast<float2*>(out + F::row_element(mt, g)) =
                   make_float2(o[mt][nt][j] * unit, o[mt][nt][2 + j] * unit);
           }
         }
+      if (lane == 0 && !ends) open_row[warp] = b * R + row, open_head[warp] = starts;
+    }
+  }
+
+  // ---- rows left open: neighbours of one row are joined, in the order of the line ----
+  __syncthreads();
+  const int mine = open_row[warp];
+  if (mine < 0) return;
+  int from = warp, to = warp;
+  while (from > 0 && open_row[from - 1] == mine) --from;
+  while (to + 1 < F::W && open_row[to + 1] == mine) ++to;
+  const int heads = min(8 * NT, a.group - mine % R % a.chunks * (8 * NT));
+  for (int hh = warp - from; hh < heads; hh += to - from + 1) {
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = from; i <= to; ++i) top = fmaxf(top, open_stats[i * 8 * NT + hh].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float4 acc[(F::DP + 127) / 128];
+#pragma unroll
+    for (int e = 0; e < (F::DP + 127) / 128; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = from; i <= to; ++i) {
+      const float2 st = open_stats[i * 8 * NT + hh];
+      const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
+      sum = fmaf(st.y, f, sum);
+      const float* part = reinterpret_cast<const float*>(smem + i * F::WARP_BYTES) + hh * F::DP;
+#pragma unroll
+      for (int e = 0; e < (F::DP + 127) / 128; ++e)
+        if (e * 128 + lane * 4 < F::DP) {
+          const float4 v = *reinterpret_cast<const float4*>(part + e * 128 + lane * 4);
+          acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
+          acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
+        }
+    }
+    const int64_t p = ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh;
+    if (lane == 0) a.part_stats[p] = make_float2(top, sum);
+#pragma unroll
+    for (int e = 0; e < (F::DP + 127) / 128; ++e)
+      if (e * 128 + lane * 4 < F::DP)
+        *reinterpret_cast<float4*>(a.part_out + p * F::DP + e * 128 + lane * 4) = acc[e];
+  }
+}
+
+// Rows that lie in several parts: a warp per sequence and query head.
+template <class QT, int DP>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  constexpr int E = (DP + 127) / 128;
+  const Cache& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);
+  next_kernel_may_start();
+  wait_previous_kernel();
+  if (id >= a.tab.sequences * a.q_heads) return;
+  const int b = id / a.q_heads, h = id % a.q_heads;
+  const int gi = h % a.group, row = h / a.group * a.chunks + gi / a.heads_per_row, hh = gi % a.heads_per_row;
+  const int R = c.heads * a.chunks;
+  const int n = a.line[a.tab.sequences], at = a.line[b], cost = (a.line[b + 1] - at) / R;
+  const Cut cut = cut_line(a, n, a.tab.sequences * R);
+  const int row_at = at + row * cost, w0 = cut.of(row_at), w1 = cut.of(row_at + cost - 1);
+  if (w0 == w1) return;
+  // what CTA w0 / per_cta joined from w0 on, what the next ones joined, and part w1
+  const int cta0 = w0 / cut.per_cta, count = (w1 - 1) / cut.per_cta - cta0 + 2;
+  auto part = [&](int k) {
+    const int w = k == 0 ? w0 : k == count - 1 ? w1 : (cta0 + k) * cut.per_cta;
+    return ((int64_t)w * 2 + (k == 0)) * a.heads_per_row + hh;
+  };
+  float top = -INFINITY;
+  for (int k = lane; k < count; k += 32) top = fmaxf(top, a.part_stats[part(k)].x);
+  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  float4 acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < count; ++k) {
+    const int64_t p = part(k);
+    const float2 st = a.part_stats[p];
+    const float f = ex2_approx(st.x - ref);
+    sum = fmaf(st.y, f, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e * 128 + lane * 4 < DP) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part_out + p * DP + e * 128 + lane * 4);
+        acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
+        acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
+      }
+  }
+  const bool none = sum == 0.0f;
+  if (lane == 0) {
+    const float z = none ? -INFINITY : top + log2f(sum);
+    if (a.lse) a.lse[id] = z * kLn2;
+    if (a.stats) a.stats[id] = z;
+  }
+  const float inv = none ? 0.0f : 1.0f / sum;
+  QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)h * a.out.head;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = e * 128 + lane * 4;
+    if (d < c.dim) {
+      store_pair(out + d, acc[e].x * inv, acc[e].y * inv, a.aligned_out);
+      store_pair(out + d + 2, acc[e].z * inv, acc[e].w * inv, a.aligned_out);
     }
   }
 }
 
-// Rows that lie in several parts: one CTA per sequence and query head.
-template <class QT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
-  __shared__ float s_max[8], s_slice[16];
-  __shared__ float4 s_out[256];
-  const Cache& c = a.c;
-  const int b = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads;
-  const int gi = h % a.group, row = h / a.group * a.chunks + gi / a.heads_per_row, hh = gi % a.heads_per_row;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  next_kernel_may_start();
-  wait_previous_kernel();
-  const int R = c.heads * a.chunks;
-  const int64_t n = a.line[a.tab.sequences], at = a.line[b], cost = (a.line[b + 1] - at) / R;
-  const int parts = part_count(a, n, (int64_t)a.tab.sequences * R);
-  const int64_t row_at = at + row * cost;
-  const int w0 = part_of(n, parts, row_at), count = part_of(n, parts, row_at + cost - 1) - w0 + 1;
-  if (count == 1) return;
-  // part k: the tail of warp w0's range, then the heads of the next warps'
-  auto part = [&](int k) { return ((int64_t)(w0 + k) * 2 + (k == 0)) * a.heads_per_row + hh; };
-  float top = -INFINITY;
-  for (int k = threadIdx.x; k < count; k += 256) top = fmaxf(top, a.part_stats[part(k)].x);
-  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, s_max[i]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  const int quads = a.dp / 4, slices = 256 / quads, e = threadIdx.x % quads, slice = threadIdx.x / quads;
-  float sum = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = slice; k < count; k += slices) {
-    const int64_t p = part(k);
-    const float2 st = a.part_stats[p];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_out + p * a.dp + 4 * e);
-    const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
-    sum = fmaf(st.y, f, sum);
-    acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-  }
-  s_out[threadIdx.x] = acc;
-  if (e == 0) s_slice[slice] = sum;
-  __syncthreads();
-  if ((int)threadIdx.x >= quads) return;
-  sum = 0.0f;
-  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = 0; i < slices; ++i) {
-    const float4 v = s_out[i * quads + e];
-    sum += s_slice[i];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-  }
-  const bool none = sum == 0.0f;
-  if (threadIdx.x == 0) {
-    const float z = none ? -INFINITY : top + log2f(sum);
-    if (a.lse) a.lse[blockIdx.x] = z * kLn2;
-    if (a.stats) a.stats[blockIdx.x] = z;
-  }
-  if (4 * e < c.dim) {
-    QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)h * a.out.head + 4 * e;
-    const float inv = none ? 0.0f : 1.0f / sum;
-    store_pair(out, acc.x * inv, acc.y * inv, a.aligned_out);
-    store_pair(out + 2, acc.z * inv, acc.w * inv, a.aligned_out);
-  }
-}
-
 // score of each token += its weights, summed over the query heads that share
-// its key/value head.  The line again, with one row per key/value head.
+// its key/value head.  The line again, with one row per key/value head; a
+// lane takes V tokens at a time: 4 neighbours in one page, or 1.
+template <int V>
 __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
   const Cache& c = a.c;
   const int lane = threadIdx.x & 31, B = a.tab.sequences;
-  const int warps = gridDim.x * 8, w = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_previous_kernel();
-  const int64_t n = a.line[B] / a.chunks;
-  int64_t x = part_begin(n, warps, w);
-  const int64_t x_end = part_begin(n, warps, w + 1);
+  const int n = a.line[B] / a.chunks, q = n / warps, longer = n - q * warps;
+  int x = w * q + min(w, longer);
+  const int x_end = x + q + (w < longer);
   if (x >= x_end) return;
   int b = 0;
   for (int lo = 0, hi = B; lo < hi;) {
@@ -822,25 +872,46 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
     else hi = mid;
   }
   for (; x < x_end; ++b) {
-    const int64_t at = a.line[b] / a.chunks, b_end = min(a.line[b + 1] / a.chunks, x_end);
+    const int at = a.line[b] / a.chunks, b_end = min(a.line[b + 1] / a.chunks, x_end);
     const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
     const int first = first_token(a, len), tile0 = first / 16, cost = tile_count(a, len) + kRowCost;
     while (x < b_end) {
-      const int kvh = (int)((x - at) / cost);
-      const int64_t row_at = at + (int64_t)kvh * cost, seg_end = min(row_at + cost, x_end);
-      const int begin = max((int)(x - row_at) - kRowCost, 0), end = max((int)(seg_end - row_at) - kRowCost, 0);
+      const int kvh = (x - at) / cost, row_at = at + kvh * cost, seg_end = min(row_at + cost, x_end);
+      const int begin = max(x - row_at - kRowCost, 0), end = max(seg_end - row_at - kRowCost, 0);
       x = seg_end;
       const int64_t h0 = (int64_t)b * a.q_heads + kvh * a.group;
-      for (int t = max((tile0 + begin) * 16, first) + lane; t < min((tile0 + end) * 16, len); t += 32) {
+      const int t_end = min((tile0 + end) * 16, len);
+      for (int t = (tile0 + begin) * 16 + lane * V; t < t_end; t += 32 * V) {
+        if (t + V <= first) continue;
         int page, off;
         if (!kv::find(c, a.tab, b, t, page, off, a.status)) continue;
-        float p = 0.0f;
+        float* score = c.score + kv::scale_at(c, page, kvh, off);
+        const float* logit = a.logits + h0 * a.logit_pitch + t;
+        float p[V] = {};
+        // a logit outside the sequence or its window is -infinity: no weight
+        if constexpr (V == 4) {
+          float4 s = *reinterpret_cast<const float4*>(score);
 #pragma unroll 4
-        for (int i = 0; i < a.group; ++i) {
-          const float z = a.stats[h0 + i], s = a.logits[(h0 + i) * a.logit_pitch + t];
-          p += z == -INFINITY ? 0.0f : ex2_approx(s - z);
+          for (int i = 0; i < a.group; ++i) {
+            const float z = a.stats[h0 + i];
+            const float4 l = __ldcs(reinterpret_cast<const float4*>(logit + i * a.logit_pitch));
+            const float r = z == -INFINITY ? INFINITY : z;
+            p[0] += ex2_approx(l.x - r), p[1] += ex2_approx(l.y - r);
+            p[2] += ex2_approx(l.z - r), p[3] += ex2_approx(l.w - r);
+          }
+          if (t >= first) s.x += p[0];
+          if (t + 1 >= first && t + 1 < len) s.y += p[1];
+          if (t + 2 >= first && t + 2 < len) s.z += p[2];
+          if (t + 3 >= first && t + 3 < len) s.w += p[3];
+          *reinterpret_cast<float4*>(score) = s;
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < a.group; ++i) {
+            const float z = a.stats[h0 + i], l = logit[i * a.logit_pitch];
+            p[0] += ex2_approx(l - (z == -INFINITY ? INFINITY : z));
+          }
+          *score += p[0];
         }
-        c.score[kv::scale_at(c, page, kvh, off)] += p;
       }
     }
   }
@@ -848,7 +919,21 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
 
 int width_of(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 int groups_of(int group) { return group <= 8 ? 1 : 2; }
-int most_warps(bool s8, int dp, int nt) { return s8 && dp <= 128 && nt == 1 ? 16 : 8; }
+int most_warps(bool s8, int dp, int nt) { return s8 && dp <= 128 && nt == 1 ? 12 : 8; }
+
+// Most that one sequence takes of the line.
+int64_t line_length(const Cache& c, const Table& tab, int64_t q_heads) {
+  const int64_t group = q_heads / c.heads;
+  return (ceil_div((int64_t)tab.max_pages * c.page_size, 16) + kRowCost) * c.heads *
+         ceil_div(group, 8 * groups_of((int)group));
+}
+
+using Join = void (*)(Args);
+Join join_of(int type, int dp) {
+  if (type == I8Q_F32) return dp == 64 ? join_kernel<float, 64> : dp == 128 ? join_kernel<float, 128> : join_kernel<float, 256>;
+  return dp == 64 ? join_kernel<__nv_bfloat16, 64>
+                  : dp == 128 ? join_kernel<__nv_bfloat16, 128> : join_kernel<__nv_bfloat16, 256>;
+}
 
 struct Layout {
   int64_t line, part_stats, part_out, stats, logits, bytes, pitch;
@@ -868,7 +953,7 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
     at += round_up(bytes, 256);
     return p;
   };
-  l.line = take((B + 1) * 8);
+  l.line = take((B + 1) * 4);
   l.part_stats = take(slots * 8);
   l.part_out = take(slots * l.dp * 4);
   l.pitch = round_up((int64_t)tab.max_pages * c.page_size, 16);
@@ -882,7 +967,7 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
 
 template <class F>
 int launch_attend(Args& a, cudaStream_t s) {
-  a.parts = sm_count() * F::W;
+  a.ctas = sm_count(), a.warps = F::W;
   a.step_bytes = a.token_bytes * 32 / F::CR;
   const int rc = smem_attr((const void*)attend_kernel<F>, F::SMEM);
   if (rc != I8Q_OK) return rc;
@@ -957,6 +1042,10 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   if (accumulate && !a.c.score)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: accumulate needs a cache that keeps scores");
   const bool s8 = cache->type == I8Q_S8;
+  const int64_t longest = line_length(a.c, a.tab, q_heads);
+  if (longest > INT32_MAX)
+    return fail(I8Q_ERR_UNSUPPORTED, "paged_attention: max_pages * page_size * kv_heads out of range");
+  const int slice = (int)std::min<int64_t>(kMaxSequences, INT32_MAX / longest);
   const Layout l = layout_of(a.c, a.tab, s8, q_heads, accumulate);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < (size_t)l.bytes)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: workspace is NULL, unaligned or too small");
@@ -970,7 +1059,7 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   a.dp = l.dp, a.heads_per_row = l.heads_per_row;
   a.chunks = (int)ceil_div(a.group, a.heads_per_row);
   char* ws = static_cast<char*>(workspace);
-  a.line = reinterpret_cast<int64_t*>(ws + l.line);
+  a.line = reinterpret_cast<int*>(ws + l.line);
   a.part_stats = reinterpret_cast<float2*>(ws + l.part_stats);
   a.part_out = reinterpret_cast<float*>(ws + l.part_out);
   if (accumulate) {
@@ -985,8 +1074,10 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   if (!a.status) return fail(I8Q_ERR_CUDA, "paged_attention: no status word");
   cudaStream_t s = as_stream(stream);
   const Table all = a.tab;
-  for (int b0 = 0; b0 < all.sequences; b0 += kMaxSequences) {
-    a.tab = Table{all.page + b0 * all.stride, all.stride, std::min(kMaxSequences, all.sequences - b0), all.max_pages};
+  const bool four = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
+  for (int b0 = 0; b0 < all.sequences; b0 += slice) {
+    a.tab = Table{all.page + b0 * all.stride, all.stride, std::min(slice, all.sequences - b0), all.max_pages};
     a.lengths = lengths + b0;
     a.q = Heads{const_cast<char*>(static_cast<const char*>(q)) + b0 * q_token_stride * es, q_token_stride, q_head_stride};
     a.out = Heads{static_cast<char*>(out) + b0 * out_token_stride * es, out_token_stride, out_head_stride};
@@ -996,13 +1087,14 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     if (rc != I8Q_OK) return rc;
     {
       I8Q_PROF("paged_attention_join", s);
-      rc = launch_after(type == I8Q_F32 ? join_kernel<float> : join_kernel<__nv_bfloat16>,
-                        (unsigned)(a.tab.sequences * a.q_heads), 256, s, "paged_attention_join", a);
+      rc = launch_after(join_of(type, l.dp), (unsigned)ceil_div(a.tab.sequences * a.q_heads, 8), 256, s,
+                        "paged_attention_join", a);
       if (rc != I8Q_OK) return rc;
     }
     if (accumulate) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = launch_after(score_kernel, (unsigned)sm_count() * 8, 256, s, "paged_attention_scores", a);
+      rc = launch_after(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, s,
+                        "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }
   }
