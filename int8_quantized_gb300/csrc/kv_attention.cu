@@ -245,7 +245,7 @@ struct Form {
   static constexpr int PV = ROW / 8 / VB;      // pieces of a value row per lane
   static constexpr int CR = ROW / 16;          // pieces of a row
   static constexpr int CT = ROW / 32;          // pieces of half a tile that a lane copies
-  static constexpr int SLOT = 16 * ROW + 80;  // half a tile: pieces, 16 scales, the mask of its tokens
+  static constexpr int SLOT = 16 * ROW + 144;  // half a tile: pieces; keys: 32 scales, the mask of the tokens
   static constexpr int Q_WORDS = NQ * NT * KS * 2;
   static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
@@ -267,6 +267,11 @@ struct Form {
   __device__ static int place(int t, int p) {
     if constexpr (ROW == 64) return t / 2 * 128 + ((((t & 1) * 4 + p) ^ (t & 6)) * 16);
     else return t * ROW + ((p ^ (t & 6) ^ ((t & 1) * 4)) * 16);
+  }
+  // The same for the r-th piece that a lane copies, from place(lane / CR, lane % CR).
+  __device__ static constexpr int copy_place(int at, int r) {
+    const int t = r * 32 / CR;
+    return ROW == 64 ? at + r * 512 : (at ^ (((t & 6) ^ ((t & 1) * 4)) * 16)) + r * 512;
   }
   // Head element that lane group g holds in row g of block mt (row g + 8: the next one).
   __device__ static int row_element(int mt, int g) {
@@ -291,6 +296,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   const int B = a.tab.sequences, R = c.heads * a.chunks;
 
   next_kernel_may_start();
+  wait_previous_kernel();
 
   // ---- the line: where each sequence starts ----
   {
@@ -339,6 +345,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   const uint32_t ring_u = smem_u32(ring);
   uint2* q_smem = reinterpret_cast<uint2*>(ring + F::SLOTS * F::SLOT) + lane;
   const bool whole_pages = c.page_size % 16 == 0;  // a tile lies in one page
+  const bool packed = a.token_bytes == F::ROW;     // and is one run of memory
+  // places that do not change, kept in registers (the compiler would work them out again in every tile)
+  int copy_at = F::place(lane / F::CR, lane % F::CR), k_at = F::place(g, tig);
+  int v_at0 = F::VB == 16 ? F::place(2 * tig, g) : F::place(2 * tig, g / 2) + g % 2 * 8;
+  int v_at1 = F::VB == 16 ? F::place(2 * tig + 1, g) : F::place(2 * tig + 1, g / 2) + g % 2 * 8;
+  asm volatile("" : "+r"(copy_at), "+r"(k_at), "+r"(v_at0), "+r"(v_at1));
   const int per_page = c.page_size / 16;
   const int D = c.dim;
 
@@ -359,18 +371,21 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 
       // ---- copies: a tile is located once, then its keys, then its values are sent for ----
       // Addresses are a lane's own: its piece of the key/value head's first
-      // rows, and the scale of token lane % 16.  A tile adds where its first
-      // row lies.
+      // rows, and the scale of token lane % 16 (lanes from 16 on: of its value).
+      // A tile adds where its first row lies.
       const int64_t head_at = kvh * a.head_bytes;
       const int64_t lane_at = head_at + lane / F::CR * a.token_bytes + lane % F::CR * 16;
       const char* const k_lane = static_cast<const char*>(c.k) + lane_at;
       const char* const v_lane = static_cast<const char*>(c.v) + lane_at;
-      const int64_t s_lane = kvh * c.s_head + (lane & 15) * c.s_token;
-      int64_t at = 0, scale_at = 0;  // of the tile: bytes (-1: no such page), and elements of the scales
+      const float* const s_head = (lane < 16 ? c.ks : c.vs) + kvh * c.s_head;
+      const float* const s_lane = s_head + (lane & 15) * c.s_token;
+      int64_t at = 0, scale_at = 0;      // of the tile: bytes (-1: no such page), and elements of the scales
       int64_t at32 = 0, scale_at32 = 0;  // of the 32 tiles from the last multiple of 32 on, one a lane
       int page_next = 0, off_next = 0;   // of the 32 after those
-      uint32_t mask = 0;             // tokens of the tile that take part
-      uint32_t odd_tiles = 0;        // bit j: of the tile sent for j tiles ago, not all of them do
+      uint32_t mask = 0xffffu;           // tokens of the tile that take part
+      bool plain = false;                // all of them, every piece inside its row, in one page
+      uint32_t odd_tiles = 0;            // bit j: of the tile sent for j tiles ago, not all tokens take part
+      const int last = tile_count(a, len) - 1;
       auto look_up = [&](int i) {
         if (i + lane < end) {
           const int t = tile0 + i + lane, p = t / per_page;
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       };
       auto locate = [&](int i) {
         const int t0 = (tile0 + i) * 16;
-        mask = 0xffffu;
+        plain = false;
         if (whole_pages) {
           const int l = (i - begin) & 31;
           if (l == 0) {
@@ -391,31 +406,33 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             look_up(i + 32);
           }
           at = __shfl_sync(0xffffffffu, at32, l);
-          if constexpr (S8) scale_at = __shfl_sync(0xffffffffu, scale_at32, l) + s_lane;
-          if (t0 < first) mask = 0xffffu << (first - t0) & 0xffffu;
-          if (len - t0 < 16) mask &= 0xffffu >> (16 - (len - t0));
+          if constexpr (S8) scale_at = __shfl_sync(0xffffffffu, scale_at32, l);
+          mask = 0xffffu;
+          if (i == 0 && t0 < first) mask = 0xffffu << (first - t0) & 0xffffu;
+          if (i == last && len - t0 < 16) mask &= 0xffffu >> (16 - (len - t0));
           if (at < 0) mask = 0;
+          plain = mask == 0xffffu && D == F::DP;
         } else {  // at and scale_at: of token lane % 16
           const int t = t0 + (lane & 15);
           int page = 0, off = 0;
           bool ok = t >= first && t < len;
           if (ok) ok = kv::find(c, a.tab, b, t, page, off, a.status);
           at = page * a.page_bytes + off * a.token_bytes;
-          scale_at = page * c.s_page + off * c.s_token + kvh * c.s_head;
+          scale_at = page * c.s_page + off * c.s_token;
           mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
         }
       };
-      // every token there, in one page, and every piece inside the row
-      auto plain = [&]() { return whole_pages && mask == 0xffffu && D == F::DP; };
-      auto send = [&](int put, const char* from, const void* pool, const float* scale) {
+      auto send = [&](int put, const char* from, const void* pool) {
         const uint32_t dst = ring_u + put;
-        if (plain()) {
+        if (plain) {
           const char* src = from + at;
+          if (packed) {
 #pragma unroll
-          for (int r = 0; r < F::CT; ++r, src += a.step_bytes)
-            copy16(dst + F::place(r * 32 / F::CR + lane / F::CR, lane % F::CR), src, 16);
-          if constexpr (S8)
-            if (lane < 16) copy4(dst + 16 * F::ROW + lane * 4, scale + scale_at, 4);
+            for (int r = 0; r < F::CT; ++r) copy16(dst + F::copy_place(copy_at, r), src + r * 512, 16);
+          } else {
+#pragma unroll
+            for (int r = 0; r < F::CT; ++r, src += a.step_bytes) copy16(dst + F::copy_place(copy_at, r), src, 16);
+          }
         } else {  // some pieces are zeros
 #pragma unroll 1
           for (int r = 0; r < F::CT; ++r) {
@@ -424,25 +441,30 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             const bool ok = (mask >> t & 1) && p * 16 < D * F::ES;
             copy16(dst + F::place(t, p), static_cast<const char*>(pool) + (ok ? head_at + row + p * 16 : 0), ok ? 16 : 0);
           }
-          if constexpr (S8)
-            if (lane < 16) {
-              const bool ok = mask >> lane & 1;
-              copy4(dst + 16 * F::ROW + lane * 4, ok ? scale + scale_at : scale, ok ? 4 : 0);
-            }
-          if (lane == 0) *reinterpret_cast<uint32_t*>(ring + put + 16 * F::ROW + 64) = mask;
         }
       };
       auto send_keys = [&](int i, int put) {
         odd_tiles <<= 1;
         if (i < end) {
           locate(i);
-          odd_tiles |= mask != 0xffffu;
-          send(put, k_lane, c.k, c.ks);
+          send(put, k_lane, c.k);
+          const uint32_t dst = ring_u + put + 16 * F::ROW + lane * 4;
+          if (plain) {
+            if constexpr (S8) copy4(dst, s_lane + scale_at, 4);
+          } else {
+            odd_tiles |= mask != 0xffffu;
+            if constexpr (S8) {
+              const bool ok = mask >> (lane & 15) & 1;
+              const float* src = (whole_pages ? s_lane : s_head) + scale_at;
+              copy4(dst, ok ? src : c.ks, ok ? 4 : 0);
+            }
+            if (lane == 0) *reinterpret_cast<uint32_t*>(ring + put + 16 * F::ROW + 128) = mask;
+          }
         }
         copy_commit();
       };
       auto send_values = [&](int i, int put) {  // of the tile located last
-        if (i < end) send(put, v_lane, c.v, c.vs);
+        if (i < end) send(put, v_lane, c.v);
         copy_commit();
       };
       // The copy for AHEAD tiles on goes where the half used last lay.
@@ -453,7 +475,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       };
       __syncwarp();
       if (whole_pages) look_up(begin);
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < F::AHEAD; ++i) {
         send_keys(begin + i, 2 * i * F::SLOT);
         send_values(begin + i, (2 * i + 1) * F::SLOT);
@@ -554,8 +576,9 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           for (int j = 0; j < 4; ++j) s[nt][j] = F::RAISED ? base[nt][j & 1] : 0.0f, rest[nt][j] = 0.0f;
 #pragma unroll
         for (int j = 0; j < F::PK; ++j) {
-          const uint4 r0 = *reinterpret_cast<const uint4*>(slot + F::place(g, j * 4 + tig));
-          const uint4 r1 = *reinterpret_cast<const uint4*>(slot + F::place(g + 8, j * 4 + tig));
+          const unsigned char* piece = slot + (k_at ^ (j & 1) * 64) + j / 2 * 128;  // place(g, j * 4 + tig)
+          const uint4 r0 = *reinterpret_cast<const uint4*>(piece);
+          const uint4 r1 = *reinterpret_cast<const uint4*>(piece + 8 * F::ROW);
           const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
           for (int k = 0; k < (S8 ? 4 : 2); ++k) {
@@ -591,14 +614,14 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
               if (fabsf(rest[nt][j]) < INFINITY) s[nt][j] += rest[nt][j];
         }
         const float* scales = reinterpret_cast<const float*>(slot + 16 * F::ROW);
-        float k0 = 1.0f, k1 = 1.0f;
-        if constexpr (S8) k0 = scales[g], k1 = scales[g + 8];
+        float k0 = 1.0f, k1 = 1.0f, f0 = 1.0f, f1 = 1.0f;  // scales of tokens g and g + 8, keys and values
+        if constexpr (S8) k0 = scales[g], k1 = scales[g + 8], f0 = scales[g + 16], f1 = scales[g + 24];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[nt][j] = s[nt][j] * (j < 2 ? k0 : k1) * factor[nt][j & 1];
         if (odd_tiles >> F::AHEAD & 1) {
-          const uint32_t taken = reinterpret_cast<const uint32_t*>(scales)[16];
+          const uint32_t taken = reinterpret_cast<const uint32_t*>(scales)[32];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -657,11 +680,6 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         __syncwarp();
         slot = ring + use;
         advance();
-        float f0 = 1.0f, f1 = 1.0f;
-        if constexpr (S8) {
-          const float* vs = reinterpret_cast<const float*>(slot + 16 * F::ROW);
-          f0 = vs[g], f1 = vs[g + 8];
-        }
         uint32_t b0[NT][F::NP], b1[NT][F::NP];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -682,12 +700,13 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           uint32_t v[4][N];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int t = 2 * tig + (r & 1) + (r & 2) * 4;
+            // token 2 tig + (0, 1, 8, 9)
+            const unsigned char* piece = slot + (r & 1 ? v_at1 : v_at0) + r / 2 * 8 * F::ROW + j * 128;
             if constexpr (F::VB == 16) {
-              const uint4 u = *reinterpret_cast<const uint4*>(slot + F::place(t, j * 8 + g));
+              const uint4 u = *reinterpret_cast<const uint4*>(piece);
               v[r][0] = u.x, v[r][1] = u.y, v[r][N - 2] = u.z, v[r][N - 1] = u.w;
             } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(slot + F::place(t, g / 2) + g % 2 * 8);
+              const uint2 u = *reinterpret_cast<const uint2*>(piece);
               v[r][0] = u.x, v[r][1] = u.y;
             }
           }
@@ -741,10 +760,13 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             // this warp's last: into its ring, to be joined with its neighbours'
             const int64_t p = (int64_t)w * 2 * (8 * NT) + hh;
             if (g == 0) (ends ? a.part_stats[p] : open_stats[warp * 8 * NT + hh]) = make_float2(m[nt][j], sum);
+            // (in the ring four elements at a time are moved by the head's number, so that
+            // the lanes of a quad of heads do not all write one bank)
             float* out = ends ? a.part_out + p * F::DP : reinterpret_cast<float*>(ring) + hh * F::DP;
+            const int moved = ends ? 0 : tig * 4;
 #pragma unroll
             for (int mt = 0; mt < F::MT; ++mt)
-              *reinterpret_cast<float2*>(out + F::row_element(mt, g)) =
+              *reinterpret_cast<float2*>(out + (F::row_element(mt, g) ^ moved)) =
                   make_float2(o[mt][nt][j] * unit, o[mt][nt][2 + j] * unit);
           }
         }
@@ -775,7 +797,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
       for (int e = 0; e < (F::DP + 127) / 128; ++e)
         if (e * 128 + lane * 4 < F::DP) {
-          const float4 v = *reinterpret_cast<const float4*>(part + e * 128 + lane * 4);
+          const float4 v = *reinterpret_cast<const float4*>(part + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
           acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
           acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
         }
@@ -789,16 +811,18 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   }
 }
 
-// Rows that lie in several parts: a warp per sequence and query head.
-template <class QT, int DP>
+// Rows that lie in several parts: S warps per sequence and query head.
+template <class QT, int DP, int S>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   constexpr int E = (DP + 127) / 128;
+  __shared__ float4 s_out[S > 1 ? 8 : 1][E][32];
+  __shared__ float2 s_stats[8];
   const Cache& c = a.c;
-  const int lane = threadIdx.x & 31;
-  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % S;
+  const int id = blockIdx.x * (8 / S) + warp / S;
   next_kernel_may_start();
   wait_previous_kernel();
-  if (id >= a.tab.sequences * a.q_heads) return;
+  if (id >= a.tab.sequences * a.q_heads) return;  // (whole CTAs where S is 8)
   const int b = id / a.q_heads, h = id % a.q_heads;
   const int gi = h % a.group, row = h / a.group * a.chunks + gi / a.heads_per_row, hh = gi % a.heads_per_row;
   const int R = c.heads * a.chunks;
@@ -812,27 +836,68 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const int w = k == 0 ? w0 : k == count - 1 ? w1 : (cta0 + k) * cut.per_cta;
     return ((int64_t)w * 2 + (k == 0)) * a.heads_per_row + hh;
   };
-  float top = -INFINITY;
-  for (int k = lane; k < count; k += 32) top = fmaxf(top, a.part_stats[part(k)].x);
-  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
   float4 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = 0; k < count; ++k) {
-    const int64_t p = part(k);
-    const float2 st = a.part_stats[p];
-    const float f = ex2_approx(st.x - ref);
-    sum = fmaf(st.y, f, sum);
+  constexpr int N = 4;  // parts read at once
+  for (int k0 = slice * N; k0 < count; k0 += S * N) {
+    float2 st[N];
+    float4 v[N][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e * 128 + lane * 4 < DP) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part_out + p * DP + e * 128 + lane * 4);
+    for (int i = 0; i < N; ++i) {
+      st[i] = make_float2(-INFINITY, 0.0f);
+      if (k0 + i < count) st[i] = a.part_stats[part(k0 + i)];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[i][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k0 + i < count && e * 128 + lane * 4 < DP)
+          v[i][e] = *reinterpret_cast<const float4*>(a.part_out + part(k0 + i) * DP + e * 128 + lane * 4);
+      }
+    }
+    float next = top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) next = fmaxf(next, st[i].x);
+    const float ref = next == -INFINITY ? 0.0f : next;
+    const float keep = ex2_approx(top - ref);  // 2^-infinity (or sums of 0) at first
+    top = next;
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e].x *= keep, acc[e].y *= keep, acc[e].z *= keep, acc[e].w *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f = ex2_approx(st[i].x - ref);  // a part without weight: 2^-infinity, or o and l of 0
+      sum = fmaf(st[i].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        acc[e].x = fmaf(v[i][e].x, f, acc[e].x), acc[e].y = fmaf(v[i][e].y, f, acc[e].y);
+        acc[e].z = fmaf(v[i][e].z, f, acc[e].z), acc[e].w = fmaf(v[i][e].w, f, acc[e].w);
+      }
+    }
+  }
+  if constexpr (S > 1) {
+    if (lane == 0) s_stats[warp] = make_float2(top, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_out[warp][e][lane] = acc[e];
+    __syncthreads();
+    if (slice) return;
+    top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) top = fmaxf(top, s_stats[warp + i].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float f = ex2_approx(s_stats[warp + i].x - ref);
+      sum = fmaf(s_stats[warp + i].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float4 v = s_out[warp + i][e][lane];
         acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
         acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
       }
+    }
   }
   const bool none = sum == 0.0f;
   if (lane == 0) {
@@ -928,11 +993,10 @@ int64_t line_length(const Cache& c, const Table& tab, int64_t q_heads) {
          ceil_div(group, 8 * groups_of((int)group));
 }
 
-using Join = void (*)(Args);
-Join join_of(int type, int dp) {
-  if (type == I8Q_F32) return dp == 64 ? join_kernel<float, 64> : dp == 128 ? join_kernel<float, 128> : join_kernel<float, 256>;
-  return dp == 64 ? join_kernel<__nv_bfloat16, 64>
-                  : dp == 128 ? join_kernel<__nv_bfloat16, 128> : join_kernel<__nv_bfloat16, 256>;
+using Kernel = void (*)(Args);
+template <class QT, int S>
+Kernel join_of(int dp) {
+  return dp == 64 ? join_kernel<QT, 64, S> : dp == 128 ? join_kernel<QT, 128, S> : join_kernel<QT, 256, S>;
 }
 
 struct Layout {
@@ -965,16 +1029,39 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
   return l;
 }
 
+// A launch that may begin while the kernel before it ends (it waits for that
+// one's results itself).  All kernels of a call ask for the same division of
+// the SM's memory, so that it is not changed between them.
+int launch_after(void (*kernel)(Args), unsigned blocks, unsigned threads, int smem, cudaStream_t s, const char* what,
+                 const Args& a) {
+  struct Attr {
+    void (*kernel)(Args);
+    int smem;
+  } want{kernel, smem};
+  const int rc = once_per_device((const void*)kernel, [](void* p) -> int {
+    const Attr* x = static_cast<const Attr*>(p);
+    I8Q_CUDA_TRY(cudaFuncSetAttribute((const void*)x->kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared));
+    if (x->smem) I8Q_CUDA_TRY(cudaFuncSetAttribute((const void*)x->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, x->smem));
+    return I8Q_OK;
+  }, &want);
+  if (rc != I8Q_OK) return rc;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  return e == cudaSuccess ? I8Q_OK : cuda_fail(e, what);
+}
+
 template <class F>
 int launch_attend(Args& a, cudaStream_t s) {
   a.ctas = sm_count(), a.warps = F::W;
   a.step_bytes = a.token_bytes * 32 / F::CR;
-  const int rc = smem_attr((const void*)attend_kernel<F>, F::SMEM);
-  if (rc != I8Q_OK) return rc;
   I8Q_PROF("paged_attention", s);
-  attend_kernel<F><<<(unsigned)sm_count(), F::W * 32, F::SMEM, s>>>(a);
-  I8Q_LAUNCH_CHECK("paged_attention");
-  return I8Q_OK;
+  return launch_after(attend_kernel<F>, (unsigned)a.ctas, F::W * 32, F::SMEM, s, "paged_attention", a);
 }
 
 template <class QT, bool S8, int DP>
@@ -986,20 +1073,6 @@ template <class QT, bool S8>
 int launch_width(Args& a, cudaStream_t s) {
   return a.dp == 64 ? launch_groups<QT, S8, 64>(a, s)
                     : a.dp == 128 ? launch_groups<QT, S8, 128>(a, s) : launch_groups<QT, S8, 256>(a, s);
-}
-
-// A launch that may begin while the kernel before it ends (it waits for that
-// one's results itself).
-template <class... P, class... V>
-int launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t s, const char* what, V... v) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.stream = s;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, v...);
-  return e == cudaSuccess ? I8Q_OK : cuda_fail(e, what);
 }
 
 }  // namespace
@@ -1087,13 +1160,18 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     if (rc != I8Q_OK) return rc;
     {
       I8Q_PROF("paged_attention_join", s);
-      rc = launch_after(join_of(type, l.dp), (unsigned)ceil_div(a.tab.sequences * a.q_heads, 8), 256, s,
-                        "paged_attention_join", a);
+      // few rows mean many parts each: 8 warps then, where one has to read all in turn (18 parts of
+      // each of 32 heads: 5 us against 9)
+      const int rows = a.tab.sequences * a.q_heads;
+      const bool few = rows <= 2 * sm_count();
+      const Kernel join = type == I8Q_F32 ? (few ? join_of<float, 8>(l.dp) : join_of<float, 1>(l.dp))
+                                          : (few ? join_of<__nv_bfloat16, 8>(l.dp) : join_of<__nv_bfloat16, 1>(l.dp));
+      rc = launch_after(join, (unsigned)(few ? rows : ceil_div(rows, 8)), 256, 0, s, "paged_attention_join", a);
       if (rc != I8Q_OK) return rc;
     }
     if (accumulate) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = launch_after(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, s,
+      rc = launch_after(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, 0, s,
                         "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }
