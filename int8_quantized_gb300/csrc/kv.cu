@@ -67,6 +67,36 @@ int check_table(const i8q_page_table* t, const Cache& c, const char* who, Table&
   return I8Q_OK;
 }
 
+int launch(const void* kernel, unsigned blocks, unsigned threads, int smem, int cluster, cudaStream_t s,
+           const char* what, void** args) {
+  struct Want {
+    const void* kernel;
+    int smem;
+  } want{kernel, smem};
+  const int rc = once_per_device(kernel, [](void* p) -> int {
+    const Want* w = static_cast<const Want*>(p);
+    I8Q_CUDA_TRY(cudaFuncSetAttribute(w->kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared));
+    cudaFuncAttributes attr;
+    I8Q_CUDA_TRY(cudaFuncGetAttributes(&attr, w->kernel));
+    if (w->smem)
+      I8Q_CUDA_TRY(cudaFuncSetAttribute(w->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        227 * 1024 - (int)attr.sharedSizeBytes));
+    return I8Q_OK;
+  }, &want);
+  if (rc != I8Q_OK) return rc;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = s;
+  cfg.attrs = attr, cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  return e == cudaSuccess ? I8Q_OK : cuda_fail(e, what);
+}
+
 }  // namespace kv
 
 namespace {
@@ -100,7 +130,8 @@ __device__ __forceinline__ void store1(T* p, float v) {
   else *p = __float2bfloat16_rn(v);
 }
 
-// One warp per row of q, k or v: lane l turns pairs l, l + 32, ...
+// Rows of any alignment: one warp per row of q, k or v, lane l turns pairs
+// l, l + 32, ...
 template <class T, bool S8>
 __global__ void __launch_bounds__(256)
 append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
@@ -182,35 +213,245 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
   }
 }
 
-template <class T, bool S8>
+// Four neighbouring elements.
+template <class T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 v;
+  __device__ float at(int i) const { return (&v.x)[i]; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 v;
+  __device__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <class T>
+__device__ __forceinline__ Four<T> load4(const T* p) {
+  return Four<T>{__ldcs(reinterpret_cast<const decltype(Four<T>::v)*>(p))};
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The same on rows that can be read four elements at a time.  L lanes (8, 16
+// or 32) hold a row, each the four pairs of its unit: elements 4u and pairs +
+// 4u on, or 8u and 8u + 4 on.  A CTA has one token (or one of `splits` shares
+// of its rows, for calls of few tokens); a lane keeps its unit, so its four
+// cosines and sines serve all heads, and sends for up to four rows before it
+// works on the first.
+template <class T, bool S8, int L>
+__global__ void __launch_bounds__(256)
+append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
+                    Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, uint32_t* status) {
+  constexpr int G = 256 / L, N = 4;
+  kv::next_kernel_may_start();
+  kv::wait_previous_kernel();
+  const int64_t t = blockIdx.x / splits;
+  const int slot = threadIdx.x / L, u = threadIdx.x % L;
+  const int per = q.heads + 2 * c.heads, step = G * splits;
+  const bool in_row = u < c.dim / 8, turns = u < r.pairs / 4;
+  const int b = seq[t], i = index[t];
+  int axis[4], pos[4];
+  bool turn_ok = true;
+  for (int a = 0; a < r.axes; ++a) turn_ok &= (unsigned)r.positions[a * r.position_stride + t] < (unsigned)r.rows;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    axis[j] = (r.axis[u >> 2 & 7] >> ((u & 3) * 8 + 2 * j)) & 3;
+    pos[j] = turns && turn_ok ? r.positions[axis[j] * r.position_stride + t] : 0;
+  }
+  // where a row lies and where its result goes
+  auto source = [&](int row) {
+    const bool is_q = row < q.heads, is_k = !is_q && row < q.heads + c.heads;
+    const int head = is_q ? row : row - q.heads - (is_k ? 0 : c.heads);
+    const Rows& in = is_q ? q : is_k ? k : v;
+    return static_cast<const T*>(in.p) + t * in.token + head * in.head;
+  };
+  auto places = [&](int row, int& e1, int& e2) {
+    const bool split = turns && !r.interleaved && row < q.heads + c.heads;
+    e1 = split ? 4 * u : 8 * u;
+    e2 = split ? r.pairs + 4 * u : 8 * u + 4;
+  };
+  int page = 0, off = 0;
+  bool ok = b >= 0;
+  if (ok) {
+    ok = b < tab.sequences && i >= 0 && i < tab.max_pages * c.page_size && turn_ok;
+    if (!ok && threadIdx.x == 0) kv::report_index(status);
+    if (ok) ok = kv::find(c, tab, b, i, page, off, status);
+  }
+  if (!ok) return;
+  float cs[4], sn[4];
+  if (turns) {
+    const int64_t g = (int64_t)pos[0] * r.pairs + 4 * u;
+    if (pos[0] == pos[1] && pos[0] == pos[2] && pos[0] == pos[3]) {
+      const float4 x = *reinterpret_cast<const float4*>(r.cos + g), y = *reinterpret_cast<const float4*>(r.sin + g);
+      cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
+      sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t gj = (int64_t)pos[j] * r.pairs + 4 * u + j;
+        cs[j] = r.cos[gj], sn[j] = r.sin[gj];
+      }
+    }
+  }
+  for (int row0 = (blockIdx.x % splits) * G + slot; row0 < per; row0 += N * step) {
+    Four<T> x[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (row0 + n * step < per && in_row) {
+        int e1, e2;
+        places(row0 + n * step, e1, e2);
+        const T* src = source(row0 + n * step);
+        x[n][0] = load4(src + e1), x[n][1] = load4(src + e2);
+      }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int row = row0 + n * step;
+      if (row >= per) break;  // (the same for the L lanes of a row)
+      const bool is_q = row < q.heads, is_v = row >= q.heads + c.heads;
+      const int head = is_q ? row : row - q.heads - (is_v ? c.heads : 0);
+      int e1, e2;
+      places(row, e1, e2);
+      float y[8];
+      uint32_t most = 0;
+      if (in_row) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = x[n][0].at(j), y[4 + j] = x[n][1].at(j);
+        if (turns && !is_v) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // pair j: elements j of the two halves, or two neighbours
+            float& a = r.interleaved ? y[2 * j] : y[j];
+            float& z = r.interleaved ? y[2 * j + 1] : y[4 + j];
+            const float w = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(z, sn[j]));
+            z = __fadd_rn(__fmul_rn(z, cs[j]), __fmul_rn(a, sn[j]));
+            a = w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(fabsf(y[j])));
+      }
+      if (is_q) {
+        if (in_row) {
+          T* o = static_cast<T*>(qo.p) + t * qo.token + head * qo.head;
+          store4(o + e1, y), store4(o + e2, y + 4);
+        }
+        continue;
+      }
+      const int64_t dst = kv::row_at(c, page, head, off);
+      if constexpr (!S8) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) + dst;
+        if (in_row) store4(o + e1, y), store4(o + e2, y + 4);
+      } else {
+        // the largest magnitude as its bit pattern: a NaN is above infinity
+        const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) most = max(most, __shfl_xor_sync(lanes, most, m));
+        float s = __fdiv_rn(__uint_as_float(most), 127.0f);
+        if (s == 0.0f) s = 1.0f;
+        const float rcp = quot_rcp(s);
+        if (in_row) {
+          int8_t* o = static_cast<int8_t*>(is_v ? c.v : c.k) + dst;
+          uint32_t code[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) code[j] = quot_code_bits(y[j], s, rcp, -128.0f, 127.0f, 0);
+          *reinterpret_cast<uint32_t*>(o + e1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
+          *reinterpret_cast<uint32_t*>(o + e2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
+        }
+        if (u == 0) (is_v ? c.vs : c.ks)[kv::scale_at(c, page, head, off)] = s;
+      }
+      if (!is_v && c.score && u == 0) c.score[kv::scale_at(c, page, head, off)] = 0.0f;
+    }
+  }
+}
+
+// Eight elements per lane, L lanes a row; a CTA has four tokens (or a share
+// of their rows), and a lane reads its piece of all four before it writes.
+template <class T, bool S8, int L>
 __global__ void __launch_bounds__(256)
 gather_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
-              Rows k, Rows v, uint32_t* status) {
-  const int lane = threadIdx.x & 31;
-  const int per = 2 * c.heads;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; w < tokens * per; w += (int64_t)gridDim.x * 8) {
-    const int64_t t = w / per;
-    const int row = (int)(w - t * per);
-    const int b = seq[t];
-    if (b < 0) continue;
-    const int i = index[t];
-    int page, off;
-    if (b >= tab.sequences || i < 0 || i >= tab.max_pages * c.page_size) {
-      kv::report_index(status);
-      continue;
+              int splits, Rows k, Rows v, int aligned, uint32_t* status) {
+  constexpr int G = 256 / L, N = 4;
+  kv::next_kernel_may_start();
+  kv::wait_previous_kernel();
+  const int64_t t0 = blockIdx.x / splits * (int64_t)N;
+  const int slot = threadIdx.x / L, d = threadIdx.x % L * 8;
+  int64_t at[N], scale_at[N];
+  bool ok[N];
+  int b[N], i[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    b[n] = t0 + n < tokens ? seq[t0 + n] : -1;
+    i[n] = t0 + n < tokens ? index[t0 + n] : 0;
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    int page = 0, off = 0;
+    ok[n] = b[n] >= 0;
+    if (ok[n]) {
+      ok[n] = b[n] < tab.sequences && i[n] >= 0 && i[n] < tab.max_pages * c.page_size;
+      if (!ok[n]) kv::report_index(status);
+      if (ok[n]) ok[n] = kv::find(c, tab, b[n], i[n], page, off, status);
     }
-    if (!kv::find(c, tab, b, i, page, off, status)) continue;
-    const bool is_k = row < c.heads;
-    const int head = is_k ? row : row - c.heads;
-    const int64_t src = kv::row_at(c, page, head, off);
-    T* o = is_k ? static_cast<T*>(k.p) + t * k.token + head * k.head : static_cast<T*>(v.p) + t * v.token + head * v.head;
-    float s = 1.0f;
-    if (S8) s = (is_k ? c.ks : c.vs)[kv::scale_at(c, page, head, off)];
-    for (int e = lane; e < c.dim; e += 32) {
-      float x;
-      if (S8) x = __fmul_rn((float)static_cast<const int8_t*>(is_k ? c.k : c.v)[src + e], s);
-      else x = __bfloat162float(static_cast<const __nv_bfloat16*>(is_k ? c.k : c.v)[src + e]);
-      store1(o + e, x);
+    at[n] = kv::row_at(c, page, 0, off) + d;
+    scale_at[n] = kv::scale_at(c, page, 0, off);
+  }
+  if (d >= c.dim) return;
+  for (int row = (blockIdx.x % splits) * G + slot; row < 2 * c.heads; row += G * splits) {
+    const bool is_v = row >= c.heads;
+    const int head = is_v ? row - c.heads : row;
+    uint4 w[N];
+    float s[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (ok[n]) {
+        const int64_t src = at[n] + head * c.head_stride;
+        if constexpr (S8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(is_v ? c.v : c.k) + src);
+          w[n].x = x.x, w[n].y = x.y;
+          s[n] = (is_v ? c.vs : c.ks)[scale_at[n] + head * c.s_head];
+        } else {
+          w[n] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? c.v : c.k) + src);
+        }
+      }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (!ok[n]) continue;
+      const uint32_t u[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (S8) y[j] = __fmul_rn((float)(int8_t)(u[j / 4] >> (8 * (j & 3))), s[n]);
+        else y[j] = __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+      }
+      T* o = (is_v ? static_cast<T*>(v.p) + (t0 + n) * v.token + head * v.head
+                   : static_cast<T*>(k.p) + (t0 + n) * k.token + head * k.head) + d;
+      if (aligned) {
+        if constexpr (std::is_same<T, float>::value) {
+          __stcs(reinterpret_cast<float4*>(o), make_float4(y[0], y[1], y[2], y[3]));
+          __stcs(reinterpret_cast<float4*>(o + 4), make_float4(y[4], y[5], y[6], y[7]));
+        } else {
+          uint32_t z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            z[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          __stcs(reinterpret_cast<uint4*>(o), make_uint4(z[0], z[1], z[2], z[3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store1(o + j, y[j]);
+      }
     }
   }
 }
@@ -221,6 +462,21 @@ int check_tokens(const char* who, const int32_t* seq, const int32_t* index, int6
   if (type != I8Q_F32 && type != I8Q_BF16) return fail(I8Q_ERR_INVALID_ARG, w + ": type must be I8Q_F32 or I8Q_BF16");
   if (tokens && (!seq || !index)) return fail(I8Q_ERR_INVALID_ARG, w + ": seq or index is NULL");
   return I8Q_OK;
+}
+
+// Whether every row begins on a multiple of n elements.
+bool rows_aligned(const Rows& r, int64_t es, int n) {
+  return reinterpret_cast<uintptr_t>(r.p) % (size_t)(es * n) == 0 && r.token % n == 0 && r.head % n == 0;
+}
+
+// Lanes of a row at eight elements a lane, as a power of two.
+int lanes_of(int dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
+
+template <class F>
+int with_lanes(int dim, F f) {
+  const int l = lanes_of(dim);
+  return l == 8 ? f(std::integral_constant<int, 8>()) : l == 16 ? f(std::integral_constant<int, 16>())
+                                                                : f(std::integral_constant<int, 32>());
 }
 
 template <class F>
@@ -281,8 +537,20 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
   cudaStream_t s = as_stream(stream);
   return with_types(type, cache->type, [&](auto t, auto s8) -> int {
     using T = decltype(t);
-    const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (q_heads + 2 * c.heads), 8), (int64_t)sm_count() * 64);
     I8Q_PROF("kv_append", s);
+    const bool units = r.pairs % 4 == 0 && rows_aligned(rk, sizeof(T), 4) && rows_aligned(rv, sizeof(T), 4) &&
+                       (!q_heads || (rows_aligned(rq, sizeof(T), 4) && rows_aligned(ro, sizeof(T), 4))) &&
+                       reinterpret_cast<uintptr_t>(r.cos) % 16 == 0 && reinterpret_cast<uintptr_t>(r.sin) % 16 == 0;
+    if (units)
+      return with_lanes(c.dim, [&](auto lanes) -> int {
+        constexpr int L = decltype(lanes)::value;
+        // few tokens: their rows over as many CTAs as two for each SM, each with a row per L lanes at least
+        const int64_t most = ceil_div(q_heads + 2 * c.heads, 256 / L);
+        const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / tokens));
+        return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), 256, 0, 1, s,
+                          "kv_append", c, tab, seq, index, splits, rq, ro, rk, rv, r, status);
+      });
+    const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (q_heads + 2 * c.heads), 8), (int64_t)sm_count() * 64);
     append_kernel<T, decltype(s8)::value>
         <<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rq, ro, rk, rv, r, status);
     I8Q_LAUNCH_CHECK("kv_append");
@@ -309,10 +577,14 @@ extern "C" int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* ta
   cudaStream_t s = as_stream(stream);
   return with_types(type, cache->type, [&](auto t, auto s8) -> int {
     using T = decltype(t);
-    const int64_t blocks = std::min<int64_t>(ceil_div(tokens * 2 * c.heads, 8), (int64_t)sm_count() * 64);
     I8Q_PROF("kv_gather", s);
-    gather_kernel<T, decltype(s8)::value><<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rk, rv, status);
-    I8Q_LAUNCH_CHECK("kv_gather");
-    return I8Q_OK;
+    const int aligned = rows_aligned(rk, sizeof(T), 16 / sizeof(T)) && rows_aligned(rv, sizeof(T), 16 / sizeof(T));
+    return with_lanes(c.dim, [&](auto lanes) -> int {
+      constexpr int L = decltype(lanes)::value;
+      const int64_t groups = ceil_div(tokens, 4), most = ceil_div(2 * c.heads, 256 / L);
+      const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / groups));
+      return kv::launch(gather_kernel<T, decltype(s8)::value, L>, (unsigned)(groups * splits), 256, 0, 1, s, "kv_gather",
+                        c, tab, seq, index, tokens, splits, rk, rv, aligned, status);
+    });
   });
 }

@@ -2,6 +2,8 @@
 // checks that its entry points share.
 #pragma once
 
+#include <tuple>
+
 #include "common.cuh"
 
 namespace i8q {
@@ -53,7 +55,29 @@ __device__ __forceinline__ int64_t scale_at(const Cache& c, int page, int head, 
   return page * c.s_page + head * c.s_head + off * c.s_token;
 }
 
-// Host side: the arguments checked, and the device forms of the structs.
+// A kernel launched by launch() may begin while the one before it ends: it
+// waits for that one's results before it reads anything, and lets the next
+// one begin.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+// Host side.
+// Launch with the stream's order relaxed as above, in clusters of `cluster`
+// CTAs.  All these kernels ask for the same division of the SM's memory, so
+// that it is not changed between them.
+int launch(const void* kernel, unsigned blocks, unsigned threads, int smem, int cluster, cudaStream_t s,
+           const char* what, void** args);
+template <class... P, class... V>
+int launch(void (*kernel)(P...), unsigned blocks, unsigned threads, int smem, int cluster, cudaStream_t s,
+           const char* what, const V&... v) {
+  std::tuple<P...> p(v...);  // the parameters in the kernel's own types
+  return std::apply([&](auto&... x) {
+    void* args[] = {const_cast<void*>(static_cast<const void*>(&x))...};
+    return launch(reinterpret_cast<const void*>(kernel), blocks, threads, smem, cluster, s, what, args);
+  }, p);
+}
+
+// The arguments checked, and the device forms of the structs.
 int check_cache(const i8q_kv_cache* c, const char* who, Cache& out);
 int check_table(const i8q_page_table* t, const Cache& c, const char* who, Table& out);
 

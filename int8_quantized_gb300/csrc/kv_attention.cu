@@ -49,6 +49,8 @@ namespace {
 
 using kv::Cache;
 using kv::Table;
+using kv::next_kernel_may_start;
+using kv::wait_previous_kernel;
 
 struct Heads {  // [sequences][heads][dim], strides in elements
   void* p;
@@ -56,8 +58,8 @@ struct Heads {  // [sequences][heads][dim], strides in elements
 };
 
 constexpr int kMaxSequences = 2048;  // of one launch: their line positions lie in shared memory
-constexpr int kRowCost = 2;          // of a row's start and end, in tiles
-constexpr int kMinPart = 8;          // a part is not shorter unless there are that many rows
+constexpr int kRowCost = 4;          // of a row's start and end, in tiles
+constexpr int kMinPart = 4;          // tiles of a part of a row that is cut
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -101,7 +103,9 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut_line(const Args& a, int n, int rows) {
   Cut c;
-  c.parts = min(max(rows, (n + kMinPart - 1) / kMinPart), a.ctas * a.warps);
+  // rows are cut where a row holds two parts of kMinPart tiles and more
+  const int tiles = n - rows * kRowCost;
+  c.parts = min(tiles / (2 * kMinPart) >= rows ? tiles / kMinPart : rows, a.ctas * a.warps);
   c.per_cta = (c.parts + a.ctas - 1) / a.ctas;
   c.q = n / c.parts;
   c.longer = n - c.q * c.parts;
@@ -120,8 +124,6 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -1029,39 +1031,12 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
   return l;
 }
 
-// A launch that may begin while the kernel before it ends (it waits for that
-// one's results itself).  All kernels of a call ask for the same division of
-// the SM's memory, so that it is not changed between them.
-int launch_after(void (*kernel)(Args), unsigned blocks, unsigned threads, int smem, cudaStream_t s, const char* what,
-                 const Args& a) {
-  struct Attr {
-    void (*kernel)(Args);
-    int smem;
-  } want{kernel, smem};
-  const int rc = once_per_device((const void*)kernel, [](void* p) -> int {
-    const Attr* x = static_cast<const Attr*>(p);
-    I8Q_CUDA_TRY(cudaFuncSetAttribute((const void*)x->kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                      cudaSharedmemCarveoutMaxShared));
-    if (x->smem) I8Q_CUDA_TRY(cudaFuncSetAttribute((const void*)x->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, x->smem));
-    return I8Q_OK;
-  }, &want);
-  if (rc != I8Q_OK) return rc;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  return e == cudaSuccess ? I8Q_OK : cuda_fail(e, what);
-}
-
 template <class F>
 int launch_attend(Args& a, cudaStream_t s) {
   a.ctas = sm_count(), a.warps = F::W;
   a.step_bytes = a.token_bytes * 32 / F::CR;
   I8Q_PROF("paged_attention", s);
-  return launch_after(attend_kernel<F>, (unsigned)a.ctas, F::W * 32, F::SMEM, s, "paged_attention", a);
+  return kv::launch(attend_kernel<F>, (unsigned)a.ctas, F::W * 32, F::SMEM, 1, s, "paged_attention", a);
 }
 
 template <class QT, bool S8, int DP>
@@ -1166,12 +1141,12 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
       const bool few = rows <= 2 * sm_count();
       const Kernel join = type == I8Q_F32 ? (few ? join_of<float, 8>(l.dp) : join_of<float, 1>(l.dp))
                                           : (few ? join_of<__nv_bfloat16, 8>(l.dp) : join_of<__nv_bfloat16, 1>(l.dp));
-      rc = launch_after(join, (unsigned)(few ? rows : ceil_div(rows, 8)), 256, 0, s, "paged_attention_join", a);
+      rc = kv::launch(join, (unsigned)(few ? rows : ceil_div(rows, 8)), 256, 0, 1, s, "paged_attention_join", a);
       if (rc != I8Q_OK) return rc;
     }
     if (accumulate) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = launch_after(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, 0, s,
+      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, 0, 1, s,
                         "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }

@@ -1,9 +1,14 @@
 // kv_evict.cu -- eviction from a paged key/value cache by accumulated
-// attention weight.
+// attention weight: which tokens of a sequence and head stay, then their
+// copies into fewer pages.
+#include <cooperative_groups.h>
+
 #include "kv.cuh"
 
 namespace i8q {
 namespace {
+
+namespace cg = cooperative_groups;
 
 using kv::Cache;
 using kv::Table;
@@ -15,6 +20,8 @@ struct Args {
   int32_t* kept;
   int32_t* new_lengths;
   int budget, sink, recent;
+  int room;    // keys of a CTA's share that its shared memory holds
+  int blocks;  // of a row in the second kernel
   uint32_t* status;
 };
 
@@ -31,11 +38,12 @@ __device__ __forceinline__ uint32_t key_of(const Args& a, int b, int h, int t) {
   return order_key(a.c.score[kv::scale_at(a.c, page, h, off)]);
 }
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kWarps = kThreads / 32, kBins = 2048;
 
-// Inclusive sum over the block of v, and its total.
-__device__ int block_scan(int v, int* total, int* warp_sums) {
+// Inclusive sum of v over the block; total: of all.
+__device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+#pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, i);
     if (lane >= i) v += u;
@@ -43,96 +51,181 @@ __device__ int block_scan(int v, int* total, int* warp_sums) {
   __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    before += w < warp ? warp_sums[w] : 0;
-    all += warp_sums[w];
+  int x = warp_sums[lane];
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, i);
+    if (lane >= i) x += u;
   }
-  *total = all;
-  return v + before;
+  *total = __shfl_sync(0xffffffffu, x, 31);
+  const int before = __shfl_sync(0xffffffffu, x, warp ? warp - 1 : 0);
+  return v + (warp ? before : 0);
 }
 
-// One CTA per sequence and head: the key of the last kept candidate, found
-// one 8-bit digit at a time from counts, then the kept indices in order.
-__global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
-  __shared__ int count[256], warp_sums[kThreads / 32], s_digit, s_need;
-  const int b = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
+// A cluster per sequence and head, each CTA an equal share of its tokens, so
+// that a long sequence is read by several SMs and its keys are read once,
+// into shared memory.  The key of the last kept candidate is found by digits
+// of 11, 11 and 10 bits: each CTA counts its keys by digit, all add up the
+// cluster's counts and pick the digit in which the wanted rank falls.  The
+// kept indices then follow from counts of the tokens before, in order.
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Args a) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_more, s_equal;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int row = blockIdx.x / C, b = row / a.c.heads, h = row % a.c.heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  kv::next_kernel_may_start();
+  kv::wait_previous_kernel();
   const int len = kv::cut_length(a.c, a.tab, a.lengths[b], a.status);
   const int n = min(len, a.budget);
-  int32_t* kept = a.kept + (int64_t)blockIdx.x * a.budget;
-  for (int j = n + threadIdx.x; j < a.budget; j += kThreads) kept[j] = -1;
-  if (h == 0 && threadIdx.x == 0 && a.new_lengths) a.new_lengths[b] = n;
-  if (n == len) {
-    for (int j = threadIdx.x; j < n; j += kThreads) kept[j] = j;
+  int32_t* kept = a.kept + (int64_t)row * a.budget;
+  const int all = C * kThreads, me = rank * kThreads + threadIdx.x;
+  for (int j = n + me; j < a.budget; j += all) kept[j] = -1;
+  if (h == 0 && me == 0 && a.new_lengths) a.new_lengths[b] = n;
+  if (n == len) {  // (all CTAs of the cluster leave here)
+    for (int j = me; j < n; j += all) kept[j] = j;
     return;
   }
-  const int lo = a.sink, hi = len - a.recent;
-  int need = a.budget - a.sink - a.recent;  // of the hi - lo candidates, which are more
+  const int share = (len + C - 1) / C, t0 = min(rank * share, len), mine = min(share, len - t0);
+  const bool held = share <= a.room;
+  if (held) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < mine; i += kThreads) keys[i] = key_of(a, b, h, t0 + i);
+  }
+  __syncthreads();
+  auto key_at = [&](int i) { return held ? keys[i] : key_of(a, b, h, t0 + i); };
+  // candidates: neither the first `sink` nor the last `recent`
+  const int lo = a.sink - t0, hi = len - a.recent - t0;
+  int need = a.budget - a.sink - a.recent;
+  const bool none = need == 0;
   uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; need && shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) count[threadIdx.x] = 0;
+  for (int shift = 21; !none && shift >= 0; shift -= shift == 21 ? 11 : 10) {
+    // digits at bits 21 to 31, 10 to 20 and 0 to 9
+    const uint32_t digits = shift ? 0x7ffu : 0x3ffu;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
     __syncthreads();
-    for (int t = lo + threadIdx.x; t < hi; t += kThreads) {
-      const uint32_t key = key_of(a, b, h, t);
-      if ((key & mask) == prefix) atomicAdd(&count[(key >> shift) & 255], 1);
+    for (int i = max(lo, 0) + threadIdx.x; i < min(hi, mine); i += kThreads) {
+      const uint32_t key = key_at(i);
+      if ((key & mask) == prefix) atomicAdd(&count[key >> shift & digits], 1);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int d = 255, left = need;
-      while (d > 0 && count[d] < left) left -= count[d--];
-      s_digit = d, s_need = left;
+    cluster.sync();
+    // two digits a thread, from the highest down
+    const int d = kBins - 1 - 2 * threadIdx.x;
+    int upper = 0, lower = 0;
+    for (int r = 0; r < C; ++r) {
+      const int* other = cluster.map_shared_rank(count, r);
+      upper += other[d], lower += other[d - 1];
     }
-    __syncthreads();
+    int total;
+    const int through = block_scan(upper + lower, &total, warp_sums), before = through - upper - lower;
+    if (before < need && need <= through) {
+      const bool first = need <= before + upper;
+      s_digit = first ? d : d - 1;
+      s_need = need - before - (first ? 0 : upper);
+    }
+    cluster.sync();  // (also: no CTA clears counts that another still reads)
     prefix |= (uint32_t)s_digit << shift;
-    mask |= 255u << shift;
+    mask |= digits << shift;
     need = s_need;
     __syncthreads();
   }
-  // candidates above the key are kept, and the first `need` that equal it
-  int at = 0, equal = 0;
-  const bool none = a.budget == a.sink + a.recent;
-  for (int t0 = 0; t0 < len; t0 += kThreads) {
-    const int t = t0 + threadIdx.x;
-    bool keep = t < len && (t < lo || t >= hi), eq = false;
-    if (!none && t >= lo && t < hi) {
-      const uint32_t key = key_of(a, b, h, t);
-      keep = key > prefix;
-      eq = key == prefix;
+  // Candidates above the key stay, and the first `need` that equal it.  Each
+  // warp has a run of the share.
+  const int run = (mine + kWarps * 32 - 1) / (kWarps * 32) * 32, i0 = warp * run, i1 = min(i0 + run, mine);
+  auto classes = [&](int i, bool& more, bool& equal) {
+    more = i < i1 && (i < lo || i >= hi);
+    equal = false;
+    if (!none && i < i1 && i >= lo && i < hi) {
+      const uint32_t key = key_at(i);
+      more = key > prefix;
+      equal = key == prefix;
     }
-    int total;
-    const int rank = block_scan(eq, &total, warp_sums) + equal;
-    if (eq && rank <= need) keep = true;
-    equal += total;
-    const int pos = block_scan(keep, &total, warp_sums) + at;
-    if (keep) kept[pos - 1] = t;
-    at += total;
+  };
+  int mores = 0, equals = 0;
+  for (int i = i0; i < i1; i += 32) {
+    bool more, equal;
+    classes(i + lane, more, equal);
+    mores += __popc(__ballot_sync(0xffffffffu, more));
+    equals += __popc(__ballot_sync(0xffffffffu, equal));
   }
+  if (lane == 0) warp_more[warp] = mores, warp_equal[warp] = equals;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int m = 0, e = 0;
+    for (int w = 0; w < kWarps; ++w) m += warp_more[w], e += warp_equal[w];
+    s_more = m, s_equal = e;
+  }
+  cluster.sync();
+  int more_before = 0, equal_before = 0;
+  for (int r = 0; r < rank; ++r) more_before += *cluster.map_shared_rank(&s_more, r), equal_before += *cluster.map_shared_rank(&s_equal, r);
+  for (int w = 0; w < warp; ++w) more_before += warp_more[w], equal_before += warp_equal[w];
+  for (int i = i0; i < i1; i += 32) {
+    bool more, equal;
+    classes(i + lane, more, equal);
+    const uint32_t m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, equal);
+    const uint32_t under = (1u << lane) - 1;
+    const int before = equal_before + __popc(e & under);
+    if (more || (equal && before < need)) kept[more_before + __popc(m & under) + min(before, need)] = t0 + i + lane;
+    more_before += __popc(m), equal_before += __popc(e);
+  }
+  cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// One warp per kept token and head.
+// A CTA copies kRows kept tokens of a row (sequence and head): first a
+// thread per token finds both places and moves its scales and score, then
+// groups of lanes move the rows, 16 bytes a lane, four in flight.
+constexpr int kRows = 64;
 template <int BYTES>
-__global__ void __launch_bounds__(256) move_kernel(Args a, int64_t rows) {
+__global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Args a) {
+  __shared__ int64_t from[kRows], to[kRows];  // bytes; from -1: nothing to move
   const Cache& c = a.c;
-  const int lane = threadIdx.x & 31;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; w < rows; w += (int64_t)gridDim.x * 8) {
-    const int64_t bh = w / a.budget;
-    const int j = (int)(w - bh * a.budget);
-    const int b = (int)(bh / c.heads), h = (int)(bh % c.heads);
-    const int t = a.kept[w];
-    if (t < 0) continue;
+  const int row = blockIdx.x / a.blocks, j0 = (blockIdx.x - row * a.blocks) * kRows;
+  const int b = row / c.heads, h = row % c.heads;
+  kv::next_kernel_may_start();
+  kv::wait_previous_kernel();
+  const int32_t* kept = a.kept + (int64_t)row * a.budget;
+  if (kept[j0] < 0) return;  // past the last kept token
+  if (threadIdx.x < kRows) {
+    const int j = j0 + threadIdx.x;
+    const int t = j < a.budget ? kept[j] : -1;
+    int64_t src = -1, dst = 0;
     int p0, o0, p1, o1;
-    if (!kv::find(c, a.tab, b, t, p0, o0, a.status) || !kv::find(c, a.to, b, j, p1, o1, a.status)) continue;
-    const int64_t src = kv::row_at(c, p0, h, o0) * BYTES, dst = kv::row_at(c, p1, h, o1) * BYTES;
-    for (int e = lane * 16; e < c.dim * BYTES; e += 512) {
-      *reinterpret_cast<uint4*>(static_cast<char*>(c.k) + dst + e) =
-          *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + src + e);
-      *reinterpret_cast<uint4*>(static_cast<char*>(c.v) + dst + e) =
-          *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + src + e);
+    if (t >= 0) {
+      const bool ok0 = kv::find(c, a.tab, b, t, p0, o0, a.status), ok1 = kv::find(c, a.to, b, j, p1, o1, a.status);
+      if (ok0 && ok1) {
+        src = kv::row_at(c, p0, h, o0) * BYTES, dst = kv::row_at(c, p1, h, o1) * BYTES;
+        const int64_t s0 = kv::scale_at(c, p0, h, o0), s1 = kv::scale_at(c, p1, h, o1);
+        const float score = c.score[s0];
+        if (BYTES == 1) {
+          const float ks = c.ks[s0], vs = c.vs[s0];
+          c.ks[s1] = ks, c.vs[s1] = vs;
+        }
+        c.score[s1] = score;
+      }
     }
-    const int64_t s0 = kv::scale_at(c, p0, h, o0), s1 = kv::scale_at(c, p1, h, o1);
-    if (lane == 0) c.score[s1] = c.score[s0];
-    if (lane == 1 && c.ks) c.ks[s1] = c.ks[s0];
-    if (lane == 2 && c.ks) c.vs[s1] = c.vs[s0];
+    from[threadIdx.x] = src, to[threadIdx.x] = dst;
+  }
+  __syncthreads();
+  const int pieces = c.dim * BYTES / 16;  // of a row
+  int lanes = 1;
+  while (lanes < pieces) lanes *= 2;
+  const int groups = 256 / lanes, group = threadIdx.x / lanes, e = threadIdx.x % lanes * 16;
+  if (e >= c.dim * BYTES) return;
+  for (int r0 = group; r0 < 2 * kRows; r0 += 4 * groups) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i * groups;
+      if (r < 2 * kRows && from[r % kRows] >= 0)
+        x[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(r < kRows ? c.k : c.v) + from[r % kRows] + e));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i * groups;
+      if (r < 2 * kRows && from[r % kRows] >= 0)
+        *reinterpret_cast<uint4*>(static_cast<char*>(r < kRows ? c.k : c.v) + to[r % kRows] + e) = x[i];
+    }
   }
 }
 
@@ -153,10 +246,11 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   if (!lengths || !kept) return fail(I8Q_ERR_INVALID_ARG, "kv_evict: lengths or kept is NULL");
   if (a.to.sequences != a.tab.sequences)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: table and new_table differ in sequences");
-  if ((int64_t)a.tab.sequences * a.c.heads > INT32_MAX)
-    return fail(I8Q_ERR_INVALID_ARG, "kv_evict: sequences * kv_heads out of range");
+  const int64_t heads = (int64_t)a.tab.sequences * a.c.heads;
   if (budget < 1 || budget > (int64_t)a.to.max_pages * a.c.page_size)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: budget must be 1 .. new_table's max_pages * page_size");
+  if (heads > INT32_MAX / 16 || heads * ceil_div(budget, kRows) > INT32_MAX)
+    return fail(I8Q_ERR_INVALID_ARG, "kv_evict: sequences * kv_heads * budget out of range");
   if (sink < 0 || recent < 0 || sink > budget || recent > budget - sink)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: sink + recent must be within 0 .. budget");
   a.lengths = lengths, a.kept = kept, a.new_lengths = new_lengths;
@@ -164,17 +258,22 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   a.status = device_status_word();
   if (!a.status) return fail(I8Q_ERR_CUDA, "kv_evict: no status word");
   cudaStream_t s = as_stream(stream);
-  const int64_t heads = (int64_t)a.tab.sequences * a.c.heads;
+  // As many CTAs to a row as give every SM one, or keep a share within 16K
+  // tokens (16 passes of a CTA), up to the portable 8.  A share whose keys
+  // shared memory cannot hold is read again in each pass.
+  const int64_t most = (int64_t)a.tab.max_pages * a.c.page_size;
+  int cluster = 1;
+  while (cluster < 8 && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384) && most / cluster > 1024)
+    cluster *= 2;
+  a.room = (int)std::min<int64_t>(ceil_div(most, cluster), 48 * 1024);
   {
     I8Q_PROF("kv_evict_select", s);
-    select_kernel<<<(unsigned)heads, kThreads, 0, s>>>(a);
-    I8Q_LAUNCH_CHECK("kv_evict_select");
+    rc = kv::launch(select_kernel, (unsigned)(heads * cluster), kThreads, a.room * 4, cluster, s, "kv_evict_select", a);
+    if (rc != I8Q_OK) return rc;
   }
   I8Q_PROF("kv_evict_move", s);
-  const int64_t rows = heads * budget;
-  const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(rows, 8), (int64_t)sm_count() * 64);
-  if (cache->type == I8Q_S8) move_kernel<1><<<blocks, 256, 0, s>>>(a, rows);
-  else move_kernel<2><<<blocks, 256, 0, s>>>(a, rows);
-  I8Q_LAUNCH_CHECK("kv_evict_move");
-  return I8Q_OK;
+  a.blocks = (int)ceil_div(budget, kRows);
+  const unsigned blocks = (unsigned)(heads * a.blocks);
+  return cache->type == I8Q_S8 ? kv::launch(move_kernel<1>, blocks, 256, 0, 1, s, "kv_evict_move", a)
+                               : kv::launch(move_kernel<2>, blocks, 256, 0, 1, s, "kv_evict_move", a);
 }
