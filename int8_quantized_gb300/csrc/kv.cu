@@ -213,6 +213,31 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
   }
 }
 
+__device__ __forceinline__ void turn(float& x1, float& x2, float cs, float sn) {
+  const float y1 = __fsub_rn(__fmul_rn(x1, cs), __fmul_rn(x2, sn));
+  x2 = __fadd_rn(__fmul_rn(x2, cs), __fmul_rn(x1, sn));
+  x1 = y1;
+}
+
+// rint of the quotients y / s, |y| <= 127 s, as low bytes.  With r = fl(1 /
+// s), the products y r (1 - 2^-20) and y r (1 + 2^-20) enclose the rounded
+// quotient; one fma with 1.5 2^23 rounds each to an integer (its low bits).
+// Where both round to the same integer so does the quotient; where they do
+// not, or 1 / s is not a normal number, the eight quotients are formed.
+__device__ __forceinline__ void quotient_codes(const float (&y)[8], float s, uint32_t (&code)[8]) {
+  const float r = quot_rcp(s), hi = __fmul_rn(r, 1.0f + 0x1p-20f), lo = __fmul_rn(r, 1.0f - 0x1p-20f);
+  uint32_t differ = r != r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    code[j] = __float_as_uint(__fmaf_rn(y[j], hi, 12582912.0f));
+    differ |= code[j] ^ __float_as_uint(__fmaf_rn(y[j], lo, 12582912.0f));
+  }
+  if (differ) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) code[j] = rint_code_bits(__fdiv_rn(y[j], s), -128.0f, 127.0f, 0);
+  }
+}
+
 // Four neighbouring elements.
 template <class T>
 struct Four;
@@ -259,60 +284,61 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   const int slot = threadIdx.x / L, u = threadIdx.x % L;
   const int per = q.heads + 2 * c.heads, step = G * splits;
   const bool in_row = u < c.dim / 8, turns = u < r.pairs / 4;
-  const int b = seq[t], i = index[t];
-  int axis[4], pos[4];
-  bool turn_ok = true;
-  for (int a = 0; a < r.axes; ++a) turn_ok &= (unsigned)r.positions[a * r.position_stride + t] < (unsigned)r.rows;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    axis[j] = (r.axis[u >> 2 & 7] >> ((u & 3) * 8 + 2 * j)) & 3;
-    pos[j] = turns && turn_ok ? r.positions[axis[j] * r.position_stride + t] : 0;
-  }
-  // where a row lies and where its result goes
-  auto source = [&](int row) {
-    const bool is_q = row < q.heads, is_k = !is_q && row < q.heads + c.heads;
-    const int head = is_q ? row : row - q.heads - (is_k ? 0 : c.heads);
-    const Rows& in = is_q ? q : is_k ? k : v;
-    return static_cast<const T*>(in.p) + t * in.token + head * in.head;
-  };
   auto places = [&](int row, int& e1, int& e2) {
     const bool split = turns && !r.interleaved && row < q.heads + c.heads;
     e1 = split ? 4 * u : 8 * u;
     e2 = split ? r.pairs + 4 * u : 8 * u + 4;
   };
-  int page = 0, off = 0;
-  bool ok = b >= 0;
-  if (ok) {
-    ok = b < tab.sequences && i >= 0 && i < tab.max_pages * c.page_size && turn_ok;
-    if (!ok && threadIdx.x == 0) kv::report_index(status);
-    if (ok) ok = kv::find(c, tab, b, i, page, off, status);
+  Four<T> x[N][2];
+  auto send = [&](int row0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int row = row0 + n * step;
+      if (row >= per || !in_row) continue;
+      const bool is_q = row < q.heads, is_k = !is_q && row < q.heads + c.heads;
+      const int head = is_q ? row : row - q.heads - (is_k ? 0 : c.heads);
+      const Rows& in = is_q ? q : is_k ? k : v;
+      const T* src = static_cast<const T*>(in.p) + t * in.token + head * in.head;
+      int e1, e2;
+      places(row, e1, e2);
+      x[n][0] = load4(src + e1), x[n][1] = load4(src + e2);
+    }
+  };
+  // the rows do not wait for the token's place and positions
+  int row0 = (blockIdx.x % splits) * G + slot;
+  send(row0);
+  const int b = seq[t], i = index[t];
+  int pos[4] = {0, 0, 0, 0};
+  bool turn_ok = true;
+  for (int a = 0; a < r.axes; ++a) {
+    const int at = r.positions[a * r.position_stride + t];
+    turn_ok &= (unsigned)at < (unsigned)r.rows;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((int)((r.axis[u >> 2 & 7] >> ((u & 3) * 8 + 2 * j)) & 3) == a) pos[j] = at;
   }
-  if (!ok) return;
-  float cs[4], sn[4];
-  if (turns) {
-    const int64_t g = (int64_t)pos[0] * r.pairs + 4 * u;
+  float cs[4] = {}, sn[4] = {};
+  if (turns && turn_ok) {
     if (pos[0] == pos[1] && pos[0] == pos[2] && pos[0] == pos[3]) {
-      const float4 x = *reinterpret_cast<const float4*>(r.cos + g), y = *reinterpret_cast<const float4*>(r.sin + g);
-      cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
-      sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
+      const int64_t g = (int64_t)pos[0] * r.pairs + 4 * u;
+      const float4 y = *reinterpret_cast<const float4*>(r.cos + g), z = *reinterpret_cast<const float4*>(r.sin + g);
+      cs[0] = y.x, cs[1] = y.y, cs[2] = y.z, cs[3] = y.w;
+      sn[0] = z.x, sn[1] = z.y, sn[2] = z.z, sn[3] = z.w;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t gj = (int64_t)pos[j] * r.pairs + 4 * u + j;
-        cs[j] = r.cos[gj], sn[j] = r.sin[gj];
+        const int64_t g = (int64_t)pos[j] * r.pairs + 4 * u + j;
+        cs[j] = r.cos[g], sn[j] = r.sin[g];
       }
     }
   }
-  for (int row0 = (blockIdx.x % splits) * G + slot; row0 < per; row0 += N * step) {
-    Four<T> x[N][2];
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (row0 + n * step < per && in_row) {
-        int e1, e2;
-        places(row0 + n * step, e1, e2);
-        const T* src = source(row0 + n * step);
-        x[n][0] = load4(src + e1), x[n][1] = load4(src + e2);
-      }
+  if (b < 0) return;
+  int page = 0, off = 0;
+  bool ok = b < tab.sequences && i >= 0 && i < tab.max_pages * c.page_size && turn_ok;
+  if (!ok && threadIdx.x == 0) kv::report_index(status);
+  if (ok) ok = kv::find(c, tab, b, i, page, off, status);
+  if (!ok) return;
+  for (; row0 < per; row0 += N * step, send(row0)) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int row = row0 + n * step;
@@ -327,14 +353,13 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = x[n][0].at(j), y[4 + j] = x[n][1].at(j);
         if (turns && !is_v) {
+          // pair j: elements j of the two halves, or two neighbours
+          if (r.interleaved) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // pair j: elements j of the two halves, or two neighbours
-            float& a = r.interleaved ? y[2 * j] : y[j];
-            float& z = r.interleaved ? y[2 * j + 1] : y[4 + j];
-            const float w = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(z, sn[j]));
-            z = __fadd_rn(__fmul_rn(z, cs[j]), __fmul_rn(a, sn[j]));
-            a = w;
+            for (int j = 0; j < 4; ++j) turn(y[2 * j], y[2 * j + 1], cs[j], sn[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) turn(y[j], y[4 + j], cs[j], sn[j]);
           }
         }
 #pragma unroll
@@ -358,12 +383,10 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
         for (int m = 1; m < L; m <<= 1) most = max(most, __shfl_xor_sync(lanes, most, m));
         float s = __fdiv_rn(__uint_as_float(most), 127.0f);
         if (s == 0.0f) s = 1.0f;
-        const float rcp = quot_rcp(s);
         if (in_row) {
           int8_t* o = static_cast<int8_t*>(is_v ? c.v : c.k) + dst;
           uint32_t code[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) code[j] = quot_code_bits(y[j], s, rcp, -128.0f, 127.0f, 0);
+          quotient_codes(y, s, code);
           *reinterpret_cast<uint32_t*>(o + e1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
           *reinterpret_cast<uint32_t*>(o + e2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
         }
@@ -374,58 +397,64 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   }
 }
 
-// Eight elements per lane, L lanes a row; a CTA has four tokens (or a share
-// of their rows), and a lane reads its piece of all four before it writes.
+// A CTA has kTokens tokens (or a share of their rows): a thread per token
+// finds its place, then L lanes hold a row, eight elements each, four rows in
+// flight.
+constexpr int kTokens = 16;
 template <class T, bool S8, int L>
 __global__ void __launch_bounds__(256)
 gather_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
               int splits, Rows k, Rows v, int aligned, uint32_t* status) {
   constexpr int G = 256 / L, N = 4;
+  __shared__ int64_t at[kTokens], scale_at[kTokens];  // at -1: left out
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
-  const int64_t t0 = blockIdx.x / splits * (int64_t)N;
-  const int slot = threadIdx.x / L, d = threadIdx.x % L * 8;
-  int64_t at[N], scale_at[N];
-  bool ok[N];
-  int b[N], i[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    b[n] = t0 + n < tokens ? seq[t0 + n] : -1;
-    i[n] = t0 + n < tokens ? index[t0 + n] : 0;
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    int page = 0, off = 0;
-    ok[n] = b[n] >= 0;
-    if (ok[n]) {
-      ok[n] = b[n] < tab.sequences && i[n] >= 0 && i[n] < tab.max_pages * c.page_size;
-      if (!ok[n]) kv::report_index(status);
-      if (ok[n]) ok[n] = kv::find(c, tab, b[n], i[n], page, off, status);
+  const int64_t t0 = blockIdx.x / splits * (int64_t)kTokens;
+  if (threadIdx.x < kTokens) {
+    int64_t src = -1;
+    const int64_t t = t0 + threadIdx.x;
+    if (t < tokens) {
+      const int b = seq[t], i = index[t];
+      int page = 0, off = 0;
+      bool ok = b >= 0;
+      if (ok) {
+        ok = b < tab.sequences && i >= 0 && i < tab.max_pages * c.page_size;
+        if (!ok) kv::report_index(status);
+        if (ok) ok = kv::find(c, tab, b, i, page, off, status);
+      }
+      if (ok) src = kv::row_at(c, page, 0, off);
+      scale_at[threadIdx.x] = kv::scale_at(c, page, 0, off);
     }
-    at[n] = kv::row_at(c, page, 0, off) + d;
-    scale_at[n] = kv::scale_at(c, page, 0, off);
+    at[threadIdx.x] = src;
   }
+  __syncthreads();
+  const int d = threadIdx.x % L * 8;
   if (d >= c.dim) return;
-  for (int row = (blockIdx.x % splits) * G + slot; row < 2 * c.heads; row += G * splits) {
-    const bool is_v = row >= c.heads;
-    const int head = is_v ? row - c.heads : row;
+  // rows of the CTA: token by token within a head, so that neighbours of a page are read together
+  const int rows = 2 * c.heads * kTokens, step = G * splits;
+  for (int r0 = (blockIdx.x % splits) * G + threadIdx.x / L; r0 < rows; r0 += N * step) {
     uint4 w[N];
     float s[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (ok[n]) {
-        const int64_t src = at[n] + head * c.head_stride;
+    for (int n = 0; n < N; ++n) {
+      const int r = r0 + n * step, row = r / kTokens, t = r % kTokens;
+      if (r < rows && at[t] >= 0) {
+        const bool is_v = row >= c.heads;
+        const int head = is_v ? row - c.heads : row;
+        const int64_t src = at[t] + head * c.head_stride + d;
         if constexpr (S8) {
-          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(is_v ? c.v : c.k) + src);
+          const uint2 x = __ldcs(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(is_v ? c.v : c.k) + src));
           w[n].x = x.x, w[n].y = x.y;
-          s[n] = (is_v ? c.vs : c.ks)[scale_at[n] + head * c.s_head];
+          s[n] = (is_v ? c.vs : c.ks)[scale_at[t] + head * c.s_head];
         } else {
-          w[n] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? c.v : c.k) + src);
+          w[n] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? c.v : c.k) + src));
         }
       }
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      if (!ok[n]) continue;
+      const int r = r0 + n * step, row = r / kTokens, t = r % kTokens;
+      if (r >= rows || at[t] < 0) continue;
       const uint32_t u[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
       float y[8];
 #pragma unroll
@@ -433,8 +462,10 @@ gather_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
         if constexpr (S8) y[j] = __fmul_rn((float)(int8_t)(u[j / 4] >> (8 * (j & 3))), s[n]);
         else y[j] = __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
       }
-      T* o = (is_v ? static_cast<T*>(v.p) + (t0 + n) * v.token + head * v.head
-                   : static_cast<T*>(k.p) + (t0 + n) * k.token + head * k.head) + d;
+      const bool is_v = row >= c.heads;
+      const int head = is_v ? row - c.heads : row;
+      const Rows& to = is_v ? v : k;
+      T* o = static_cast<T*>(to.p) + (t0 + t) * to.token + head * to.head + d;
       if (aligned) {
         if constexpr (std::is_same<T, float>::value) {
           __stcs(reinterpret_cast<float4*>(o), make_float4(y[0], y[1], y[2], y[3]));
@@ -581,7 +612,7 @@ extern "C" int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* ta
     const int aligned = rows_aligned(rk, sizeof(T), 16 / sizeof(T)) && rows_aligned(rv, sizeof(T), 16 / sizeof(T));
     return with_lanes(c.dim, [&](auto lanes) -> int {
       constexpr int L = decltype(lanes)::value;
-      const int64_t groups = ceil_div(tokens, 4), most = ceil_div(2 * c.heads, 256 / L);
+      const int64_t groups = ceil_div(tokens, kTokens), most = ceil_div(2 * c.heads * kTokens, 256 / L);
       const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / groups));
       return kv::launch(gather_kernel<T, decltype(s8)::value, L>, (unsigned)(groups * splits), 256, 0, 1, s, "kv_gather",
                         c, tab, seq, index, tokens, splits, rk, rv, aligned, status);

@@ -90,8 +90,29 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int share = (len + C - 1) / C, t0 = min(rank * share, len), mine = min(share, len - t0);
   const bool held = share <= a.room;
   if (held) {
-#pragma unroll 8
-    for (int i = threadIdx.x; i < mine; i += kThreads) keys[i] = key_of(a, b, h, t0 + i);
+    // eight pages are looked up before the first of their scores is read
+    constexpr int N = 8;
+    const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
+    for (int i0 = threadIdx.x; i0 < mine; i0 += N * kThreads) {
+      int page[N], off[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int i = i0 + n * kThreads, p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size);
+        off[n] = t0 + i - p * a.c.page_size;
+        page[n] = i < mine ? pages[p] : 0;
+      }
+      float score[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const bool ok = (unsigned)page[n] < (unsigned)a.c.pages;
+        if (!ok) kv::report_index(a.status);
+        score[n] = i0 + n * kThreads < mine && ok ? a.c.score[kv::scale_at(a.c, page[n], h, off[n])] : 0.0f;
+        if (!ok) page[n] = -1;
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (i0 + n * kThreads < mine) keys[i0 + n * kThreads] = page[n] < 0 ? 0 : order_key(score[n]);
+    }
   }
   __syncthreads();
   auto key_at = [&](int i) { return held ? keys[i] : key_of(a, b, h, t0 + i); };
