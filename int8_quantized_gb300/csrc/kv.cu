@@ -271,43 +271,50 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
 // or 32) hold a row, each the four pairs of its unit: elements 4u and pairs +
 // 4u on, or 8u and 8u + 4 on.  A CTA has one token (or one of `splits` shares
 // of its rows, for calls of few tokens); a lane keeps its unit, so its four
-// cosines and sines serve all heads, and sends for up to four rows before it
-// works on the first.
+// cosines and sines serve all heads, and its first rows are sent for before
+// the token's place and positions are known.  128 threads a token: with 256
+// half of the instructions were what a thread does once.
+constexpr int kUnitThreads = 128;
 template <class T, bool S8, int L>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
                     Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, uint32_t* status) {
-  constexpr int G = 256 / L, N = 4;
+  constexpr int G = kUnitThreads / L, NQ = 4, NK = 2;  // rows of q, and of k and v, that a lane has in flight
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
-  const int64_t t = blockIdx.x / splits;
-  const int slot = threadIdx.x / L, u = threadIdx.x % L;
-  const int per = q.heads + 2 * c.heads, step = G * splits;
-  const bool in_row = u < c.dim / 8, turns = u < r.pairs / 4;
-  auto places = [&](int row, int& e1, int& e2) {
-    const bool split = turns && !r.interleaved && row < q.heads + c.heads;
-    e1 = split ? 4 * u : 8 * u;
-    e2 = split ? r.pairs + 4 * u : 8 * u + 4;
-  };
-  Four<T> x[N][2];
-  auto send = [&](int row0) {
+  const int64_t t = splits == 1 ? blockIdx.x : blockIdx.x / splits;
+  const int slot = threadIdx.x / L + (splits == 1 ? 0 : blockIdx.x % splits * G), u = threadIdx.x % L;
+  const int step = G * splits;
+  const bool in_row = u < c.dim / 8, turns = u < r.pairs / 4, split = turns && !r.interleaved;
+  // a unit's two places in a row that is turned by halves, and in any other
+  const int h1 = split ? 4 * u : 8 * u, h2 = split ? r.pairs + 4 * u : 8 * u + 4, e1 = 8 * u, e2 = 8 * u + 4;
+  const T* q_row = static_cast<const T*>(q.p) + t * q.token;
+  const T* k_row = static_cast<const T*>(k.p) + t * k.token;
+  const T* v_row = static_cast<const T*>(v.p) + t * v.token;
+  Four<T> xq[NQ][2], xk[NK][2];
+  auto send_q = [&](int head) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int row = row0 + n * step;
-      if (row >= per || !in_row) continue;
-      const bool is_q = row < q.heads, is_k = !is_q && row < q.heads + c.heads;
-      const int head = is_q ? row : row - q.heads - (is_k ? 0 : c.heads);
-      const Rows& in = is_q ? q : is_k ? k : v;
-      const T* src = static_cast<const T*>(in.p) + t * in.token + head * in.head;
-      int e1, e2;
-      places(row, e1, e2);
-      x[n][0] = load4(src + e1), x[n][1] = load4(src + e2);
+    for (int n = 0; n < NQ; ++n)
+      if (head + n * step < q.heads && in_row) {
+        const T* src = q_row + (head + n * step) * q.head;
+        xq[n][0] = load4(src + h1), xq[n][1] = load4(src + h2);
+      }
+  };
+  auto send_k = [&](int row) {  // keys' heads, then values'
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      const int j = row + n * step;
+      if (j < 2 * c.heads && in_row) {
+        const bool is_v = j >= c.heads;
+        const T* src = is_v ? v_row + (j - c.heads) * v.head : k_row + j * k.head;
+        xk[n][0] = load4(src + (is_v ? e1 : h1)), xk[n][1] = load4(src + (is_v ? e2 : h2));
+      }
     }
   };
-  // the rows do not wait for the token's place and positions
-  int row0 = (blockIdx.x % splits) * G + slot;
-  send(row0);
+  send_k(slot);
+  send_q(slot);
   const int b = seq[t], i = index[t];
+  const uint32_t axis = r.axis[u >> 2 & 7] >> ((u & 3) * 8) & 0xffu;  // two bits a pair
   int pos[4] = {0, 0, 0, 0};
   bool turn_ok = true;
   for (int a = 0; a < r.axes; ++a) {
@@ -315,7 +322,7 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
     turn_ok &= (unsigned)at < (unsigned)r.rows;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if ((int)((r.axis[u >> 2 & 7] >> ((u & 3) * 8 + 2 * j)) & 3) == a) pos[j] = at;
+      if ((int)(axis >> 2 * j & 3) == a) pos[j] = at;
   }
   float cs[4] = {}, sn[4] = {};
   if (turns && turn_ok) {
@@ -338,47 +345,53 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   if (!ok && threadIdx.x == 0) kv::report_index(status);
   if (ok) ok = kv::find(c, tab, b, i, page, off, status);
   if (!ok) return;
-  for (; row0 < per; row0 += N * step, send(row0)) {
+  auto turned = [&](const Four<T> (&x)[2], float (&y)[8], bool really) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int row = row0 + n * step;
-      if (row >= per) break;  // (the same for the L lanes of a row)
-      const bool is_q = row < q.heads, is_v = row >= q.heads + c.heads;
-      const int head = is_q ? row : row - q.heads - (is_v ? c.heads : 0);
-      int e1, e2;
-      places(row, e1, e2);
-      float y[8];
-      uint32_t most = 0;
-      if (in_row) {
+    for (int j = 0; j < 4; ++j) y[j] = x[0].at(j), y[4 + j] = x[1].at(j);
+    if (!really) return;
+    // pair j: elements j of the two halves, or two neighbours
+    if (r.interleaved) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = x[n][0].at(j), y[4 + j] = x[n][1].at(j);
-        if (turns && !is_v) {
-          // pair j: elements j of the two halves, or two neighbours
-          if (r.interleaved) {
+      for (int j = 0; j < 4; ++j) turn(y[2 * j], y[2 * j + 1], cs[j], sn[j]);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) turn(y[2 * j], y[2 * j + 1], cs[j], sn[j]);
-          } else {
+      for (int j = 0; j < 4; ++j) turn(y[j], y[4 + j], cs[j], sn[j]);
+    }
+  };
+  T* const o_row = static_cast<T*>(qo.p) + t * qo.token;
+  for (int head = slot; head < q.heads;) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) turn(y[j], y[4 + j], cs[j], sn[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(fabsf(y[j])));
+    for (int n = 0; n < NQ; ++n)
+      if (head + n * step < q.heads && in_row) {
+        float y[8];
+        turned(xq[n], y, turns);
+        T* o = o_row + (head + n * step) * qo.head;
+        store4(o + h1, y), store4(o + h2, y + 4);
       }
-      if (is_q) {
-        if (in_row) {
-          T* o = static_cast<T*>(qo.p) + t * qo.token + head * qo.head;
-          store4(o + e1, y), store4(o + e2, y + 4);
-        }
-        continue;
-      }
-      const int64_t dst = kv::row_at(c, page, head, off);
+    head += NQ * step;
+    send_q(head);
+  }
+  const int64_t at = kv::row_at(c, page, 0, off), scale_at = kv::scale_at(c, page, 0, off);
+  const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
+  for (int row = slot; row < 2 * c.heads;) {
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      const int j = row + n * step;
+      if (j >= 2 * c.heads) break;  // (the same for the L lanes of a row)
+      const bool is_v = j >= c.heads;
+      const int head = is_v ? j - c.heads : j;
+      const int p1 = is_v ? e1 : h1, p2 = is_v ? e2 : h2;
+      const int64_t dst = at + head * c.head_stride, sc = scale_at + head * c.s_head;
+      float y[8] = {};
+      if (in_row) turned(xk[n], y, turns && !is_v);
       if constexpr (!S8) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) + dst;
-        if (in_row) store4(o + e1, y), store4(o + e2, y + 4);
+        if (in_row) store4(o + p1, y), store4(o + p2, y + 4);
       } else {
         // the largest magnitude as its bit pattern: a NaN is above infinity
-        const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(fabsf(y[e])));
 #pragma unroll
         for (int m = 1; m < L; m <<= 1) most = max(most, __shfl_xor_sync(lanes, most, m));
         float s = __fdiv_rn(__uint_as_float(most), 127.0f);
@@ -387,13 +400,15 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
           int8_t* o = static_cast<int8_t*>(is_v ? c.v : c.k) + dst;
           uint32_t code[8];
           quotient_codes(y, s, code);
-          *reinterpret_cast<uint32_t*>(o + e1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
-          *reinterpret_cast<uint32_t*>(o + e2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
+          *reinterpret_cast<uint32_t*>(o + p1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
+          *reinterpret_cast<uint32_t*>(o + p2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
         }
-        if (u == 0) (is_v ? c.vs : c.ks)[kv::scale_at(c, page, head, off)] = s;
+        if (u == 0) (is_v ? c.vs : c.ks)[sc] = s;
       }
-      if (!is_v && c.score && u == 0) c.score[kv::scale_at(c, page, head, off)] = 0.0f;
+      if (!is_v && c.score && u == 0) c.score[sc] = 0.0f;
     }
+    row += NK * step;
+    send_k(row);
   }
 }
 
@@ -576,9 +591,9 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
       return with_lanes(c.dim, [&](auto lanes) -> int {
         constexpr int L = decltype(lanes)::value;
         // few tokens: their rows over as many CTAs as two for each SM, each with a row per L lanes at least
-        const int64_t most = ceil_div(q_heads + 2 * c.heads, 256 / L);
+        const int64_t most = ceil_div(std::max<int64_t>(q_heads, 2 * c.heads), kUnitThreads / L);
         const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / tokens));
-        return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), 256, 0, 1, s,
+        return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), kUnitThreads, 0, 1, s,
                           "kv_append", c, tab, seq, index, splits, rq, ro, rk, rv, r, status);
       });
     const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (q_heads + 2 * c.heads), 8), (int64_t)sm_count() * 64);

@@ -22,6 +22,7 @@ struct Args {
   int budget, sink, recent;
   int room;    // keys of a CTA's share that its shared memory holds
   int blocks;  // of a row in the second kernel
+  int fours;   // four neighbouring tokens' scores can be read at once
   uint32_t* status;
 };
 
@@ -34,7 +35,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 __device__ __forceinline__ uint32_t key_of(const Args& a, int b, int h, int t) {
   int page, off;
-  if (!kv::find(a.c, a.tab, b, t, page, off, a.status)) return 0;
+  if (!kv::find(a.c, a.tab, b, t, page, off, a.status)) return order_key(-INFINITY);
   return order_key(a.c.score[kv::scale_at(a.c, page, h, off)]);
 }
 
@@ -62,6 +63,46 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
   return v + (warp ? before : 0);
 }
 
+// The keys of tokens t0 .. t0 + n - 1, V neighbours of a page at a time.
+template <int V>
+__device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const float* scores, int t0, int n,
+                                     uint32_t* keys) {
+  constexpr int N = 4;
+  for (int i0 = threadIdx.x * V; i0 < n; i0 += N * V * kThreads) {
+    int64_t at[N];  // -1: no such page
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = i0 + j * V * kThreads;
+      if (i >= n) break;
+      const int p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size), page = pages[p];
+      at[j] = page * a.c.s_page + (t0 + i - p * a.c.page_size) * a.c.s_token;
+      if ((unsigned)page >= (unsigned)a.c.pages) {
+        kv::report_index(a.status);
+        at[j] = -1;
+      }
+    }
+    float x[N][V];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (i0 + j * V * kThreads >= n) break;
+      if (at[j] < 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[j][v] = -INFINITY;
+      } else if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(x[j]) = *reinterpret_cast<const float4*>(scores + at[j]);
+      } else {
+        x[j][0] = scores[at[j]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (i0 + j * V * kThreads >= n) break;
+#pragma unroll
+      for (int v = 0; v < V; ++v) keys[i0 + j * V * kThreads + v] = order_key(x[j][v]);
+    }
+  }
+}
+
 // A cluster per sequence and head, each CTA an equal share of its tokens, so
 // that a long sequence is read by several SMs and its keys are read once,
 // into shared memory.  The key of the last kept candidate is found by digits
@@ -69,7 +110,7 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
 // cluster's counts and pick the digit in which the wanted rank falls.  The
 // kept indices then follow from counts of the tokens before, in order.
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Args a) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ int count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_more, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -87,32 +128,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     for (int j = me; j < n; j += all) kept[j] = j;
     return;
   }
-  const int share = (len + C - 1) / C, t0 = min(rank * share, len), mine = min(share, len - t0);
+  const int share = ((len + C - 1) / C + 3) / 4 * 4, t0 = min(rank * share, len), mine = min(share, len - t0);  // shares begin on multiples of 4
   const bool held = share <= a.room;
   if (held) {
-    // eight pages are looked up before the first of their scores is read
-    constexpr int N = 8;
+    // four neighbouring scores of a page at once where they lie so, and four
+    // places looked up before the first of them is read
     const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
-    for (int i0 = threadIdx.x; i0 < mine; i0 += N * kThreads) {
-      int page[N], off[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int i = i0 + n * kThreads, p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size);
-        off[n] = t0 + i - p * a.c.page_size;
-        page[n] = i < mine ? pages[p] : 0;
-      }
-      float score[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const bool ok = (unsigned)page[n] < (unsigned)a.c.pages;
-        if (!ok) kv::report_index(a.status);
-        score[n] = i0 + n * kThreads < mine && ok ? a.c.score[kv::scale_at(a.c, page[n], h, off[n])] : 0.0f;
-        if (!ok) page[n] = -1;
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (i0 + n * kThreads < mine) keys[i0 + n * kThreads] = page[n] < 0 ? 0 : order_key(score[n]);
-    }
+    const float* scores = a.c.score + h * a.c.s_head;
+    if (a.fours) hold<4>(a, pages, scores, t0, mine, keys);
+    else hold<1>(a, pages, scores, t0, mine, keys);
   }
   __syncthreads();
   auto key_at = [&](int i) { return held ? keys[i] : key_of(a, b, h, t0 + i); };
@@ -126,9 +150,20 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const uint32_t digits = shift ? 0x7ffu : 0x3ffu;
     for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
     __syncthreads();
-    for (int i = max(lo, 0) + threadIdx.x; i < min(hi, mine); i += kThreads) {
-      const uint32_t key = key_at(i);
+    auto add = [&](uint32_t key) {
       if ((key & mask) == prefix) atomicAdd(&count[key >> shift & digits], 1);
+    };
+    const int c0 = max(lo, 0), c1 = min(hi, mine);
+    if (held) {  // four keys at a time between the ends
+      const int q0 = (c0 + 3) / 4 * 4, q1 = max(q0, c1 / 4 * 4);
+      for (int i = q0 + threadIdx.x * 4; i < q1; i += kThreads * 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        add(k.x), add(k.y), add(k.z), add(k.w);
+      }
+      if (c0 + (int)threadIdx.x < min(q0, c1)) add(keys[c0 + threadIdx.x]);
+      if (q1 + (int)threadIdx.x < c1) add(keys[q1 + threadIdx.x]);
+    } else {
+      for (int i = c0 + threadIdx.x; i < c1; i += kThreads) add(key_of(a, b, h, t0 + i));
     }
     cluster.sync();
     // two digits a thread, from the highest down
@@ -280,13 +315,16 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   if (!a.status) return fail(I8Q_ERR_CUDA, "kv_evict: no status word");
   cudaStream_t s = as_stream(stream);
   // As many CTAs to a row as give every SM one, or keep a share within 16K
-  // tokens (16 passes of a CTA), up to the portable 8.  A share whose keys
-  // shared memory cannot hold is read again in each pass.
+  // tokens, up to the portable 8 (8 rows of 131072 tokens took three times
+  // as long in clusters of 16).  A share whose keys shared memory cannot hold
+  // is read again in each pass.
   const int64_t most = (int64_t)a.tab.max_pages * a.c.page_size;
   int cluster = 1;
   while (cluster < 8 && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384) && most / cluster > 1024)
     cluster *= 2;
-  a.room = (int)std::min<int64_t>(ceil_div(most, cluster), 48 * 1024);
+  a.room = (int)std::min<int64_t>(round_up(ceil_div(most, cluster), 4), 48 * 1024);
+  a.fours = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
+            reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
   {
     I8Q_PROF("kv_evict_select", s);
     rc = kv::launch(select_kernel, (unsigned)(heads * cluster), kThreads, a.room * 4, cluster, s, "kv_evict_select", a);
