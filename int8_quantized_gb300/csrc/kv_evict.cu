@@ -111,7 +111,7 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
 // kept indices then follow from counts of the tokens before, in order.
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_more, s_equal;
+  __shared__ int count[kBins], total_count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_more, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / C, b = row / a.c.heads, h = row % a.c.heads;
@@ -165,14 +165,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     } else {
       for (int i = c0 + threadIdx.x; i < c1; i += kThreads) add(key_of(a, b, h, t0 + i));
     }
-    cluster.sync();
-    // two digits a thread, from the highest down
-    const int d = kBins - 1 - 2 * threadIdx.x;
-    int upper = 0, lower = 0;
-    for (int r = 0; r < C; ++r) {
-      const int* other = cluster.map_shared_rank(count, r);
-      upper += other[d], lower += other[d - 1];
+    // each CTA adds up a share of the digits and hands the sums to all
+    const int* sums = count;
+    if (C > 1) {
+      cluster.sync();
+      const int part = kBins / C;
+      for (int i = threadIdx.x; i < part; i += kThreads) {
+        int x = 0;
+        for (int r = 0; r < C; ++r) x += cluster.map_shared_rank(count, r)[rank * part + i];
+        for (int r = 0; r < C; ++r) cluster.map_shared_rank(total_count, r)[rank * part + i] = x;
+      }
+      cluster.sync();
+      sums = total_count;
+    } else {
+      __syncthreads();
     }
+    // two digits a thread, from the highest down
+    const int d = kBins - 1 - 2 * threadIdx.x, upper = sums[d], lower = sums[d - 1];
     int total;
     const int through = block_scan(upper + lower, &total, warp_sums), before = through - upper - lower;
     if (before < need && need <= through) {
@@ -180,10 +189,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       s_digit = first ? d : d - 1;
       s_need = need - before - (first ? 0 : upper);
     }
-    cluster.sync();  // (also: no CTA clears counts that another still reads)
+    __syncthreads();
     prefix |= (uint32_t)s_digit << shift;
     mask |= digits << shift;
     need = s_need;
+    // (a CTA that clears its counts has passed the second cluster.sync, after which none reads them; the
+    // sums are written anew after the next pass's first)
     __syncthreads();
   }
   // Candidates above the key stay, and the first `need` that equal it.  Each
