@@ -195,34 +195,41 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&r)[N]) {
   }
 }
 
-template <class T>
-__device__ __forceinline__ float as_float(T x) {
-  if constexpr (std::is_same<T, float>::value) return x;
-  else return __bfloat162float(x);
-}
-
 __device__ __forceinline__ float fp16_sum(uint32_t w) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
   return f.x + f.y;
 }
 
-// N consecutive elements of a q row, in fp32.
+// N consecutive elements of a q row as they lie in memory, and in fp32.
 template <class T, int N>
-__device__ __forceinline__ void load_row(const T* p, bool aligned, float (&x)[N]) {
-  if (aligned) {
-    constexpr int V = 16 / sizeof(T);
+struct Piece {
+  uint4 w[N * sizeof(T) / 16];
+  __device__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < N / V; ++i) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p + i * V);
-      const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[i * V + j] = as_float(e[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = as_float(p[i]);
+    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
+  __device__ void load_any(const T* p) {  // at any alignment
+    T e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(e)[i];
+  }
+  __device__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ void to_float(float (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int word = i * (int)sizeof(T) / 4;
+      const uint4 u = w[word / 4];
+      const uint32_t v = word % 4 == 0 ? u.x : word % 4 == 1 ? u.y : word % 4 == 2 ? u.z : u.w;
+      if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(v);
+      else x[i] = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
+    }
+  }
+};
 
 template <class T>
 __device__ __forceinline__ void store_pair(T* p, float x, float y, bool paired) {
@@ -266,7 +273,7 @@ struct Form {
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
   // warps: 12 of 168 registers where they suffice, else 8 or 4 of 255 (at
   // 128 registers 16 warps spent a fifth more instructions on addresses)
-  static constexpr int W = S8 && DP <= 128 && NT == 1 ? 12 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  static constexpr int W = (S8 || DP == 64) && DP <= 128 && NT == 1 ? 12 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
   static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
   static constexpr int AHEAD = ROOM >= 7 ? 3 : ROOM >= 5 ? 2 : 1;  // tiles in flight
   static constexpr int SLOTS = 2 * AHEAD + 1;
@@ -443,11 +450,20 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       bool plain = false;                // all of them, every piece inside its row, in one page
       uint32_t odd_tiles = 0;            // bit j: of the tile sent for j tiles ago, not all tokens take part
       const int last = tile_count(a, len) - 1;
-      auto look_up = [&](int i) {
-        if (i + lane < end) {
-          const int t = tile0 + i + lane, p = t / per_page;
-          off_next = (t - p * per_page) * 16;
-          page_next = pages[p];
+      bool in_next = false;
+      auto look_up = [&](int i) {  // ahead of their use: tiles i + lane, or token lane % 16 of tile i
+        if (whole_pages) {
+          if (i + lane < end) {
+            const int t = tile0 + i + lane, p = t / per_page;
+            off_next = (t - p * per_page) * 16;
+            page_next = pages[p];
+          }
+        } else {
+          const int t = (tile0 + i) * 16 + (lane & 15);
+          in_next = i < end && t >= first && t < len;
+          const int p = (int)((unsigned)t / (unsigned)c.page_size);
+          off_next = t - p * c.page_size;
+          page_next = in_next ? pages[p] : 0;
         }
       };
       auto locate = [&](int i) {
@@ -470,13 +486,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           if (at < 0) mask = 0;
           plain = mask == 0xffffu && D == F::DP;
         } else {  // at and scale_at: of token lane % 16
-          const int t = t0 + (lane & 15);
-          int page = 0, off = 0;
-          bool ok = t >= first && t < len;
-          if (ok) ok = kv::find(c, a.tab, b, t, page, off, a.status);
-          at = page * a.page_bytes + off * a.token_bytes;
-          scale_at = page * c.s_page + off * c.s_token;
-          mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+          const bool bad = (unsigned)page_next >= (unsigned)c.pages;
+          if (bad) kv::report_index(a.status);
+          at = page_next * a.page_bytes + off_next * a.token_bytes;
+          scale_at = page_next * c.s_page + off_next * c.s_token;
+          mask = __ballot_sync(0xffffffffu, in_next && !bad) & 0xffffu;
+          look_up(i + 1);
         }
       };
       auto send = [&](int put, const char* from, const void* pool) {
@@ -531,7 +546,23 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         use = use == (F::SLOTS - 1) * F::SLOT ? 0 : use + F::SLOT;
       };
       __syncwarp();
-      if (whole_pages) look_up(begin);
+      look_up(begin);
+      // the query's elements are asked for ahead of the tiles (behind them they
+      // came 3 us later where all SMs begin at once)
+      constexpr int N = S8 ? 16 : 8;  // elements of a piece
+      Piece<QT, N> q_raw[NT][F::PK];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool live = nt * 8 + g < heads;
+        const QT* src = static_cast<const QT*>(a.q.p) + b * a.q.token + (int64_t)(h0 + nt * 8 + g) * a.q.head;
+#pragma unroll
+        for (int j = 0; j < F::PK; ++j) {
+          const int d = (j * 4 + tig) * N;
+          if (!live || d >= D) q_raw[nt][j].clear();
+          else if (a.aligned_q) q_raw[nt][j].load(src + d);
+          else q_raw[nt][j].load_any(src + d);
+        }
+      }
 #pragma unroll 1
       for (int i = 0; i < F::AHEAD; ++i) {
         send_keys(begin + i, 2 * i * F::SLOT);
@@ -544,20 +575,9 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       float base[NT][2];    // where their sums start: what the codes' 128 add up to, subtracted
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        constexpr int N = S8 ? 16 : 8;  // elements of a piece
         float v[F::PK][N];
-        const bool live = nt * 8 + g < heads;
-        const QT* src = static_cast<const QT*>(a.q.p) + b * a.q.token + (int64_t)(h0 + nt * 8 + g) * a.q.head;
 #pragma unroll
-        for (int j = 0; j < F::PK; ++j) {
-          const int d = (j * 4 + tig) * N;
-          if (live && d < D) {
-            load_row<QT, N>(src + d, a.aligned_q, v[j]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[j][i] = 0.0f;
-          }
-        }
+        for (int j = 0; j < F::PK; ++j) q_raw[nt][j].to_float(v[j]);
         float f = a.scale * kLog2e;
         if constexpr (S8) {
           // by a power of two to [1, 2): fp16 then holds every element to
