@@ -273,9 +273,9 @@ struct Form {
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
   // warps: 12 of 168 registers where they suffice, else 8 or 4 of 255 (at
   // 128 registers 16 warps spent a fifth more instructions on addresses)
-  static constexpr int W = (S8 || DP == 64) && DP <= 128 && NT == 1 ? 12 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  static constexpr int W = (S8 || DP == 64) && DP <= 128 && NT == 1 ? 16 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
   static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
-  static constexpr int AHEAD = ROOM >= 7 ? 3 : ROOM >= 5 ? 2 : 1;  // tiles in flight
+  static constexpr int AHEAD = ROOM >= 5 ? 2 : 1;  // tiles in flight
   static constexpr int SLOTS = 2 * AHEAD + 1;
   static constexpr int WARP_BYTES = SLOTS * SLOT + Q_BYTES;
   static constexpr int SMEM = W * WARP_BYTES + (kMaxSequences + 1) * 4 + 12 + W * (8 * NT * 8 + 16);
