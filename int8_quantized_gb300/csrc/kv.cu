@@ -219,6 +219,13 @@ __device__ __forceinline__ void turn(float& x1, float& x2, float cs, float sn) {
   x1 = y1;
 }
 
+// The larger magnitude, or NaN where either is one.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 // rint of the quotients y / s, |y| <= 127 s, as low bytes.  With r = fl(1 /
 // s), the products y r (1 - 2^-20) and y r (1 + 2^-20) enclose the rounded
 // quotient; one fma with 1.5 2^23 rounds each to an integer (its low bits).
@@ -226,11 +233,14 @@ __device__ __forceinline__ void turn(float& x1, float& x2, float cs, float sn) {
 // not, or 1 / s is not a normal number, the eight quotients are formed.
 __device__ __forceinline__ void quotient_codes(const float (&y)[8], float s, uint32_t (&code)[8]) {
   const float r = quot_rcp(s), hi = __fmul_rn(r, 1.0f + 0x1p-20f), lo = __fmul_rn(r, 1.0f - 0x1p-20f);
+  const float2 magic = make_float2(12582912.0f, 12582912.0f);
   uint32_t differ = r != r;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    code[j] = __float_as_uint(__fmaf_rn(y[j], hi, 12582912.0f));
-    differ |= code[j] ^ __float_as_uint(__fmaf_rn(y[j], lo, 12582912.0f));
+  for (int j = 0; j < 8; j += 2) {
+    const float2 v = make_float2(y[j], y[j + 1]);
+    const float2 h = fma2_rn(v, make_float2(hi, hi), magic), l = fma2_rn(v, make_float2(lo, lo), magic);
+    code[j] = __float_as_uint(h.x), code[j + 1] = __float_as_uint(h.y);
+    differ |= (code[j] ^ __float_as_uint(l.x)) | (code[j + 1] ^ __float_as_uint(l.y));
   }
   if (differ) {
 #pragma unroll
@@ -279,7 +289,7 @@ template <class T, bool S8, int L>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
                     Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, uint32_t* status) {
-  constexpr int G = kUnitThreads / L, NQ = 4, NK = 2;  // rows of q, and of k and v, that a lane has in flight
+  constexpr int G = kUnitThreads / L, NQ = 4;  // rows of q that a lane has in flight, beside one of k and one of v
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
   const int64_t t = splits == 1 ? blockIdx.x : blockIdx.x / splits;
@@ -291,7 +301,7 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   const T* q_row = static_cast<const T*>(q.p) + t * q.token;
   const T* k_row = static_cast<const T*>(k.p) + t * k.token;
   const T* v_row = static_cast<const T*>(v.p) + t * v.token;
-  Four<T> xq[NQ][2], xk[NK][2];
+  Four<T> xq[NQ][2], xk[2], xv[2];
   auto send_q = [&](int head) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -300,18 +310,14 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
         xq[n][0] = load4(src + h1), xq[n][1] = load4(src + h2);
       }
   };
-  auto send_k = [&](int row) {  // keys' heads, then values'
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const int j = row + n * step;
-      if (j < 2 * c.heads && in_row) {
-        const bool is_v = j >= c.heads;
-        const T* src = is_v ? v_row + (j - c.heads) * v.head : k_row + j * k.head;
-        xk[n][0] = load4(src + (is_v ? e1 : h1)), xk[n][1] = load4(src + (is_v ? e2 : h2));
-      }
+  auto send_kv = [&](int head) {
+    if (head < c.heads && in_row) {
+      const T *src = k_row + head * k.head, *from = v_row + head * v.head;
+      xk[0] = load4(src + h1), xk[1] = load4(src + h2);
+      xv[0] = load4(from + e1), xv[1] = load4(from + e2);
     }
   };
-  send_k(slot);
+  send_kv(slot);
   send_q(slot);
   const int b = seq[t], i = index[t];
   const uint32_t axis = r.axis[u >> 2 & 7] >> ((u & 3) * 8) & 0xffu;  // two bits a pair
@@ -373,42 +379,38 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   }
   const int64_t at = kv::row_at(c, page, 0, off), scale_at = kv::scale_at(c, page, 0, off);
   const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
-  for (int row = slot; row < 2 * c.heads;) {
+  auto put = [&](void* pool, float* scale, const float (&y)[8], int p1, int p2, int64_t dst, int64_t sc) {
+    if constexpr (!S8) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(pool) + dst;
+      if (in_row) store4(o + p1, y), store4(o + p2, y + 4);
+    } else {
+      float most = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const int j = row + n * step;
-      if (j >= 2 * c.heads) break;  // (the same for the L lanes of a row)
-      const bool is_v = j >= c.heads;
-      const int head = is_v ? j - c.heads : j;
-      const int p1 = is_v ? e1 : h1, p2 = is_v ? e2 : h2;
-      const int64_t dst = at + head * c.head_stride, sc = scale_at + head * c.s_head;
-      float y[8] = {};
-      if (in_row) turned(xk[n], y, turns && !is_v);
-      if constexpr (!S8) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) + dst;
-        if (in_row) store4(o + p1, y), store4(o + p2, y + 4);
-      } else {
-        // the largest magnitude as its bit pattern: a NaN is above infinity
-        uint32_t most = 0;
+      for (int e = 0; e < 8; ++e) most = larger(most, y[e]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(fabsf(y[e])));
-#pragma unroll
-        for (int m = 1; m < L; m <<= 1) most = max(most, __shfl_xor_sync(lanes, most, m));
-        float s = __fdiv_rn(__uint_as_float(most), 127.0f);
-        if (s == 0.0f) s = 1.0f;
-        if (in_row) {
-          int8_t* o = static_cast<int8_t*>(is_v ? c.v : c.k) + dst;
-          uint32_t code[8];
-          quotient_codes(y, s, code);
-          *reinterpret_cast<uint32_t*>(o + p1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
-          *reinterpret_cast<uint32_t*>(o + p2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
-        }
-        if (u == 0) (is_v ? c.vs : c.ks)[sc] = s;
+      for (int m = 1; m < L; m <<= 1) most = larger(most, __shfl_xor_sync(lanes, most, m));
+      float s = __fdiv_rn(most, 127.0f);
+      if (s == 0.0f) s = 1.0f;
+      if (in_row) {
+        int8_t* o = static_cast<int8_t*>(pool) + dst;
+        uint32_t code[8];
+        quotient_codes(y, s, code);
+        *reinterpret_cast<uint32_t*>(o + p1) = pack_low_bytes(code[0], code[1], code[2], code[3]);
+        *reinterpret_cast<uint32_t*>(o + p2) = pack_low_bytes(code[4], code[5], code[6], code[7]);
       }
-      if (!is_v && c.score && u == 0) c.score[sc] = 0.0f;
+      if (u == 0) scale[sc] = s;
     }
-    row += NK * step;
-    send_k(row);
+  };
+  for (int head = slot; head < c.heads;) {  // (the same for the L lanes of a row)
+    const int64_t dst = at + head * c.head_stride, sc = scale_at + head * c.s_head;
+    float y[8] = {};
+    if (in_row) turned(xk, y, turns);
+    put(c.k, c.ks, y, h1, h2, dst, sc);
+    if (in_row) turned(xv, y, false);
+    put(c.v, c.vs, y, e1, e2, dst, sc);
+    if (c.score && u == 0) c.score[sc] = 0.0f;
+    head += step;
+    send_kv(head);
   }
 }
 
@@ -591,7 +593,7 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
       return with_lanes(c.dim, [&](auto lanes) -> int {
         constexpr int L = decltype(lanes)::value;
         // few tokens: their rows over as many CTAs as two for each SM, each with a row per L lanes at least
-        const int64_t most = ceil_div(std::max<int64_t>(q_heads, 2 * c.heads), kUnitThreads / L);
+        const int64_t most = ceil_div(std::max<int64_t>(q_heads, c.heads), kUnitThreads / L);
         const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / tokens));
         return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), kUnitThreads, 0, 1, s,
                           "kv_append", c, tab, seq, index, splits, rq, ro, rk, rv, r, status);

@@ -111,11 +111,13 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
   int x = w * q + min(w, longer);
   const int x_end = x + q + (w < longer);
   if (x >= x_end) return;
+  // the last sequence that begins at or before x, by 32 of them at a time
+  // (a binary search would read the line eleven times in turn)
   int b = 0;
-  for (int lo = 0, hi = B; lo < hi;) {
-    const int mid = (lo + hi) / 2;
-    if (a.line[mid] / a.chunks <= x) b = mid, lo = mid + 1;
-    else hi = mid;
+  for (int step = B <= 32 ? 1 : B <= 1024 ? 32 : 1024; step; step /= 32) {
+    const int i = b + lane * step;
+    const bool before = i < B && a.line[i] / a.chunks <= x;
+    b += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
   }
   for (; x < x_end; ++b) {
     const int at = a.line[b] / a.chunks, b_end = min(a.line[b + 1] / a.chunks, x_end);
@@ -305,7 +307,7 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     }
     if (accumulate) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 8, 256, 0, 1, s,
+      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 16, 256, 0, 1, s,
                         "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }
