@@ -282,9 +282,11 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
 // 4u on, or 8u and 8u + 4 on.  A CTA has one token (or one of `splits` shares
 // of its rows, for calls of few tokens); a lane keeps its unit, so its four
 // cosines and sines serve all heads, and its first rows are sent for before
-// the token's place and positions are known.  128 threads a token: with 256
-// half of the instructions were what a thread does once.
-constexpr int kUnitThreads = 128;
+// the token's place and positions are known.  64 threads a token: what a
+// thread does once is then a tenth of its work (16384 tokens of 48 rows of
+// 128: 83 us, against 92 with 128 threads and 154 with 256).  The sums of two
+// products are scalar: the compiler fuses a paired sum with its products.
+constexpr int kUnitThreads = 64;
 template <class T, bool S8, int L>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
