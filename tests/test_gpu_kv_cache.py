@@ -110,9 +110,9 @@ def reference_attention(cache, table, lens, qx, window, scale):
 
 
 def check_attention(dev, lens, Hq, H, D, page, qtype, cache, window=0, accumulate=False, order="phtd", seed=0,
-                    scale=None, strided=False, q_gain=2.0, change=None):
+                    scale=None, strided=False, q_gain=2.0, change=None, extra=0):
     g = gen(seed)
-    table, pages, _ = make_table(g, dev, lens, page)
+    table, pages, _ = make_table(g, dev, lens, page, extra=extra)
     c = make_cache(g, dev, pages, H, page, D, cache, order)
     if change:
         change(c, table)
@@ -196,6 +196,40 @@ def test_attention_window(dev, window, cache):
 def test_attention_orders_and_strides(dev, order, cache):
     check_attention(dev, [70, 200], 6, 3, 96, 16, "bf16", cache, order=order, accumulate=True, strided=True)
     check_attention(dev, [70, 200], 6, 3, 96, 20, "f32", cache, order=order, strided=True)
+
+
+# Tables with room for long sequences: rows are then cut where the line says,
+# not kept whole by a CTA.
+CUT = [1, 0, 37, 300, 2000, 16, 700, 5]
+
+
+@pytest.mark.parametrize("cache", ["s8", "bf16"])
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 144, 256])
+@pytest.mark.parametrize("G", [1, 5, 16])
+def test_attention_cut_rows(dev, D, G, qtype, cache):
+    check_attention(dev, CUT, 3 * G, 3, D, 16, qtype, cache, seed=D + G, accumulate=G != 5, extra=2000)
+
+
+@pytest.mark.parametrize("cache,qtype", [("s8", "bf16"), ("bf16", "f32"), ("s8", "f32")])
+@pytest.mark.parametrize("window", [0, 17, 250])
+@pytest.mark.parametrize("page", [5, 24, 64])
+def test_attention_cut_rows_pages_and_windows(dev, page, window, cache, qtype):
+    check_attention(dev, CUT, 20, 1, 96, page, qtype, cache, window=window, seed=page, accumulate=True, extra=2000,
+                    order="pthd", strided=True)
+
+
+@pytest.mark.parametrize("lens", [[4000], [0, 0, 0], [1], [65] * 40, [5000, 1, 1, 1], [16 * 9] * 7])
+def test_attention_cut_rows_lengths(dev, lens):
+    check_attention(dev, lens, 8, 2, 128, 16, "bf16", "s8", accumulate=True, extra=2000)
+    check_attention(dev, lens, 2, 2, 64, 16, "bf16", "bf16", extra=2000)
+
+
+def test_attention_cut_rows_over_many_sequences(dev):
+    r = np.random.default_rng(5)
+    check_attention(dev, [int(x) for x in r.integers(0, 200, 700)], 4, 2, 64, 16, "bf16", "s8", accumulate=True,
+                    extra=300)
+    check_attention(dev, [int(x) for x in r.integers(0, 20, 2500)], 2, 1, 16, 4, "f32", "bf16", extra=300)
 
 
 @pytest.mark.parametrize("cache,qtype", [("s8", "bf16"), ("bf16", "f32")])

@@ -177,3 +177,11 @@ def test_binding_refuses_what_the_library_cannot_see():
         _i32(t, "seq", 1)
     with pytest.raises(TypeError, match="CUDA"):
         _rows(k, "q", 2, 2, 64, torch.int8)
+
+
+def test_attention_refuses_lines_past_32_bits(lib):
+    """A sequence whose row of the table times the heads cannot be cut by 32-bit positions."""
+    huge = dict(c=cache(kv_heads=60000, page_size=1 << 20, page_stride=1 << 50, head_stride=1 << 30),
+                t=table(max_pages=2000, stride=2000), q_heads=60000)
+    assert attend(lib, **huge) == -2
+    assert b"out of range" in lib.i8q_last_error()
