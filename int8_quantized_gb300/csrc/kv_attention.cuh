@@ -271,9 +271,11 @@ struct Form {
   static constexpr int Q_WORDS = NQ * NT * KS * 2;
   static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
-  // warps: 12 of 168 registers where they suffice, else 8 or 4 of 255 (at
-  // 128 registers 16 warps spent a fifth more instructions on addresses)
-  static constexpr int W = (S8 || DP == 64) && DP <= 128 && NT == 1 ? 16 : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  // Warps: 16 of 128 registers where they suffice (1 x 131072 tokens: 60 us,
+  // as with 12 of 168, and 64 x 8192: 205 us against 211), 12, else 8 or 4 of
+  // 255.
+  static constexpr int W = NT == 1 && S8 && DP <= 128 && !WIDE ? 16 : NT == 1 && (S8 ? DP <= 128 : DP == 64) ? 12
+                           : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
   static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
   static constexpr int AHEAD = ROOM >= 5 ? 2 : 1;  // tiles in flight
   static constexpr int SLOTS = 2 * AHEAD + 1;
@@ -643,9 +645,10 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         __syncwarp();
         const unsigned char* slot = ring + use;
         advance();
-        // bf16 keys may be infinite, and infinity times a later part of q (0, or
-        // of the other sign) is NaN: the first part's sum is kept apart
-        constexpr bool APART = !S8 && F::NQ > 1;
+        // fp32 queries: the products with q's first part are added up outside the
+        // tensor pipe, whose sums are cut rather than rounded, and apart from the
+        // others: bf16 keys may be infinite, and infinity times a later part (0, or
+        // of the other sign) is NaN
         float s[NT][4], rest[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -679,11 +682,17 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
                 uint2 bq;
                 if constexpr (F::Q_REG) bq = q_reg[at_q];
                 else bq = q_smem[at_q * 32];
-                mma<S8>(APART && p ? rest[nt] : s[nt], a0, a1, a2, a3, bq.x, bq.y);
+                if (F::WIDE && p == 0) {
+                  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma<S8>(x, a0, a1, a2, a3, bq.x, bq.y);
+                  s[nt][0] += x[0], s[nt][1] += x[1], s[nt][2] += x[2], s[nt][3] += x[3];
+                } else {
+                  mma<S8>(F::WIDE ? rest[nt] : s[nt], a0, a1, a2, a3, bq.x, bq.y);
+                }
               }
           }
         }
-        if constexpr (APART) {
+        if constexpr (F::WIDE) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -767,9 +776,18 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         }
         auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (F::WIDE) {  // a tile's sum by itself, then rounded to the whole
+              float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int p = 0; p < F::NP; ++p) mma<false>(o[mt][nt], a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
+              for (int p = F::NP - 1; p >= 0; --p) mma<false>(x, a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[mt][nt][j] += x[j];
+            } else {
+#pragma unroll
+              for (int p = 0; p < F::NP; ++p) mma<false>(o[mt][nt], a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
+            }
+          }
         };
 #pragma unroll
         for (int j = 0; j < F::PV; ++j) {
