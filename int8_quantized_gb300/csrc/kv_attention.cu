@@ -105,12 +105,14 @@ template <int V>
 __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
   const Cache& c = a.c;
   const int lane = threadIdx.x & 31, B = a.tab.sequences;
-  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_previous_kernel();
-  const int n = a.line[B] / a.chunks, q = n / warps, longer = n - q * warps;
+  // parts of 16 tiles at least; the other warps have none
+  const int n = a.line[B] / a.chunks, parts = max(1, min((int)gridDim.x * 8, n / 16));
+  if (w >= parts) return;
+  const int q = n / parts, longer = n - q * parts;
   int x = w * q + min(w, longer);
   const int x_end = x + q + (w < longer);
-  if (x >= x_end) return;
   // the last sequence that begins at or before x, by 32 of them at a time
   // (a binary search would read the line eleven times in turn)
   int b = 0;
