@@ -265,6 +265,7 @@ struct Form {
   static constexpr int PK = ROW / 64;          // 16-byte pieces of a key row per lane
   static constexpr int VB = ROW == 64 ? 8 : 16;
   static constexpr int PV = ROW / 8 / VB;      // pieces of a value row per lane
+  static constexpr int E = (DP + 127) / 128;   // four elements of a head's result a lane, so many times
   static constexpr int CR = ROW / 16;          // pieces of a row
   static constexpr int CT = ROW / 32;          // pieces of half a tile that a lane copies
   static constexpr int SLOT = 16 * ROW + 144;  // half a tile: pieces; keys: 32 scales, the mask of the tokens
@@ -328,6 +329,16 @@ __device__ __forceinline__ void finish_row(const Args& a, int b, int h, int lane
   }
 }
 
+// The same of a part of a row, to the workspace.
+template <int DP>
+__device__ __forceinline__ void put_part(const Args& a, int64_t part, int lane, float m, float l,
+                                         const float4 (&o)[(DP + 127) / 128]) {
+  if (lane == 0) a.part_stats[part] = make_float2(m, l);
+#pragma unroll
+  for (int e = 0; e < (DP + 127) / 128; ++e)
+    if (e * 128 + lane * 4 < DP) *reinterpret_cast<float4*>(a.part_out + part * DP + e * 128 + lane * 4) = o[e];
+}
+
 // WHOLE: rows are not cut (warps_per_row), else they follow the line.
 template <class F, bool WHOLE>
 __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_constant__ Args a) {
@@ -364,6 +375,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       if (lane == 31) sums[warp] = x;
       __syncthreads();
       int before = 0, all = 0;
+#pragma unroll 4
       for (int w = 0; w < F::W; ++w) {
         const int u = sums[w];
         before += w < warp ? u : 0;
@@ -823,8 +835,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         __syncwarp();
       }
 
-      // ---- the row, or this part of it ----
+      // ---- the row, or this part of it, into the ring: a warp's stores of
+      // fragments to the workspace or the output touch 32 sectors each (16 warps'
+      // took 4 us).  Four elements at a time are moved by the head's number, so
+      // that the lanes of a quad of heads do not all write one bank. ----
       constexpr float unit = S8 ? 64.0f : 1.0f;  // of codes_bf16
+      float* const result = reinterpret_cast<float*>(ring);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -834,38 +850,29 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
           const int hh = nt * 8 + 2 * tig + j;
-          if (hh >= heads) continue;
-          if (starts && ends) {
-            const int64_t h = (int64_t)b * a.q_heads + h0 + hh;
-            const bool none = sum == 0.0f;
-            const float z = none ? -INFINITY : m[nt][j] + log2f(sum);
-            if (g == 0) {
-              if (a.lse) a.lse[h] = z * kLn2;
-              if (a.stats) a.stats[h] = z;
-            }
-            QT* out = static_cast<QT*>(a.out.p) + b * a.out.token + (int64_t)(h0 + hh) * a.out.head;
-            const float inv = none ? 0.0f : unit / sum;
+          if (g == 0) open_stats[warp * 8 * NT + hh] = make_float2(m[nt][j], sum);
 #pragma unroll
-            for (int mt = 0; mt < F::MT; ++mt) {
-              const int d = F::row_element(mt, g);
-              if (d < D) store_pair(out + d, o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv, a.aligned_out);
-            }
-          } else {
-            // a part that ends a row goes to the workspace; one that leaves it open is
-            // this warp's last: into its ring, to be joined with its neighbours'
-            const int64_t p = (int64_t)w * 2 * (8 * NT) + hh;
-            if (g == 0) (ends ? a.part_stats[p] : open_stats[warp * 8 * NT + hh]) = make_float2(m[nt][j], sum);
-            // (in the ring four elements at a time are moved by the head's number, so that
-            // the lanes of a quad of heads do not all write one bank)
-            float* out = ends ? a.part_out + p * F::DP : reinterpret_cast<float*>(ring) + hh * F::DP;
-            const int moved = ends ? 0 : tig * 4;
-#pragma unroll
-            for (int mt = 0; mt < F::MT; ++mt)
-              *reinterpret_cast<float2*>(out + (F::row_element(mt, g) ^ moved)) =
-                  make_float2(o[mt][nt][j] * unit, o[mt][nt][2 + j] * unit);
-          }
+          for (int mt = 0; mt < F::MT; ++mt)
+            *reinterpret_cast<float2*>(result + hh * F::DP + (F::row_element(mt, g) ^ tig * 4)) =
+                make_float2(o[mt][nt][j] * unit, o[mt][nt][2 + j] * unit);
         }
-      if (lane == 0 && !ends) open_row[warp] = b * R + row, open_head[warp] = starts;
+      __syncwarp();
+      if (ends) {
+#pragma unroll 1
+        for (int hh = 0; hh < heads; ++hh) {
+          const float2 st = open_stats[warp * 8 * NT + hh];
+          float4 acc[F::E];
+#pragma unroll
+          for (int e = 0; e < F::E; ++e)
+            if (e * 128 + lane * 4 < F::DP)
+              acc[e] = *reinterpret_cast<const float4*>(result + hh * F::DP + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
+          if (starts) finish_row<QT, F::DP>(a, b, h0 + hh, lane, st.x, st.y, acc);
+          else put_part<F::DP>(a, ((int64_t)w * 2) * (8 * NT) + hh, lane, st.x, st.y, acc);
+        }
+        __syncwarp();
+      } else if (lane == 0) {  // this warp's last: to be joined with its neighbours' there
+        open_row[warp] = b * R + row, open_head[warp] = starts;
+      }
     }
   }
 
@@ -877,20 +884,23 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   while (from > 0 && open_row[from - 1] == mine) --from;
   while (to + 1 < F::W && open_row[to + 1] == mine) ++to;
   const int heads = min(8 * NT, a.group - mine % R % a.chunks * (8 * NT));
+#pragma unroll 1
   for (int hh = warp - from; hh < heads; hh += to - from + 1) {
     float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
     for (int i = from; i <= to; ++i) top = fmaxf(top, open_stats[i * 8 * NT + hh].x);
     const float ref = top == -INFINITY ? 0.0f : top;
-    float4 acc[(F::DP + 127) / 128];
+    float4 acc[F::E];
 #pragma unroll
-    for (int e = 0; e < (F::DP + 127) / 128; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < F::E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
     for (int i = from; i <= to; ++i) {
       const float2 st = open_stats[i * 8 * NT + hh];
       const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
       sum = fmaf(st.y, f, sum);
       const float* part = reinterpret_cast<const float*>(smem + i * F::WARP_BYTES) + hh * F::DP;
 #pragma unroll
-      for (int e = 0; e < (F::DP + 127) / 128; ++e)
+      for (int e = 0; e < F::E; ++e)
         if (e * 128 + lane * 4 < F::DP) {
           const float4 v = *reinterpret_cast<const float4*>(part + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
           acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
@@ -898,16 +908,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         }
     }
     if constexpr (WHOLE) {  // that was the row
-      const int b_row = mine / R, h = mine % R / a.chunks * a.group + mine % R % a.chunks * (8 * NT) + hh;
-      finish_row<QT, F::DP>(a, b_row, h, lane, top, sum, acc);
-      continue;
+      const int in_b = mine % R;
+      finish_row<QT, F::DP>(a, mine / R, in_b / a.chunks * a.group + in_b % a.chunks * (8 * NT) + hh, lane, top, sum, acc);
+    } else {
+      put_part<F::DP>(a, ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh, lane, top,
+                      sum, acc);
     }
-    const int64_t p = ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh;
-    if (lane == 0) a.part_stats[p] = make_float2(top, sum);
-#pragma unroll
-    for (int e = 0; e < (F::DP + 127) / 128; ++e)
-      if (e * 128 + lane * 4 < F::DP)
-        *reinterpret_cast<float4*>(a.part_out + p * F::DP + e * 128 + lane * 4) = acc[e];
   }
 }
 
