@@ -287,18 +287,18 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Args 
   if (e >= c.dim * BYTES) return;
   for (int r0 = group; r0 < 2 * kRows; r0 += 4 * groups) {
     uint4 x[4];
+    char* dst[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + i * groups;
-      if (r < 2 * kRows && from[r % kRows] >= 0)
-        x[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(r < kRows ? c.k : c.v) + from[r % kRows] + e));
+      const int64_t src = r < 2 * kRows ? from[r % kRows] : -1;
+      char* const pool = static_cast<char*>(r < kRows ? c.k : c.v);
+      dst[i] = src < 0 ? nullptr : pool + to[r % kRows] + e;
+      if (src >= 0) x[i] = __ldcs(reinterpret_cast<const uint4*>(pool + src + e));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + i * groups;
-      if (r < 2 * kRows && from[r % kRows] >= 0)
-        *reinterpret_cast<uint4*>(static_cast<char*>(r < kRows ? c.k : c.v) + to[r % kRows] + e) = x[i];
-    }
+    for (int i = 0; i < 4; ++i)
+      if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = x[i];
   }
 }
 
