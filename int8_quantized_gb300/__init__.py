@@ -420,14 +420,18 @@ class KVCache:
         if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
             raise ValueError("an int8 cache needs k_scale and v_scale, a bfloat16 cache has none")
         self.k, self.v, self.k_scale, self.v_scale, self.score = k, v, k_scale, v_scale, score
+        self.shape = tuple(k.shape)
         ptr = [None if t is None else t.data_ptr() for t in (k, v, k_scale, v_scale, score)]
         scale_strides = per[0][0].stride() if per else (0, 0, 0)
         self._struct = _lib.KVCacheStruct(*ptr, _TORCH_TYPE[k.dtype], *k.shape, *k.stride()[:3], *scale_strides)
         self._ref = ctypes.byref(self._struct)
 
 
+_Tensor, _I32, _F32 = torch.Tensor, torch.int32, torch.float32
+
+
 def _page_table(t, name="page_table"):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2:
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or not t.is_cuda or t.dim() != 2:
         raise TypeError(f"{name} must be an int32 CUDA tensor of 2 axes")
     (rows, columns), (stride, one) = t.shape, t.stride()
     if one != 1 and columns > 1:
@@ -435,24 +439,43 @@ def _page_table(t, name="page_table"):
     return _lib.PageTableStruct(t.data_ptr(), rows, columns, stride)
 
 
-def _rows(t, name, n, heads, dim, dtype):
-    """Pointer and (token, head) strides of a [n, heads, dim] CUDA tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+def _rows(t, name, shape, dtype):
+    """Pointer and (token, head) strides of a CUDA tensor of a [n, heads, dim] shape."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
-    if t.shape != (n, heads, dim):
-        raise ValueError(f"{name} must be [{n}, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
     token, head, one = t.stride()
-    if one != 1 and dim > 1:
+    if one != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
     return t.data_ptr(), token, head
 
 
 def _i32(t, name, n):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries")
     return t.data_ptr()
+
+
+def _rotary(positions, cos, sin, pair_axis, interleaved, tokens):
+    if not isinstance(positions, _Tensor) or positions.dtype is not _I32 or not positions.is_cuda:
+        raise TypeError("positions must be an int32 CUDA tensor")
+    if not (isinstance(cos, _Tensor) and isinstance(sin, _Tensor) and cos.dtype is _F32 and sin.dtype is _F32 and
+            cos.is_cuda and sin.is_cuda and cos.is_contiguous() and sin.is_contiguous()):
+        raise TypeError("cos and sin must be contiguous float32 CUDA tensors")
+    shape, strides = positions.shape, positions.stride()
+    if len(shape) not in (1, 2) or shape[-1] != tokens or (strides[-1] != 1 and tokens > 1):
+        raise ValueError("positions must be [axes, tokens] or [tokens] with contiguous rows")
+    table = cos.shape
+    if len(table) != 2 or table != sin.shape:
+        raise ValueError("cos and sin must both be [rows, pairs]")
+    if pair_axis is not None and len(pair_axis) != table[1]:
+        raise ValueError("pair_axis must have an entry for each pair")
+    axes, stride = (shape[0], strides[0]) if len(shape) == 2 else (1, 0)
+    return _lib.RotaryStruct(positions.data_ptr(), stride, axes, cos.data_ptr(), sin.data_ptr(), table[0], table[1],
+                             None if pair_axis is None else bytes(pair_axis), bool(interleaved))
 
 
 def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions=None, cos=None, sin=None,
@@ -465,34 +488,20 @@ def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions
     q and k are turned first; pair_axis: the axis of each pair (default 0);
     interleaved: pairs are (2j, 2j+1) instead of (j, j + pairs).  See
     i8q_kv_append.  Returns q_out."""
-    T, H, D = k.shape
-    rot = None
     if (cos is None) != (sin is None) or (cos is None) != (positions is None):
         raise ValueError("positions, cos and sin come together")
+    tokens, dtype = k.shape[0], k.dtype
+    _, H, _, D = cache.shape
+    rot = None
     if cos is not None:
-        if not (positions.is_cuda and positions.dtype == torch.int32) or positions.dim() > 2:
-            raise TypeError("positions must be an int32 CUDA tensor of 1 or 2 axes")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        if positions.shape[-1] != T or (positions.stride(-1) != 1 and T > 1):
-            raise ValueError("positions must be [axes, tokens] with contiguous rows")
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous float32 CUDA tensor")
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must both be [rows, pairs]")
-        if pair_axis is not None and len(pair_axis) != cos.shape[1]:
-            raise ValueError("pair_axis must have an entry for each pair")
-        rot = ctypes.byref(_lib.RotaryStruct(positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0,
-                                             axes, cos.data_ptr(), sin.data_ptr(), *cos.shape,
-                                             None if pair_axis is None else bytes(pair_axis), int(bool(interleaved))))
-    shape = cache.k.shape
+        rot = ctypes.byref(_rotary(positions, cos, sin, pair_axis, interleaved, tokens))
     qs, qo, heads = (None, 0, 0), (None, 0, 0), 0
     if q is not None:
         heads = q.shape[1]
-        qs, qo = _rows(q, "q", T, heads, shape[3], k.dtype), _rows(q_out, "q_out", T, heads, shape[3], k.dtype)
-    check(_L().i8q_kv_append(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", T),
-                             _i32(index, "index", T), T, _float_type(k), *_rows(k, "k", T, shape[1], shape[3], k.dtype),
-                             *_rows(v, "v", T, shape[1], shape[3], k.dtype), *qs, heads, *qo, rot, _stream(stream)),
+        qs, qo = _rows(q, "q", (tokens, heads, D), dtype), _rows(q_out, "q_out", (tokens, heads, D), dtype)
+    check(_L().i8q_kv_append(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", tokens),
+                             _i32(index, "index", tokens), tokens, _float_type(k), *_rows(k, "k", (tokens, H, D), dtype),
+                             *_rows(v, "v", (tokens, H, D), dtype), *qs, heads, *qo, rot, _stream(stream)),
           "kv_append")
     return q_out
 
@@ -506,11 +515,11 @@ def _float_type(t):
 def kv_gather(cache, page_table, seq, index, k_out, v_out, stream=None):
     """Read tokens back: k_out, v_out [tokens, kv_heads, head_dim] (fp32 or
     bf16) receive token index[t] of sequence seq[t] (i8q_kv_gather)."""
-    T, shape = k_out.shape[0], cache.k.shape
+    T, dtype = k_out.shape[0], k_out.dtype
+    shape = (T, cache.shape[1], cache.shape[3])
     check(_L().i8q_kv_gather(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", T),
-                             _i32(index, "index", T), T, _float_type(k_out),
-                             *_rows(k_out, "k_out", T, shape[1], shape[3], k_out.dtype),
-                             *_rows(v_out, "v_out", T, shape[1], shape[3], k_out.dtype), _stream(stream)), "kv_gather")
+                             _i32(index, "index", T), T, _float_type(k_out), *_rows(k_out, "k_out", shape, dtype),
+                             *_rows(v_out, "v_out", shape, dtype), _stream(stream)), "kv_gather")
     return k_out, v_out
 
 
@@ -530,7 +539,7 @@ def paged_attention(cache, page_table, lengths, q, out, lse=None, softmax_scale=
     1 / sqrt(head_dim); window: the last `window` tokens only (0: all);
     accumulate: add each token's weight to cache.score.  See
     i8q_paged_attention.  Returns out."""
-    shape = cache.k.shape
+    D, dtype = cache.shape[3], q.dtype
     B, heads = page_table.shape[0], q.shape[1]
     if workspace is None:
         workspace = torch.empty(paged_attention_workspace_size(cache, page_table, heads, accumulate),
@@ -540,9 +549,9 @@ def paged_attention(cache, page_table, lengths, q, out, lse=None, softmax_scale=
     if lse is not None and lse.shape != (B, heads):
         raise ValueError(f"lse must be [{B}, {heads}]")
     check(_L().i8q_paged_attention(cache._ref, ctypes.byref(_page_table(page_table)), _i32(lengths, "lengths", B),
-                                   _float_type(q), *_rows(q, "q", B, heads, shape[3], q.dtype), heads,
-                                   *_rows(out, "out", B, heads, shape[3], q.dtype), _dev(lse, "lse", torch.float32),
-                                   shape[3] ** -0.5 if softmax_scale is None else softmax_scale, window,
+                                   _float_type(q), *_rows(q, "q", (B, heads, D), dtype), heads,
+                                   *_rows(out, "out", (B, heads, D), dtype), _dev(lse, "lse", torch.float32),
+                                   D ** -0.5 if softmax_scale is None else softmax_scale, window,
                                    int(bool(accumulate)), _dev(workspace, "workspace"),
                                    workspace.numel() * workspace.element_size(), _stream(stream)), "paged_attention")
     return out
@@ -554,7 +563,7 @@ def kv_evict(cache, page_table, lengths, new_table, kept, new_lengths=None, sink
     copy them in order to the pages of new_table (i8q_kv_evict).  kept int32
     [sequences, kv_heads, budget] receives their indices (-1 past the end),
     new_lengths int32 [sequences] the new lengths.  Returns kept."""
-    B, H = page_table.shape[0], cache.k.shape[1]
+    B, H = page_table.shape[0], cache.shape[1]
     if kept.dim() != 3 or kept.shape[:2] != (B, H):
         raise ValueError(f"kept must be [{B}, {H}, budget]")
     check(_L().i8q_kv_evict(cache._ref, ctypes.byref(_page_table(page_table)), _i32(lengths, "lengths", B),

@@ -176,7 +176,7 @@ def test_binding_refuses_what_the_library_cannot_see():
     with pytest.raises(TypeError, match="int32"):
         _i32(t, "seq", 1)
     with pytest.raises(TypeError, match="CUDA"):
-        _rows(k, "q", 2, 2, 64, torch.int8)
+        _rows(k, "q", (2, 2, 64), torch.int8)
 
 
 def test_attention_refuses_lines_past_32_bits(lib):
