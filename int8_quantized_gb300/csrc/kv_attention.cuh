@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             for (int r = 0; r < F::CT; ++r, src += a.step_bytes) copy16(dst + F::copy_place(copy_at, r), src, 16);
           }
         } else {  // some pieces are zeros
-#pragma unroll 1
+#pragma unroll (F::CT <= 4 ? F::CT : 1)
           for (int r = 0; r < F::CT; ++r) {
             const int t = (r * 32 + lane) / F::CR, p = lane % F::CR;
             const int64_t row = whole_pages ? at + t * a.token_bytes : __shfl_sync(0xffffffffu, at, t);
