@@ -291,7 +291,7 @@ template <class T, bool S8, int L>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
                     Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, uint32_t* status) {
-  constexpr int G = kUnitThreads / L, NQ = 4;  // rows of q that a lane has in flight, beside one of k and one of v
+  constexpr int G = kUnitThreads / L, NQ = 2;  // rows of q that a lane has in flight, beside one of k and one of v
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
   const int64_t t = splits == 1 ? blockIdx.x : blockIdx.x / splits;
