@@ -626,7 +626,9 @@ size_t i8q_paged_attention_workspace_size(const i8q_kv_cache* cache, const i8q_p
  * once this call is done); a new page must not be one of them.
  * kept: device int32 [sequences, kv_heads, budget], the kept tokens'
  * indices, -1 from n on.  new_lengths: device int32 [sequences], or NULL.
- * sink + recent <= budget <= new_table's max_pages * page_size.
+ * sink + recent <= budget.  A kept token that new_table's rows have no place
+ * for (n above its max_pages * page_size) is not copied, and reported like
+ * an index out of range.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
 int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* lengths,
                  const i8q_page_table* new_table, int32_t* kept, int64_t budget, int64_t sink, int64_t recent,

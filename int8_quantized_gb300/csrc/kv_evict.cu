@@ -265,7 +265,10 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Args 
     int64_t src = -1, dst = 0;
     int p0, o0, p1, o1;
     if (t >= 0) {
-      const bool ok0 = kv::find(c, a.tab, b, t, p0, o0, a.status), ok1 = kv::find(c, a.to, b, j, p1, o1, a.status);
+      const bool room = j < a.to.max_pages * c.page_size;
+      if (!room) kv::report_index(a.status);
+      const bool ok0 = kv::find(c, a.tab, b, t, p0, o0, a.status);
+      const bool ok1 = room && kv::find(c, a.to, b, j, p1, o1, a.status);
       if (ok0 && ok1) {
         src = kv::row_at(c, p0, h, o0) * BYTES, dst = kv::row_at(c, p1, h, o1) * BYTES;
         const int64_t s0 = kv::scale_at(c, p0, h, o0), s1 = kv::scale_at(c, p1, h, o1);
@@ -320,8 +323,7 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   if (a.to.sequences != a.tab.sequences)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: table and new_table differ in sequences");
   const int64_t heads = (int64_t)a.tab.sequences * a.c.heads;
-  if (budget < 1 || budget > (int64_t)a.to.max_pages * a.c.page_size)
-    return fail(I8Q_ERR_INVALID_ARG, "kv_evict: budget must be 1 .. new_table's max_pages * page_size");
+  if (budget < 1 || budget > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "kv_evict: budget must be 1 .. 2^31 - 1");
   if (heads > INT32_MAX / 16 || heads * ceil_div(budget, kRows) > INT32_MAX)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: sequences * kv_heads * budget out of range");
   if (sink < 0 || recent < 0 || sink > budget || recent > budget - sink)

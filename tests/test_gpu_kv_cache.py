@@ -782,6 +782,29 @@ def test_out_of_range_pages_are_left_out(dev, cache, page_id):
     assert set(changed) <= {int(new[1, 0])}
 
 
+def test_evict_into_too_few_pages(dev):
+    """A budget above what new_table names is fine while no sequence needs it;
+    kept tokens without a place are left out."""
+    g = gen(3)
+    table, pages, free = make_table(g, dev, [20, 60], 16, spare=6)
+    c = make_cache(g, dev, pages, 2, 16, 64, "s8")
+    new = free[:4].view(2, 2).to(torch.int32).to(dev)
+    lengths = torch.tensor([20, 30], dtype=torch.int32, device=dev)
+    kept = torch.empty((2, 2, 1000), dtype=torch.int32, device=dev)
+    q.kv_evict(c, table, lengths, new, kept)
+    q.sync_status()
+    assert (kept[0, :, :20] == torch.arange(20, device=dev)).all() and (kept[0, :, 20:] == -1).all()
+    for t in (0, 15, 16, 29):
+        assert torch.equal(c.k[new[1, t // 16], :, t % 16], c.k[table[1, t // 16], :, t % 16])
+    before = c.k.clone()
+    lengths[1] = 60
+    reported(lambda: q.kv_evict(c, table, lengths, new, kept))
+    changed = (c.k != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert set(changed) <= set(new.flatten().tolist())
+    for t in (0, 31):
+        assert torch.equal(c.k[new[1, t // 16], :, t % 16], c.k[table[1, t // 16], :, t % 16])
+
+
 def test_out_of_range_tokens_are_left_out(dev):
     g = gen(0)
     table, pages, _ = make_table(g, dev, [32, 32], 16)

@@ -151,7 +151,7 @@ def test_attention_refusals(lib):
 def test_evict_refusals(lib):
     for what, kw in [(b"no scores", dict(c=cache(score=None))), (b"NULL", dict(lengths=None)), (b"NULL", dict(kept=None)),
                      (b"differ in sequences", dict(n=table(sequences=2))), (b"budget", dict(budget=0)),
-                     (b"budget", dict(budget=33)), (b"sink", dict(sink=-1)), (b"sink", dict(recent=-1)),
+                     (b"budget", dict(budget=-3)), (b"budget", dict(budget=1 << 31)), (b"sink", dict(sink=-1)), (b"sink", dict(recent=-1)),
                      (b"sink", dict(sink=30)), (b"sink", dict(sink=33)), (b"NULL", dict(n=table(table=None)))]:
         assert evict(lib, **kw) == -1, kw
         assert what in lib.i8q_last_error(), kw
