@@ -594,9 +594,10 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
     if (units)
       return with_lanes(c.dim, [&](auto lanes) -> int {
         constexpr int L = decltype(lanes)::value;
-        // few tokens: their rows over as many CTAs as two for each SM, each with a row per L lanes at least
+        // few tokens: their rows over as many CTAs as 16 for each SM (what fits), each with a row per L lanes
+        // at least
         const int64_t most = ceil_div(std::max<int64_t>(q_heads, c.heads), kUnitThreads / L);
-        const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / tokens));
+        const int splits = (int)std::max<int64_t>(1, std::min(most, 16 * sm_count() / tokens));
         return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), kUnitThreads, 0, 1, s,
                           "kv_append", c, tab, seq, index, splits, rq, ro, rk, rv, r, status);
       });

@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   int copy_at = F::place(lane / F::CR, lane % F::CR), k_at = F::place(g, tig);
   int v_at0 = F::VB == 16 ? F::place(2 * tig, g) : F::place(2 * tig, g / 2) + g % 2 * 8;
   int v_at1 = F::VB == 16 ? F::place(2 * tig + 1, g) : F::place(2 * tig + 1, g / 2) + g % 2 * 8;
+  const int piece_bytes = lane % F::CR * 16 < c.dim * F::ES ? 16 : 0;  // a piece past head_dim is zeros
   asm volatile("" : "+r"(copy_at), "+r"(k_at), "+r"(v_at0), "+r"(v_at1));
   const int per_page = c.page_size / 16;
   const int D = c.dim;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       int64_t at32 = 0, scale_at32 = 0;  // of the 32 tiles from the last multiple of 32 on, one a lane
       int page_next = 0, off_next = 0;   // of the 32 after those
       uint32_t mask = 0xffffu;           // tokens of the tile that take part
-      bool plain = false;                // all of them, every piece inside its row, in one page
+      bool plain = false;                // all of them, in one page
       uint32_t odd_tiles = 0;            // bit j: of the tile sent for j tiles ago, not all tokens take part
       const int last = tile_count(a, len) - 1;
       bool in_next = false;
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           if (i == 0 && t0 < first) mask = 0xffffu << (first - t0) & 0xffffu;
           if (i == last && len - t0 < 16) mask &= 0xffffu >> (16 - (len - t0));
           if (at < 0) mask = 0;
-          plain = mask == 0xffffu && D == F::DP;
+          plain = mask == 0xffffu;
         } else {  // at and scale_at: of token lane % 16
           const bool bad = (unsigned)page_next >= (unsigned)c.pages;
           if (bad) kv::report_index(a.status);
@@ -514,13 +515,19 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           const char* src = from + at;
           if (packed) {
 #pragma unroll
-            for (int r = 0; r < F::CT; ++r) copy16(dst + F::copy_place(copy_at, r), src + r * 512, 16);
+            for (int r = 0; r < F::CT; ++r) copy16(dst + F::copy_place(copy_at, r), src + r * 512, piece_bytes);
           } else {
 #pragma unroll
-            for (int r = 0; r < F::CT; ++r, src += a.step_bytes) copy16(dst + F::copy_place(copy_at, r), src, 16);
+            for (int r = 0; r < F::CT; ++r, src += a.step_bytes)
+              copy16(dst + F::copy_place(copy_at, r), src, piece_bytes);
           }
-        } else {  // some pieces are zeros
-#pragma unroll (F::CT <= 4 ? F::CT : 1)
+        } else if (!whole_pages && mask == 0xffffu) {  // rows of several pages
+          const char* src = from - lane / F::CR * a.token_bytes;
+#pragma unroll
+          for (int r = 0; r < F::CT; ++r)
+            copy16(dst + F::copy_place(copy_at, r), src + __shfl_sync(0xffffffffu, at, (r * 32 + lane) / F::CR), piece_bytes);
+        } else {  // some tokens are zeros
+#pragma unroll 1
           for (int r = 0; r < F::CT; ++r) {
             const int t = (r * 32 + lane) / F::CR, p = lane % F::CR;
             const int64_t row = whole_pages ? at + t * a.token_bytes : __shfl_sync(0xffffffffu, at, t);
