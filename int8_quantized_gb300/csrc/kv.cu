@@ -417,14 +417,15 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
 }
 
 // A CTA has kTokens tokens (or a share of their rows): a thread per token
-// finds its place, then L lanes hold a row, eight elements each, four rows in
-// flight.
+// finds its place, then head_dim / 8 lanes hold a row, eight elements each,
+// four rows in flight.
 constexpr int kTokens = 16;
-template <class T, bool S8, int L>
+template <class T, bool S8, int LANES>
 __global__ void __launch_bounds__(256)
 gather_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
               int splits, Rows k, Rows v, int aligned, uint32_t* status) {
-  constexpr int G = 256 / L, N = 4;
+  constexpr int N = 4;
+  const int L = LANES ? LANES : c.dim / 8, G = 256 / L;  // (a constant for 64, 128 and 256: 32 registers, not 48)
   __shared__ int64_t at[kTokens], scale_at[kTokens];  // at -1: left out
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
@@ -448,7 +449,7 @@ gather_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
   }
   __syncthreads();
   const int d = threadIdx.x % L * 8;
-  if (d >= c.dim) return;
+  if ((int)threadIdx.x >= L * G) return;
   // rows of the CTA: token by token within a head, so that neighbours of a page are read together
   const int rows = 2 * c.heads * kTokens, step = G * splits;
   for (int r0 = (blockIdx.x % splits) * G + threadIdx.x / L; r0 < rows; r0 += N * step) {
@@ -630,12 +631,14 @@ extern "C" int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* ta
     using T = decltype(t);
     I8Q_PROF("kv_gather", s);
     const int aligned = rows_aligned(rk, sizeof(T), 16 / sizeof(T)) && rows_aligned(rv, sizeof(T), 16 / sizeof(T));
-    return with_lanes(c.dim, [&](auto lanes) -> int {
-      constexpr int L = decltype(lanes)::value;
-      const int64_t groups = ceil_div(tokens, kTokens), most = ceil_div(2 * c.heads * kTokens, 256 / L);
-      const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / groups));
-      return kv::launch(gather_kernel<T, decltype(s8)::value, L>, (unsigned)(groups * splits), 256, 0, 1, s, "kv_gather",
-                        c, tab, seq, index, tokens, splits, rk, rv, aligned, status);
-    });
+    const int64_t groups = ceil_div(tokens, kTokens), most = ceil_div(2 * c.heads * kTokens, 256 / (c.dim / 8));
+    const int splits = (int)std::max<int64_t>(1, std::min(most, 2 * sm_count() / groups));
+    constexpr bool S8 = decltype(s8)::value;
+    auto run = [&](auto kernel) {
+      return kv::launch(kernel, (unsigned)(groups * splits), 256, 0, 1, s, "kv_gather", c, tab, seq, index, tokens, splits,
+                        rk, rv, aligned, status);
+    };
+    return c.dim == 64 ? run(gather_kernel<T, S8, 8>) : c.dim == 128 ? run(gather_kernel<T, S8, 16>)
+           : c.dim == 256 ? run(gather_kernel<T, S8, 32>) : run(gather_kernel<T, S8, 0>);
   });
 }

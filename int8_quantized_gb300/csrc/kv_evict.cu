@@ -39,12 +39,12 @@ __device__ __forceinline__ uint32_t key_of(const Args& a, int b, int h, int t) {
   return order_key(a.c.score[kv::scale_at(a.c, page, h, off)]);
 }
 
-// 512 threads of 64 registers: two CTAs to an SM (256 rows of 8192 tokens: 17
-// us, against 22 with 1024 threads).
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kDigits = kBins / kThreads;
+constexpr int kBins = 2048;
 
 // Inclusive sum of v over the block; total: of all.
+template <int THREADS>
 __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
+  constexpr int kWarps = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -66,15 +66,15 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
 }
 
 // The keys of tokens t0 .. t0 + n - 1, V neighbours of a page at a time.
-template <int V>
+template <int V, int THREADS>
 __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const float* scores, int t0, int n,
                                      uint32_t* keys) {
   constexpr int N = 4;
-  for (int i0 = threadIdx.x * V; i0 < n; i0 += N * V * kThreads) {
+  for (int i0 = threadIdx.x * V; i0 < n; i0 += N * V * THREADS) {
     int64_t at[N];  // -1: no such page
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int i = i0 + j * V * kThreads;
+      const int i = i0 + j * V * THREADS;
       if (i >= n) break;
       const int p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size), page = pages[p];
       at[j] = page * a.c.s_page + (t0 + i - p * a.c.page_size) * a.c.s_token;
@@ -86,7 +86,7 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
     float x[N][V];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (i0 + j * V * kThreads >= n) break;
+      if (i0 + j * V * THREADS >= n) break;
       if (at[j] < 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) x[j][v] = -INFINITY;
@@ -98,9 +98,9 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (i0 + j * V * kThreads >= n) break;
+      if (i0 + j * V * THREADS >= n) break;
 #pragma unroll
-      for (int v = 0; v < V; ++v) keys[i0 + j * V * kThreads + v] = order_key(x[j][v]);
+      for (int v = 0; v < V; ++v) keys[i0 + j * V * THREADS + v] = order_key(x[j][v]);
     }
   }
 }
@@ -110,10 +110,16 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
 // into shared memory.  The key of the last kept candidate is found by digits
 // of 11, 11 and 10 bits: each CTA counts its keys by digit, all add up the
 // cluster's counts and pick the digit in which the wanted rank falls.  The
-// kept indices then follow from counts of the tokens before, in order.
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Args a) {
+// kept indices then follow from counts of the tokens before, in order.  A
+// pass whose digit is taken whole is the last: two passes mostly do.
+// 512 threads of 64 registers, two CTAs to an SM (256 rows of 8192 tokens: 17
+// us, against 22 with 1024); 128 threads where the rows are
+// short and more than that.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ Args a) {
+  constexpr int kThreads = THREADS, kWarps = kThreads / 32, kDigits = kBins / kThreads;
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int count[kBins], total_count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_more, s_equal;
+  __shared__ int count[kBins], total_count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_whole, s_more, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / C, b = row / a.c.heads, h = row % a.c.heads;
@@ -137,17 +143,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     // places looked up before the first of them is read
     const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
     const float* scores = a.c.score + h * a.c.s_head;
-    if (a.fours) hold<4>(a, pages, scores, t0, mine, keys);
-    else hold<1>(a, pages, scores, t0, mine, keys);
+    if (a.fours) hold<4, THREADS>(a, pages, scores, t0, mine, keys);
+    else hold<1, THREADS>(a, pages, scores, t0, mine, keys);
   }
   __syncthreads();
-  auto key_at = [&](int i) { return held ? keys[i] : key_of(a, b, h, t0 + i); };
   // candidates: neither the first `sink` nor the last `recent`
   const int lo = a.sink - t0, hi = len - a.recent - t0;
   int need = a.budget - a.sink - a.recent;
   const bool none = need == 0;
   uint32_t prefix = 0, mask = 0;
-  for (int shift = 21; !none && shift >= 0; shift -= shift == 21 ? 11 : 10) {
+  bool whole = false;  // all keys that begin with prefix stay
+  for (int shift = 21; !none && !whole && shift >= 0; shift -= shift == 21 ? 11 : 10) {
     // digits at bits 21 to 31, 10 to 20 and 0 to 9
     const uint32_t digits = shift ? 0x7ffu : 0x3ffu;
     for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
@@ -187,41 +193,55 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     int mine_count = 0, total;
 #pragma unroll
     for (int i = 0; i < kDigits; ++i) mine_count += sums[d - i];
-    const int through = block_scan(mine_count, &total, warp_sums);
+    const int through = block_scan<THREADS>(mine_count, &total, warp_sums);
     int before = through - mine_count;
     if (before < need && need <= through) {
       int digit = d;
       while (need > before + sums[digit]) before += sums[digit--];
       s_digit = digit;
       s_need = need - before;
+      s_whole = need - before == sums[digit];
     }
     __syncthreads();
     prefix |= (uint32_t)s_digit << shift;
     mask |= digits << shift;
     need = s_need;
+    whole = s_whole;
     // (a CTA that clears its counts has passed the second cluster.sync, after which none reads them; the
     // sums are written anew after the next pass's first)
     __syncthreads();
   }
-  // Candidates above the key stay, and the first `need` that equal it.  Each
-  // warp has a run of the share.
-  const int run = (mine + kWarps * 32 - 1) / (kWarps * 32) * 32, i0 = warp * run, i1 = min(i0 + run, mine);
-  auto classes = [&](int i, bool& more, bool& equal) {
-    more = i < i1 && (i < lo || i >= hi);
-    equal = false;
-    if (!none && i < i1 && i >= lo && i < hi) {
-      const uint32_t key = key_at(i);
-      more = key > prefix;
-      equal = key == prefix;
+  // Candidates above the key stay, and the first `need` that equal it (or all
+  // from the prefix on).  Each warp has a run of the share.
+  const int run = (mine + kWarps * 128 - 1) / (kWarps * 128) * 128, i0 = warp * run, i1 = min(i0 + run, mine);
+  // of four neighbours: bit j of more: kept; of equal: kept by rank
+  auto classes = [&](int i, uint32_t& more, uint32_t& equal) {
+    more = equal = 0;
+    if (i >= i1) return;
+    uint32_t key[4] = {};
+    if (held) {  // (the last four may reach past the share, within the room)
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      key[0] = k.x, key[1] = k.y, key[2] = k.z, key[3] = k.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < i1) key[j] = key_of(a, b, h, t0 + i + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + j >= i1) break;
+      const bool sure = i + j < lo || i + j >= hi;
+      more |= (sure || (!none && (whole ? key[j] >= prefix : key[j] > prefix)) ? 1u : 0u) << j;
+      equal |= (!sure && !none && !whole && key[j] == prefix ? 1u : 0u) << j;
     }
   };
   int mores = 0, equals = 0;
-  for (int i = i0; i < i1; i += 32) {
-    bool more, equal;
-    classes(i + lane, more, equal);
-    mores += __popc(__ballot_sync(0xffffffffu, more));
-    equals += __popc(__ballot_sync(0xffffffffu, equal));
+  for (int i = i0; i < i1; i += 128) {
+    uint32_t more, equal;
+    classes(i + 4 * lane, more, equal);
+    mores += __popc(more), equals += __popc(equal);
   }
+  mores = __reduce_add_sync(0xffffffffu, mores), equals = __reduce_add_sync(0xffffffffu, equals);
   if (lane == 0) warp_more[warp] = mores, warp_equal[warp] = equals;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -233,14 +253,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   int more_before = 0, equal_before = 0;
   for (int r = 0; r < rank; ++r) more_before += *cluster.map_shared_rank(&s_more, r), equal_before += *cluster.map_shared_rank(&s_equal, r);
   for (int w = 0; w < warp; ++w) more_before += warp_more[w], equal_before += warp_equal[w];
-  for (int i = i0; i < i1; i += 32) {
-    bool more, equal;
-    classes(i + lane, more, equal);
-    const uint32_t m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, equal);
-    const uint32_t under = (1u << lane) - 1;
-    const int before = equal_before + __popc(e & under);
-    if (more || (equal && before < need)) kept[more_before + __popc(m & under) + min(before, need)] = t0 + i + lane;
-    more_before += __popc(m), equal_before += __popc(e);
+  for (int i = i0; i < i1; i += 128) {
+    uint32_t more, equal;
+    classes(i + 4 * lane, more, equal);
+    const int own = __popc(more) | __popc(equal) << 16;
+    int upto = own;  // both counts, of the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += u;
+    }
+    int m = more_before + ((upto - own) & 0xffff), e = equal_before + ((upto - own) >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool is_more = more >> j & 1, is_equal = equal >> j & 1;
+      if (is_more || (is_equal && e < need)) kept[m + min(e, need)] = t0 + i + 4 * lane + j;
+      m += is_more, e += is_equal;
+    }
+    const int all_lanes = __shfl_sync(0xffffffffu, upto, 31);
+    more_before += all_lanes & 0xffff, equal_before += all_lanes >> 16;
   }
   cluster.sync();  // no CTA leaves while another reads its counts
 }
@@ -283,11 +314,9 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Args 
     from[threadIdx.x] = src, to[threadIdx.x] = dst;
   }
   __syncthreads();
-  const int pieces = c.dim * BYTES / 16;  // of a row
-  int lanes = 1;
-  while (lanes < pieces) lanes *= 2;
-  const int groups = 256 / lanes, group = threadIdx.x / lanes, e = threadIdx.x % lanes * 16;
-  if (e >= c.dim * BYTES) return;
+  const int pieces = c.dim * BYTES / 16;  // of a row, a lane each
+  const int groups = 256 / pieces, group = threadIdx.x / pieces, e = threadIdx.x % pieces * 16;
+  if (group >= groups) return;
   for (int r0 = group; r0 < 2 * kRows; r0 += 4 * groups) {
     uint4 x[4];
     char* dst[4];
@@ -333,20 +362,23 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   a.status = device_status_word();
   if (!a.status) return fail(I8Q_ERR_CUDA, "kv_evict: no status word");
   cudaStream_t s = as_stream(stream);
-  // As many CTAs to a row as give every SM one, or keep a share within 16K
-  // tokens (32 passes of a CTA), up to the portable 8 (8 rows of 131072 tokens took three times
-  // as long in clusters of 16).  A share whose keys shared memory cannot hold
-  // is read again in each pass.
+  // Long rows: as many CTAs to a row as give every SM one, or keep a share
+  // within 16K tokens, up to the portable 8 (8 rows of 131072 tokens took three
+  // times as long in clusters of 16).  A CTA takes 1 us per 1000 tokens and a
+  // cluster 6 us of its own, so rows up to 12288 tokens have one CTA.  A share
+  // whose keys shared memory cannot hold is read again in each pass.
   const int64_t most = (int64_t)a.tab.max_pages * a.c.page_size;
   int cluster = 1;
-  while (cluster < 8 && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384) && most / cluster > 1024)
-    cluster *= 2;
+  while (most > 12288 && cluster < 8 && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384)) cluster *= 2;
   a.room = (int)std::min<int64_t>(round_up(ceil_div(most, cluster), 4), 48 * 1024);
   a.fours = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
             reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
   {
     I8Q_PROF("kv_evict_select", s);
-    rc = kv::launch(select_kernel, (unsigned)(heads * cluster), kThreads, a.room * 4, cluster, s, "kv_evict_select", a);
+    rc = most <= 1024 && heads > 2 * sm_count() ? kv::launch(select_kernel<128>, (unsigned)(heads * cluster), 128, a.room * 4, cluster, s,
+                                   "kv_evict_select", a)
+                      : kv::launch(select_kernel<512>, (unsigned)(heads * cluster), 512, a.room * 4, cluster, s,
+                                   "kv_evict_select", a);
     if (rc != I8Q_OK) return rc;
   }
   I8Q_PROF("kv_evict_move", s);
