@@ -273,10 +273,12 @@ struct Form {
   static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
   // Warps: 16 of 128 registers where they suffice (1 x 131072 tokens: 60 us,
-  // as with 12 of 168, and 64 x 8192: 205 us against 211), 12, else 8 or 4 of
-  // 255.
-  static constexpr int W = NT == 1 && S8 && DP <= 128 && !WIDE ? 16 : NT == 1 && (S8 ? DP <= 128 : DP == 64) ? 12
-                           : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024 ? 8 : 4;
+  // as with 12 of 168, and 64 x 8192: 205 us against 211), else 12 (of 16
+  // heads of 64: 37 us against 45 with 8; of 128: 41 against 29), 8 or 4 of 255.
+  static constexpr int W = NT == 1 && S8 && DP <= 128 && !WIDE                               ? 16
+                           : (NT == 1 && (S8 ? DP <= 128 : DP == 64)) || (DP == 64 && !WIDE) ? 12
+                           : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024                          ? 8
+                                                                                             : 4;
   static constexpr int ROOM = (208 * 1024 / W - Q_BYTES) / SLOT;
   static constexpr int AHEAD = ROOM >= 5 ? 2 : 1;  // tiles in flight
   static constexpr int SLOTS = 2 * AHEAD + 1;
