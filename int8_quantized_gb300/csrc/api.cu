@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kv.cuh"
 
 namespace i8q {
 

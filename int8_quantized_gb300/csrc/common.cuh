@@ -50,9 +50,6 @@ int smem_attr(const void* func, int bytes);
 
 // Device-side status word for bounded waits (see i8q_sync_status).
 uint32_t* device_status_word();
-// Its bit for an index out of range in a key/value cache call's device data
-// (the bits below it belong to the bounded waits).
-constexpr uint32_t ST_KV_INDEX = 1u << 31;
 
 // Kernel timing (i8q_profile_*): while enabled, a ProfScope brackets the
 // launches made in its lifetime with CUDA events on the launch stream.

