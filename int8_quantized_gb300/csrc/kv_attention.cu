@@ -7,32 +7,43 @@ namespace {
 
 using namespace kva;
 
+// The parts of a row that was cut.
+struct Parts {
+  int w0, w1, cta0, count, per_cta;  // count 1: it was not
+  // part k: what CTA w0 / per_cta joined from w0 on, what the next ones joined, and part w1
+  __device__ int64_t at(const Args& a, int k, int hh) const {
+    const int w = k == 0 ? w0 : k == count - 1 ? w1 : (cta0 + k) * per_cta;
+    return ((int64_t)w * 2 + (k == 0)) * a.heads_per_row + hh;
+  }
+};
+__device__ __forceinline__ Parts parts_of(const Args& a, const Cut& cut, int row_at, int cost) {
+  Parts p;
+  p.w0 = cut.of(row_at), p.w1 = cut.of(row_at + cost - 1);
+  p.per_cta = cut.per_cta;
+  p.cta0 = p.w0 / cut.per_cta;
+  p.count = p.w0 == p.w1 ? 1 : (p.w1 - 1) / cut.per_cta - p.cta0 + 2;
+  return p;
+}
+
 // Rows that lie in several parts: S warps per sequence and query head, each
 // reading four parts at once (a chain of four dependent loads: 4 us a call).
 template <class QT, int DP, int S>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void join_rows(const Args& a) {
   constexpr int E = (DP + 127) / 128;
   __shared__ float4 s_out[S > 1 ? 8 : 1][E][32];
   __shared__ float2 s_stats[8];
   const Cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % S;
   const int id = blockIdx.x * (8 / S) + warp / S;
-  next_kernel_may_start();
-  wait_previous_kernel();
   if (id >= a.tab.sequences * a.q_heads) return;  // (whole CTAs where S is 8, as in the other returns)
   const int b = id / a.q_heads, h = id % a.q_heads;
   const int gi = h % a.group, row = h / a.group * a.chunks + gi / a.heads_per_row, hh = gi % a.heads_per_row;
   const int R = c.heads * a.chunks;
   const int n = a.line[a.tab.sequences], at = a.line[b], cost = (a.line[b + 1] - at) / R;
   const Cut cut = cut_line(a, n, a.tab.sequences * R);
-  const int row_at = at + row * cost, w0 = cut.of(row_at), w1 = cut.of(row_at + cost - 1);
-  if (w0 == w1) return;
-  // what CTA w0 / per_cta joined from w0 on, what the next ones joined, and part w1
-  const int cta0 = w0 / cut.per_cta, count = (w1 - 1) / cut.per_cta - cta0 + 2;
-  auto part = [&](int k) {
-    const int w = k == 0 ? w0 : k == count - 1 ? w1 : (cta0 + k) * cut.per_cta;
-    return ((int64_t)w * 2 + (k == 0)) * a.heads_per_row + hh;
-  };
+  const Parts p = parts_of(a, cut, at + row * cost, cost);
+  const int count = p.count;
+  if (count == 1) return;
   float top = -INFINITY, sum = 0.0f;
   float4 acc[E];
 #pragma unroll
@@ -44,12 +55,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       st[i] = make_float2(-INFINITY, 0.0f);
-      if (k0 + i < count) st[i] = a.part_stats[part(k0 + i)];
+      if (k0 + i < count) st[i] = a.part_stats[p.at(a, k0 + i, hh)];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         v[i][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (k0 + i < count && e * 128 + lane * 4 < DP)
-          v[i][e] = *reinterpret_cast<const float4*>(a.part_out + part(k0 + i) * DP + e * 128 + lane * 4);
+          v[i][e] = *reinterpret_cast<const float4*>(a.part_out + p.at(a, k0 + i, hh) * DP + e * 128 + lane * 4);
       }
     }
     float next = top;
@@ -103,15 +114,19 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 // its key/value head.  The line again, with one row per key/value head; a
 // lane takes V tokens at a time: 4 neighbours in one page, or 1 (64 sequences
 // of 8192, 32 and 8 heads, 101 MB: 23 us with 4, 70 with 1).
-template <int V>
-__global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
+// HERE: the log of the sum of exponentials of rows that were cut is joined
+// here too, a lane per query head (at most 32), from the parts' maxima and
+// sums: the scores then need not wait for join_rows.
+template <int V, bool HERE>
+__device__ __forceinline__ void add_scores(const Args& a, int block, int blocks) {
+  __shared__ float s_log[8][32];
   const Cache& c = a.c;
-  const int lane = threadIdx.x & 31, B = a.tab.sequences;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  wait_previous_kernel();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = a.tab.sequences;
+  const int w = block * 8 + warp;
   // parts of 16 tiles at least; the other warps have none
-  const int n = a.line[B] / a.chunks, parts = max(1, min((int)gridDim.x * 8, n / 16));
+  const int total = a.line[B], n = total / a.chunks, parts = max(1, min(blocks * 8, n / 16));
   if (w >= parts) return;
+  const Cut cut = cut_line(a, total, B * c.heads * a.chunks);
   const int q = n / parts, longer = n - q * parts;
   int x = w * q + min(w, longer);
   const int x_end = x + q + (w < longer);
@@ -132,6 +147,38 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
       const int begin = max(x - row_at - kRowCost, 0), end = max(seg_end - row_at - kRowCost, 0);
       x = seg_end;
       const int64_t h0 = (int64_t)b * a.q_heads + kvh * a.group;
+      if constexpr (HERE) {
+        if (lane < a.group) {
+          const int hh = lane % a.heads_per_row;
+          const Parts p = parts_of(a, cut, a.line[b] + (kvh * a.chunks + lane / a.heads_per_row) * cost, cost);
+          float z;
+          if (p.count == 1) {
+            z = a.stats[h0 + lane];
+          } else {
+            float top = -INFINITY, sum = 0.0f;
+            for (int k0 = 0; k0 < p.count; k0 += 4) {
+              float2 st[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                st[i] = k0 + i < p.count ? a.part_stats[p.at(a, k0 + i, hh)] : make_float2(-INFINITY, 0.0f);
+              const float next = fmaxf(fmaxf(top, fmaxf(st[0].x, st[1].x)), fmaxf(st[2].x, st[3].x));
+              const float ref = next == -INFINITY ? 0.0f : next;
+              sum *= ex2_approx(top - ref);
+              top = next;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum = fmaf(st[i].y, ex2_approx(st[i].x - ref), sum);
+            }
+            z = sum == 0.0f ? -INFINITY : top + log2f(sum);
+          }
+          s_log[warp][lane] = z == -INFINITY ? INFINITY : z;
+        }
+        __syncwarp();
+      }
+      auto log_of = [&](int i) {  // infinite where there is no weight
+        if constexpr (HERE) return s_log[warp][i];
+        const float z = a.stats[h0 + i];
+        return z == -INFINITY ? INFINITY : z;
+      };
       const int t_end = min((tile0 + end) * 16, len);
       for (int t = (tile0 + begin) * 16 + lane * V; t < t_end; t += 32 * V) {
         if (t + V <= first) continue;
@@ -145,9 +192,8 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
           float4 s = *reinterpret_cast<const float4*>(score);
 #pragma unroll 4
           for (int i = 0; i < a.group; ++i) {
-            const float z = a.stats[h0 + i];
+            const float r = log_of(i);
             const float4 l = __ldcs(reinterpret_cast<const float4*>(logit + i * a.logit_pitch));
-            const float r = z == -INFINITY ? INFINITY : z;
             p[0] += ex2_approx(l.x - r), p[1] += ex2_approx(l.y - r);
             p[2] += ex2_approx(l.z - r), p[3] += ex2_approx(l.w - r);
           }
@@ -159,14 +205,35 @@ __global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args
         } else {
 #pragma unroll 4
           for (int i = 0; i < a.group; ++i) {
-            const float z = a.stats[h0 + i], l = logit[i * a.logit_pitch];
-            p[0] += ex2_approx(l - (z == -INFINITY ? INFINITY : z));
+            p[0] += ex2_approx(logit[i * a.logit_pitch] - log_of(i));
           }
           *score += p[0];
         }
       }
+      if constexpr (HERE) __syncwarp();  // (the next row's logs go to the same place)
     }
   }
+}
+
+template <class QT, int DP, int S>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  next_kernel_may_start();
+  wait_previous_kernel();
+  join_rows<QT, DP, S>(a);
+}
+
+template <int V>
+__global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ Args a) {
+  wait_previous_kernel();
+  add_scores<V, false>(a, blockIdx.x, gridDim.x);
+}
+
+// Both at once: the first `joins` CTAs join rows, the others add scores.
+template <class QT, int DP, int S, int V>
+__global__ void __launch_bounds__(256) join_and_score_kernel(const __grid_constant__ Args a, int joins) {
+  wait_previous_kernel();
+  if ((int)blockIdx.x < joins) join_rows<QT, DP, S>(a);
+  else add_scores<V, true>(a, blockIdx.x - joins, gridDim.x - joins);
 }
 
 int width_of(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -181,9 +248,16 @@ int64_t line_length(const Cache& c, const Table& tab, int64_t q_heads) {
 }
 
 using Kernel = void (*)(Args);
+using KernelAt = void (*)(Args, int);
 template <class QT, int S>
 Kernel join_of(int dp) {
   return dp == 64 ? join_kernel<QT, 64, S> : dp == 128 ? join_kernel<QT, 128, S> : join_kernel<QT, 256, S>;
+}
+template <class QT, int S>
+KernelAt join_and_score_of(int dp, bool four) {
+  if (dp == 64) return four ? join_and_score_kernel<QT, 64, S, 4> : join_and_score_kernel<QT, 64, S, 1>;
+  if (dp == 128) return four ? join_and_score_kernel<QT, 128, S, 4> : join_and_score_kernel<QT, 128, S, 1>;
+  return four ? join_and_score_kernel<QT, 256, S, 4> : join_and_score_kernel<QT, 256, S, 1>;
 }
 
 struct Layout {
@@ -298,21 +372,34 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     a.lse = lse ? lse + b0 * q_heads : nullptr;
     rc = (l.dp == 64 ? attend_64 : l.dp == 128 ? attend_128 : attend_256)(a, type, s8, s);
     if (rc != I8Q_OK) return rc;
+    // few rows mean many parts each: 8 warps a row then, where one would read all in turn (18 parts of each of
+    // 32 heads: 5 us against 9)
+    const int heads = a.tab.sequences * a.q_heads;
+    const bool few = heads <= 2 * sm_count();
+    const unsigned joins = (unsigned)(few ? heads : ceil_div(heads, 8)), scores = 16 * (unsigned)sm_count();
+    // Both in one launch where there is not much to score: 24 x 2500 tokens of 16 heads take 37 us instead of 40;
+    // with twice the registers of the scores alone 64 x 8192 of 8 heads would take 237 instead of 231.
+    const int64_t tokens = (int64_t)a.tab.sequences * a.c.heads * a.tab.max_pages * a.c.page_size;
+    if (!a.per_row && accumulate && a.group <= 32 && tokens <= 1 << 21) {
+      I8Q_PROF("paged_attention_join_and_scores", s);
+      const KernelAt kernel = type == I8Q_F32
+                                  ? (few ? join_and_score_of<float, 8>(l.dp, four) : join_and_score_of<float, 1>(l.dp, four))
+                                  : (few ? join_and_score_of<__nv_bfloat16, 8>(l.dp, four)
+                                         : join_and_score_of<__nv_bfloat16, 1>(l.dp, four));
+      rc = kv::launch(kernel, joins + scores, 256, 0, 1, s, "paged_attention_join_and_scores", a, (int)joins);
+      if (rc != I8Q_OK) return rc;
+      continue;
+    }
     if (!a.per_row) {
       I8Q_PROF("paged_attention_join", s);
-      // few rows mean many parts each: 8 warps then, where one has to read all in turn (18 parts of
-      // each of 32 heads: 5 us against 9)
-      const int heads = a.tab.sequences * a.q_heads;
-      const bool few = heads <= 2 * sm_count();
       const Kernel join = type == I8Q_F32 ? (few ? join_of<float, 8>(l.dp) : join_of<float, 1>(l.dp))
                                           : (few ? join_of<__nv_bfloat16, 8>(l.dp) : join_of<__nv_bfloat16, 1>(l.dp));
-      rc = kv::launch(join, (unsigned)(few ? heads : ceil_div(heads, 8)), 256, 0, 1, s, "paged_attention_join", a);
+      rc = kv::launch(join, joins, 256, 0, 1, s, "paged_attention_join", a);
       if (rc != I8Q_OK) return rc;
     }
     if (accumulate) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, (unsigned)sm_count() * 16, 256, 0, 1, s,
-                        "paged_attention_scores", a);
+      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, scores, 256, 0, 1, s, "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }
   }

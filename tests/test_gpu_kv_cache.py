@@ -225,6 +225,16 @@ def test_attention_cut_rows_lengths(dev, lens):
     check_attention(dev, lens, 2, 2, 64, 16, "bf16", "bf16", extra=2000)
 
 
+@pytest.mark.parametrize("G", [1, 4, 9, 32, 33, 40])
+@pytest.mark.parametrize("page", [6, 16])
+@pytest.mark.parametrize("B", [1, 30])
+def test_attention_cut_rows_scores_in_one_launch_or_two(dev, G, page, B):
+    """Tables that name up to 2^21 tokens of all heads, and more; up to 32 heads to one, and more."""
+    for extra in (500, 140000):
+        check_attention(dev, [900, 0, 77] * B, 2 * G, 2, 64, page, "bf16", "s8", accumulate=True, window=600,
+                        extra=extra // B)
+
+
 def test_attention_cut_rows_over_many_sequences(dev):
     r = np.random.default_rng(5)
     check_attention(dev, [int(x) for x in r.integers(0, 200, 700)], 4, 2, 64, 16, "bf16", "s8", accumulate=True,
