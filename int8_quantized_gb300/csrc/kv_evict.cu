@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t key_of(const Args& a, int b, int h, int t) {
   return order_key(a.c.score[kv::scale_at(a.c, page, h, off)]);
 }
 
-constexpr int kBins = 2048;
+constexpr int kBins = 2048, kMostCtas = 8;  // CTAs of a cluster
 
 // Inclusive sum of v over the block; total: of all.
 template <int THREADS>
@@ -65,42 +65,48 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
   return v + (warp ? before : 0);
 }
 
-// The keys of tokens t0 .. t0 + n - 1, V neighbours of a page at a time.
+// The keys of tokens t0 .. t0 + n - 1, V neighbours of a page at a time; those
+// of tokens lo .. hi - 1 are counted by their first digit on the way.
+constexpr int kFirstShift = 21;
 template <int V, int THREADS>
 __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const float* scores, int t0, int n,
-                                     uint32_t* keys) {
-  constexpr int N = 4;
+                                     uint32_t* keys, int* count, int lo, int hi) {
+  constexpr int N = 8;
   for (int i0 = threadIdx.x * V; i0 < n; i0 += N * V * THREADS) {
-    int64_t at[N];  // -1: no such page
+    int page[N], off[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int i = i0 + j * V * THREADS;
       if (i >= n) break;
-      const int p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size), page = pages[p];
-      at[j] = page * a.c.s_page + (t0 + i - p * a.c.page_size) * a.c.s_token;
-      if ((unsigned)page >= (unsigned)a.c.pages) {
-        kv::report_index(a.status);
-        at[j] = -1;
-      }
+      const int p = (int)((unsigned)(t0 + i) / (unsigned)a.c.page_size);
+      page[j] = pages[p];
+      off[j] = t0 + i - p * a.c.page_size;
     }
     float x[N][V];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (i0 + j * V * THREADS >= n) break;
-      if (at[j] < 0) {
+      const float* at = scores + page[j] * a.c.s_page + off[j] * a.c.s_token;
+      if ((unsigned)page[j] >= (unsigned)a.c.pages) {
+        kv::report_index(a.status);
 #pragma unroll
         for (int v = 0; v < V; ++v) x[j][v] = -INFINITY;
       } else if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(x[j]) = *reinterpret_cast<const float4*>(scores + at[j]);
+        *reinterpret_cast<float4*>(x[j]) = *reinterpret_cast<const float4*>(at);
       } else {
-        x[j][0] = scores[at[j]];
+        x[j][0] = *at;
       }
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (i0 + j * V * THREADS >= n) break;
+      const int i = i0 + j * V * THREADS;
+      if (i >= n) break;
 #pragma unroll
-      for (int v = 0; v < V; ++v) keys[i0 + j * V * THREADS + v] = order_key(x[j][v]);
+      for (int v = 0; v < V; ++v) {
+        const uint32_t key = order_key(x[j][v]);
+        keys[i + v] = key;
+        if (i + v >= lo && i + v < hi) atomicAdd(&count[key >> kFirstShift], 1);
+      }
     }
   }
 }
@@ -116,15 +122,18 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
 // us, against 22 with 1024); 128 threads where the rows are
 // short and more than that.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const __grid_constant__ Args a) {
   constexpr int kThreads = THREADS, kWarps = kThreads / 32, kDigits = kBins / kThreads;
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int count[kBins], total_count[kBins], warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_whole, s_more, s_equal;
+  __shared__ __align__(16) int count[kBins], total_count[kBins];
+  __shared__ int warp_sums[kWarps], warp_more[kWarps], warp_equal[kWarps], s_digit, s_need, s_whole, s_more, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / C, b = row / a.c.heads, h = row % a.c.heads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   kv::next_kernel_may_start();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
+  __syncthreads();
   kv::wait_previous_kernel();
   const int len = kv::cut_length(a.c, a.tab, a.lengths[b], a.status);
   const int n = min(len, a.budget);
@@ -138,31 +147,34 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   }
   const int share = ((len + C - 1) / C + 3) / 4 * 4, t0 = min(rank * share, len), mine = min(share, len - t0);  // shares begin on multiples of 4
   const bool held = share <= a.room;
+  // candidates: neither the first `sink` nor the last `recent`
+  const int lo = a.sink - t0, hi = len - a.recent - t0, c0 = max(lo, 0), c1 = min(hi, mine);
   if (held) {
-    // four neighbouring scores of a page at once where they lie so, and four
+    // four neighbouring scores of a page at once where they lie so, and eight
     // places looked up before the first of them is read
     const int32_t* pages = a.tab.page + (int64_t)b * a.tab.stride;
     const float* scores = a.c.score + h * a.c.s_head;
-    if (a.fours) hold<4, THREADS>(a, pages, scores, t0, mine, keys);
-    else hold<1, THREADS>(a, pages, scores, t0, mine, keys);
+    if (a.fours) hold<4, THREADS>(a, pages, scores, t0, mine, keys, count, c0, c1);
+    else hold<1, THREADS>(a, pages, scores, t0, mine, keys, count, c0, c1);
   }
-  __syncthreads();
-  // candidates: neither the first `sink` nor the last `recent`
-  const int lo = a.sink - t0, hi = len - a.recent - t0;
   int need = a.budget - a.sink - a.recent;
   const bool none = need == 0;
+  if (none) __syncthreads();  // (else after the counts)
   uint32_t prefix = 0, mask = 0;
   bool whole = false;  // all keys that begin with prefix stay
-  for (int shift = 21; !none && !whole && shift >= 0; shift -= shift == 21 ? 11 : 10) {
+  for (int shift = kFirstShift; !none && !whole && shift >= 0; shift -= shift == kFirstShift ? 11 : 10) {
     // digits at bits 21 to 31, 10 to 20 and 0 to 9
     const uint32_t digits = shift ? 0x7ffu : 0x3ffu;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
-    __syncthreads();
+    if (shift != kFirstShift) {
+      for (int i = threadIdx.x; i < kBins; i += kThreads) count[i] = 0;
+      __syncthreads();
+    }
     auto add = [&](uint32_t key) {
       if ((key & mask) == prefix) atomicAdd(&count[key >> shift & digits], 1);
     };
-    const int c0 = max(lo, 0), c1 = min(hi, mine);
-    if (held) {  // four keys at a time between the ends
+    if (!held) {
+      for (int i = c0 + threadIdx.x; i < c1; i += kThreads) add(key_of(a, b, h, t0 + i));
+    } else if (shift != kFirstShift) {  // four keys at a time between the ends
       const int q0 = (c0 + 3) / 4 * 4, q1 = max(q0, c1 / 4 * 4);
       for (int i = q0 + threadIdx.x * 4; i < q1; i += kThreads * 4) {
         const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
@@ -170,18 +182,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
       }
       if (c0 + (int)threadIdx.x < min(q0, c1)) add(keys[c0 + threadIdx.x]);
       if (q1 + (int)threadIdx.x < c1) add(keys[q1 + threadIdx.x]);
-    } else {
-      for (int i = c0 + threadIdx.x; i < c1; i += kThreads) add(key_of(a, b, h, t0 + i));
     }
     // each CTA adds up a share of the digits and hands the sums to all
     const int* sums = count;
     if (C > 1) {
       cluster.sync();
       const int part = kBins / C;
-      for (int i = threadIdx.x; i < part; i += kThreads) {
-        int x = 0;
-        for (int r = 0; r < C; ++r) x += cluster.map_shared_rank(count, r)[rank * part + i];
-        for (int r = 0; r < C; ++r) cluster.map_shared_rank(total_count, r)[rank * part + i] = x;
+      for (int i = rank * part + threadIdx.x; i < (rank + 1) * part; i += kThreads) {
+        int y[kMostCtas], x = 0;
+#pragma unroll
+        for (int r = 0; r < kMostCtas; ++r) y[r] = r < C ? cluster.map_shared_rank(count, r)[i] : 0;
+#pragma unroll
+        for (int r = 0; r < kMostCtas; ++r) x += y[r];
+#pragma unroll
+        for (int r = 0; r < kMostCtas; ++r)
+          if (r < C) cluster.map_shared_rank(total_count, r)[i] = x;
       }
       cluster.sync();
       sums = total_count;
@@ -189,18 +204,26 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
       __syncthreads();
     }
     // kDigits digits a thread, from the highest down
-    const int d = kBins - 1 - kDigits * threadIdx.x;
-    int mine_count = 0, total;
+    const int d = kBins - kDigits * (threadIdx.x + 1);
+    int sum[kDigits], mine_count = 0, total;
 #pragma unroll
-    for (int i = 0; i < kDigits; ++i) mine_count += sums[d - i];
+    for (int i = 0; i < kDigits; i += 4) *reinterpret_cast<int4*>(sum + i) = *reinterpret_cast<const int4*>(sums + d + i);
+#pragma unroll
+    for (int i = 0; i < kDigits; ++i) mine_count += sum[i];
     const int through = block_scan<THREADS>(mine_count, &total, warp_sums);
     int before = through - mine_count;
     if (before < need && need <= through) {
-      int digit = d;
-      while (need > before + sums[digit]) before += sums[digit--];
-      s_digit = digit;
-      s_need = need - before;
-      s_whole = need - before == sums[digit];
+      bool found = false;
+#pragma unroll
+      for (int i = kDigits - 1; i >= 0; --i) {
+        if (!found && need <= before + sum[i]) {
+          found = true;
+          s_digit = d + i;
+          s_need = need - before;
+          s_whole = need - before == sum[i];
+        }
+        before += sum[i];
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)s_digit << shift;
@@ -214,6 +237,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   // Candidates above the key stay, and the first `need` that equal it (or all
   // from the prefix on).  Each warp has a run of the share.
   const int run = (mine + kWarps * 128 - 1) / (kWarps * 128) * 128, i0 = warp * run, i1 = min(i0 + run, mine);
+  // no key has the value of all ones
+  const uint32_t from = none ? ~0u : whole ? prefix : prefix + 1, same = none || whole ? ~0u : prefix;
   // of four neighbours: bit j of more: kept; of equal: kept by rank
   auto classes = [&](int i, uint32_t& more, uint32_t& equal) {
     more = equal = 0;
@@ -227,12 +252,17 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
       for (int j = 0; j < 4; ++j)
         if (i + j < i1) key[j] = key_of(a, b, h, t0 + i + j);
     }
+    if (i >= lo && i + 4 <= min(hi, i1)) {  // candidates all
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i + j >= i1) break;
-      const bool sure = i + j < lo || i + j >= hi;
-      more |= (sure || (!none && (whole ? key[j] >= prefix : key[j] > prefix)) ? 1u : 0u) << j;
-      equal |= (!sure && !none && !whole && key[j] == prefix ? 1u : 0u) << j;
+      for (int j = 0; j < 4; ++j) more |= (uint32_t)(key[j] >= from) << j, equal |= (uint32_t)(key[j] == same) << j;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j >= i1) break;
+        const bool sure = i + j < lo || i + j >= hi;
+        more |= (uint32_t)(sure || key[j] >= from) << j;
+        equal |= (uint32_t)(!sure && key[j] == same) << j;
+      }
     }
   };
   int mores = 0, equals = 0;
@@ -244,36 +274,48 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   mores = __reduce_add_sync(0xffffffffu, mores), equals = __reduce_add_sync(0xffffffffu, equals);
   if (lane == 0) warp_more[warp] = mores, warp_equal[warp] = equals;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int m = 0, e = 0;
-    for (int w = 0; w < kWarps; ++w) m += warp_more[w], e += warp_equal[w];
-    s_more = m, s_equal = e;
+  // of the share, then of the warps and CTAs before this one
+  const int lane_more = lane < kWarps ? warp_more[lane] : 0, lane_equal = lane < kWarps ? warp_equal[lane] : 0;
+  if (warp == 0) {
+    const int m = __reduce_add_sync(0xffffffffu, lane_more), e = __reduce_add_sync(0xffffffffu, lane_equal);
+    if (lane == 0) s_more = m, s_equal = e;
   }
-  cluster.sync();
-  int more_before = 0, equal_before = 0;
-  for (int r = 0; r < rank; ++r) more_before += *cluster.map_shared_rank(&s_more, r), equal_before += *cluster.map_shared_rank(&s_equal, r);
-  for (int w = 0; w < warp; ++w) more_before += warp_more[w], equal_before += warp_equal[w];
+  if (C > 1) cluster.sync();
+  int more_before = lane < warp ? lane_more : 0, equal_before = lane < warp ? lane_equal : 0;
+  if (lane < rank) more_before += *cluster.map_shared_rank(&s_more, lane), equal_before += *cluster.map_shared_rank(&s_equal, lane);
+  more_before = __reduce_add_sync(0xffffffffu, more_before), equal_before = __reduce_add_sync(0xffffffffu, equal_before);
+  const uint32_t lanes_before = (1u << lane) - 1;
   for (int i = i0; i < i1; i += 128) {
     uint32_t more, equal;
     classes(i + 4 * lane, more, equal);
-    const int own = __popc(more) | __popc(equal) << 16;
-    int upto = own;  // both counts, of the lanes up to this one
+    const int t = t0 + i + 4 * lane;
+    int m = more_before;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += u;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t of_all = __ballot_sync(0xffffffffu, more >> j & 1);
+      m += __popc(of_all & lanes_before), more_before += __popc(of_all);
     }
-    int m = more_before + ((upto - own) & 0xffff), e = equal_before + ((upto - own) >> 16);
+    if (!__any_sync(0xffffffffu, equal)) {
+      m += min(equal_before, need);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (more >> j & 1) kept[m++] = t + j;
+      continue;
+    }
+    int e = equal_before;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t of_all = __ballot_sync(0xffffffffu, equal >> j & 1);
+      e += __popc(of_all & lanes_before), equal_before += __popc(of_all);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool is_more = more >> j & 1, is_equal = equal >> j & 1;
-      if (is_more || (is_equal && e < need)) kept[m + min(e, need)] = t0 + i + 4 * lane + j;
+      if (is_more || (is_equal && e < need)) kept[m + min(e, need)] = t + j;
       m += is_more, e += is_equal;
     }
-    const int all_lanes = __shfl_sync(0xffffffffu, upto, 31);
-    more_before += all_lanes & 0xffff, equal_before += all_lanes >> 16;
   }
-  cluster.sync();  // no CTA leaves while another reads its counts
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its counts
 }
 
 // A CTA copies kRows kept tokens of a row (sequence and head): first a
@@ -371,7 +413,7 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   // whose keys shared memory cannot hold is read again in each pass.
   const int64_t most = (int64_t)a.tab.max_pages * a.c.page_size;
   int cluster = 1;
-  while (most > 12288 && cluster < 8 && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384)) cluster *= 2;
+  while (most > 12288 && cluster < kMostCtas && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384)) cluster *= 2;
   a.room = (int)std::min<int64_t>(round_up(ceil_div(most, cluster), 4), 48 * 1024);
   a.fours = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
             reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
