@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
   for (int i = i0; i < i1; i += 128) {
     uint32_t more, equal;
     classes(i + 4 * lane, more, equal);
+    if (held && i + 4 * lane < i1) keys[i + 4 * lane] = more | equal << 4;  // in place of the keys
     mores += __popc(more), equals += __popc(equal);
   }
   mores = __reduce_add_sync(0xffffffffu, mores), equals = __reduce_add_sync(0xffffffffu, equals);
@@ -285,35 +286,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
   if (lane < rank) more_before += *cluster.map_shared_rank(&s_more, lane), equal_before += *cluster.map_shared_rank(&s_equal, lane);
   more_before = __reduce_add_sync(0xffffffffu, more_before), equal_before = __reduce_add_sync(0xffffffffu, equal_before);
   const uint32_t lanes_before = (1u << lane) - 1;
+  int at = more_before + min(equal_before, need);  // what a warp keeps is one run of `kept`
   for (int i = i0; i < i1; i += 128) {
     uint32_t more, equal;
-    classes(i + 4 * lane, more, equal);
-    const int t = t0 + i + 4 * lane;
-    int m = more_before;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t of_all = __ballot_sync(0xffffffffu, more >> j & 1);
-      m += __popc(of_all & lanes_before), more_before += __popc(of_all);
+    if (held) {
+      const uint32_t both = i + 4 * lane < i1 ? keys[i + 4 * lane] : 0;
+      more = both & 15, equal = both >> 4;
+    } else {
+      classes(i + 4 * lane, more, equal);
     }
-    if (!__any_sync(0xffffffffu, equal)) {
-      m += min(equal_before, need);
+    const int t = t0 + i + 4 * lane;
+    if (__any_sync(0xffffffffu, equal)) {  // the first `need` of them stay
+      int e = equal_before;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t of_all = __ballot_sync(0xffffffffu, equal >> j & 1);
+        e += __popc(of_all & lanes_before), equal_before += __popc(of_all);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (more >> j & 1) kept[m++] = t + j;
-      continue;
+        if (equal >> j & 1) more |= (uint32_t)(e++ < need) << j;
     }
-    int e = equal_before;
+    const int own = __popc(more);  // 0 to 4: three votes add them up
+    int m = at;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t of_all = __ballot_sync(0xffffffffu, equal >> j & 1);
-      e += __popc(of_all & lanes_before), equal_before += __popc(of_all);
+    for (int j = 0; j < 3; ++j) {
+      const uint32_t of_all = __ballot_sync(0xffffffffu, own >> j & 1);
+      m += __popc(of_all & lanes_before) << j, at += __popc(of_all) << j;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool is_more = more >> j & 1, is_equal = equal >> j & 1;
-      if (is_more || (is_equal && e < need)) kept[m + min(e, need)] = t + j;
-      m += is_more, e += is_equal;
-    }
+    for (int j = 0; j < 4; ++j)
+      if (more >> j & 1) kept[m++] = t + j;
   }
   if (C > 1) cluster.sync();  // no CTA leaves while another reads its counts
 }
