@@ -118,9 +118,9 @@ __device__ __forceinline__ void hold(const Args& a, const int32_t* pages, const 
 // cluster's counts and pick the digit in which the wanted rank falls.  The
 // kept indices then follow from counts of the tokens before, in order.  A
 // pass whose digit is taken whole is the last: two passes mostly do.
-// 512 threads of 64 registers, two CTAs to an SM (256 rows of 8192 tokens: 17
-// us, against 22 with 1024); 128 threads where the rows are
-// short and more than that.
+// 512 threads of 64 registers, two CTAs to an SM (256 rows of 8192 tokens: 14
+// us, of which 4 until the keys are there; 1024 threads took a quarter longer);
+// 128 threads where the rows are short and more than that.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const __grid_constant__ Args a) {
   constexpr int kThreads = THREADS, kWarps = kThreads / 32, kDigits = kBins / kThreads;
@@ -409,14 +409,17 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   a.status = device_status_word();
   if (!a.status) return fail(I8Q_ERR_CUDA, "kv_evict: no status word");
   cudaStream_t s = as_stream(stream);
-  // Long rows: as many CTAs to a row as give every SM one, or keep a share
-  // within 16K tokens, up to the portable 8 (8 rows of 131072 tokens took three
-  // times as long in clusters of 16).  A CTA takes 1 us per 1000 tokens and a
-  // cluster 6 us of its own, so rows up to 12288 tokens have one CTA.  A share
-  // whose keys shared memory cannot hold is read again in each pass.
+  // Long rows have as many CTAs, up to the portable 8, as fit the SMs twice
+  // over (8 rows of 131072 tokens took three times as long in clusters of 16):
+  // a CTA takes 0.6 us per 1000 tokens, a cluster 4 us of its own.  So rows up
+  // to 12288 tokens have one CTA, and many rows too, while two CTAs' keys fit
+  // an SM (24K each): 256 rows of 18000 tokens 31 us, in clusters of two 42.  A
+  // share whose keys shared memory cannot hold is read again in each pass.
   const int64_t most = (int64_t)a.tab.max_pages * a.c.page_size;
   int cluster = 1;
-  while (most > 12288 && cluster < kMostCtas && (heads * cluster < sm_count() || ceil_div(most, cluster) > 16384)) cluster *= 2;
+  while (most > 12288 && cluster < kMostCtas &&
+         (heads * cluster * 2 <= sm_count() || ceil_div(most, cluster) > 24 * 1024))
+    cluster *= 2;
   a.room = (int)std::min<int64_t>(round_up(ceil_div(most, cluster), 4), 48 * 1024);
   a.fours = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
             reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;

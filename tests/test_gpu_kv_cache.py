@@ -736,6 +736,21 @@ def test_evict_lengths(dev, n, budget):
     check_evict(dev, [n, n // 3], budget, 4, 33, 2, 16, 16, "s8", seed=n)
 
 
+@pytest.mark.parametrize("rows", [1, 10, 20, 40])
+@pytest.mark.parametrize("kind", ["drawn", "two"])
+def test_evict_long_rows_by_one_to_eight_blocks(dev, rows, kind):
+    # (of two values, so that many equal ones are taken in order across the blocks of a row)
+    lens = [int(x) for x in np.random.default_rng(rows).integers(9000, 13500, rows)]
+    lens[0] = 13501
+    check_evict(dev, lens, 5000, 5, 100, 2, 16, 20, "s8", seed=rows,
+                change=(lambda c, t: c.score.copy_((c.score > 0.7).float())) if kind == "two" else None)
+
+
+@pytest.mark.parametrize("sink,recent", [(4, 33), (0, 0), (300, 700)])
+def test_evict_more_keys_than_shared_memory_holds(dev, sink, recent):
+    check_evict(dev, [400000], 1000, sink, recent, 1, 16, 256, "s8", seed=sink)
+
+
 def test_evict_many(dev):
     r = np.random.default_rng(0)
     check_evict(dev, [int(x) for x in r.integers(0, 90, 400)], 24, 2, 5, 2, 16, 8, "bf16")
