@@ -179,37 +179,7 @@ __device__ __forceinline__ void add_scores(const Args& a, int block, int blocks)
         const float z = a.stats[h0 + i];
         return z == -INFINITY ? INFINITY : z;
       };
-      const int t_end = min((tile0 + end) * 16, len);
-      for (int t = (tile0 + begin) * 16 + lane * V; t < t_end; t += 32 * V) {
-        if (t + V <= first) continue;
-        int page, off;
-        if (!kv::find(c, a.tab, b, t, page, off, a.status)) continue;
-        float* score = c.score + kv::scale_at(c, page, kvh, off);
-        const float* logit = a.logits + h0 * a.logit_pitch + t;
-        float p[V] = {};
-        // a logit outside the sequence or its window is -infinity: no weight
-        if constexpr (V == 4) {
-          float4 s = *reinterpret_cast<const float4*>(score);
-#pragma unroll 4
-          for (int i = 0; i < a.group; ++i) {
-            const float r = log_of(i);
-            const float4 l = __ldcs(reinterpret_cast<const float4*>(logit + i * a.logit_pitch));
-            p[0] += ex2_approx(l.x - r), p[1] += ex2_approx(l.y - r);
-            p[2] += ex2_approx(l.z - r), p[3] += ex2_approx(l.w - r);
-          }
-          if (t >= first) s.x += p[0];
-          if (t + 1 >= first && t + 1 < len) s.y += p[1];
-          if (t + 2 >= first && t + 2 < len) s.z += p[2];
-          if (t + 3 >= first && t + 3 < len) s.w += p[3];
-          *reinterpret_cast<float4*>(score) = s;
-        } else {
-#pragma unroll 4
-          for (int i = 0; i < a.group; ++i) {
-            p[0] += ex2_approx(logit[i * a.logit_pitch] - log_of(i));
-          }
-          *score += p[0];
-        }
-      }
+      add_weights<V>(a, b, kvh, first, len, (tile0 + begin) * 16, min((tile0 + end) * 16, len), lane, log_of);
       if constexpr (HERE) __syncwarp();  // (the next row's logs go to the same place)
     }
   }
@@ -254,10 +224,10 @@ Kernel join_of(int dp) {
   return dp == 64 ? join_kernel<QT, 64, S> : dp == 128 ? join_kernel<QT, 128, S> : join_kernel<QT, 256, S>;
 }
 template <class QT, int S>
-KernelAt join_and_score_of(int dp, bool four) {
-  if (dp == 64) return four ? join_and_score_kernel<QT, 64, S, 4> : join_and_score_kernel<QT, 64, S, 1>;
-  if (dp == 128) return four ? join_and_score_kernel<QT, 128, S, 4> : join_and_score_kernel<QT, 128, S, 1>;
-  return four ? join_and_score_kernel<QT, 256, S, 4> : join_and_score_kernel<QT, 256, S, 1>;
+KernelAt join_and_score_of(int dp, bool fours) {
+  if (dp == 64) return fours ? join_and_score_kernel<QT, 64, S, 4> : join_and_score_kernel<QT, 64, S, 1>;
+  if (dp == 128) return fours ? join_and_score_kernel<QT, 128, S, 4> : join_and_score_kernel<QT, 128, S, 1>;
+  return fours ? join_and_score_kernel<QT, 256, S, 4> : join_and_score_kernel<QT, 256, S, 1>;
 }
 
 struct Layout {
@@ -362,8 +332,8 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   if (!a.status) return fail(I8Q_ERR_CUDA, "paged_attention: no status word");
   cudaStream_t s = as_stream(stream);
   const Table all = a.tab;
-  const bool four = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
-                    reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
+  a.fours = a.c.page_size % 4 == 0 && a.c.s_token == 1 && a.c.s_page % 4 == 0 && a.c.s_head % 4 == 0 &&
+            reinterpret_cast<uintptr_t>(a.c.score) % 16 == 0;
   for (int b0 = 0; b0 < all.sequences; b0 += slice) {
     a.tab = Table{all.page + b0 * all.stride, all.stride, std::min(slice, all.sequences - b0), all.max_pages};
     a.lengths = lengths + b0;
@@ -383,9 +353,9 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     if (!a.per_row && accumulate && a.group <= 32 && tokens <= 1 << 21) {
       I8Q_PROF("paged_attention_join_and_scores", s);
       const KernelAt kernel = type == I8Q_F32
-                                  ? (few ? join_and_score_of<float, 8>(l.dp, four) : join_and_score_of<float, 1>(l.dp, four))
-                                  : (few ? join_and_score_of<__nv_bfloat16, 8>(l.dp, four)
-                                         : join_and_score_of<__nv_bfloat16, 1>(l.dp, four));
+                                  ? (few ? join_and_score_of<float, 8>(l.dp, a.fours) : join_and_score_of<float, 1>(l.dp, a.fours))
+                                  : (few ? join_and_score_of<__nv_bfloat16, 8>(l.dp, a.fours)
+                                         : join_and_score_of<__nv_bfloat16, 1>(l.dp, a.fours));
       rc = kv::launch(kernel, joins + scores, 256, 0, 1, s, "paged_attention_join_and_scores", a, (int)joins);
       if (rc != I8Q_OK) return rc;
       continue;
@@ -397,9 +367,9 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
       rc = kv::launch(join, joins, 256, 0, 1, s, "paged_attention_join", a);
       if (rc != I8Q_OK) return rc;
     }
-    if (accumulate) {
+    if (accumulate && !a.scores_here) {
       I8Q_PROF("paged_attention_scores", s);
-      rc = kv::launch(four ? score_kernel<4> : score_kernel<1>, scores, 256, 0, 1, s, "paged_attention_scores", a);
+      rc = kv::launch(a.fours ? score_kernel<4> : score_kernel<1>, scores, 256, 0, 1, s, "paged_attention_scores", a);
       if (rc != I8Q_OK) return rc;
     }
   }

@@ -90,6 +90,8 @@ struct Args {
   float* logits;               // [sequences][q_heads][logit_pitch], or null
   int64_t logit_pitch;
   float* stats;                // [sequences][q_heads] m + log2 l (with logits)
+  int fours;                   // scores of four neighbouring tokens can be read at once
+  int scores_here;             // the first kernel adds the scores: its rows are whole and have all heads that share a key
   uint32_t* status;
 };
 
@@ -345,6 +347,45 @@ __device__ __forceinline__ void put_part(const Args& a, int64_t part, int lane, 
     if (e * 128 + lane * 4 < DP) *reinterpret_cast<float4*>(a.part_out + part * DP + e * 128 + lane * 4) = o[e];
 }
 
+// score of tokens begin .. end - 1 of sequence b, V at a time a lane, += their
+// weights, summed over the query heads that share key/value head kvh; log_of(i):
+// the log2 of the sum of exponentials of the i-th of them, infinite where there
+// is no weight.
+template <int V, class LogOf>
+__device__ __forceinline__ void add_weights(const Args& a, int b, int kvh, int first, int len, int begin, int end,
+                                            int lane, LogOf&& log_of) {
+  const Cache& c = a.c;
+  const int64_t h0 = (int64_t)b * a.q_heads + kvh * a.group;
+  for (int t = begin + lane * V; t < end; t += 32 * V) {
+    if (t + V <= first) continue;
+    int page, off;
+    if (!kv::find(c, a.tab, b, t, page, off, a.status)) continue;
+    float* score = c.score + kv::scale_at(c, page, kvh, off);
+    const float* logit = a.logits + h0 * a.logit_pitch + t;
+    float p[V] = {};
+    // a logit outside the sequence or its window is -infinity: no weight
+    if constexpr (V == 4) {
+      float4 s = *reinterpret_cast<const float4*>(score);
+#pragma unroll 4
+      for (int i = 0; i < a.group; ++i) {
+        const float r = log_of(i);
+        const float4 l = __ldcs(reinterpret_cast<const float4*>(logit + i * a.logit_pitch));
+        p[0] += ex2_approx(l.x - r), p[1] += ex2_approx(l.y - r);
+        p[2] += ex2_approx(l.z - r), p[3] += ex2_approx(l.w - r);
+      }
+      if (t >= first) s.x += p[0];
+      if (t + 1 >= first && t + 1 < len) s.y += p[1];
+      if (t + 2 >= first && t + 2 < len) s.z += p[2];
+      if (t + 3 >= first && t + 3 < len) s.w += p[3];
+      *reinterpret_cast<float4*>(score) = s;
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < a.group; ++i) p[0] += ex2_approx(logit[i * a.logit_pitch] - log_of(i));
+      *score += p[0];
+    }
+  }
+}
+
 // WHOLE: rows are not cut (warps_per_row), else they follow the line.
 template <class F, bool WHOLE>
 __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_constant__ Args a) {
@@ -366,7 +407,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 
   // ---- the line: where each sequence starts ----
   if (lane == 0) open_row[warp] = -1;
-  if (!WHOLE || (a.logits && blockIdx.x == 0)) {  // (the scores' kernel follows it too)
+  if (!WHOLE || (a.logits && !a.scores_here && blockIdx.x == 0)) {  // (the scores' kernel follows it too)
     int run = 0;
     for (int b0 = 0; b0 < B; b0 += F::W * 32) {
       const int b = b0 + threadIdx.x;
@@ -892,41 +933,58 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   // ---- rows left open: neighbours of one row are joined, in the order of the line ----
   __syncthreads();
   const int mine = open_row[warp];
-  if (mine < 0) return;
-  int from = warp, to = warp;
-  while (from > 0 && open_row[from - 1] == mine) --from;
-  while (to + 1 < F::W && open_row[to + 1] == mine) ++to;
-  const int heads = min(8 * NT, a.group - mine % R % a.chunks * (8 * NT));
+  if (mine >= 0) {
+    int from = warp, to = warp;
+    while (from > 0 && open_row[from - 1] == mine) --from;
+    while (to + 1 < F::W && open_row[to + 1] == mine) ++to;
+    const int heads = min(8 * NT, a.group - mine % R % a.chunks * (8 * NT));
 #pragma unroll 1
-  for (int hh = warp - from; hh < heads; hh += to - from + 1) {
-    float top = -INFINITY, sum = 0.0f;
+    for (int hh = warp - from; hh < heads; hh += to - from + 1) {
+      float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-    for (int i = from; i <= to; ++i) top = fmaxf(top, open_stats[i * 8 * NT + hh].x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float4 acc[F::E];
+      for (int i = from; i <= to; ++i) top = fmaxf(top, open_stats[i * 8 * NT + hh].x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float4 acc[F::E];
 #pragma unroll
-    for (int e = 0; e < F::E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int e = 0; e < F::E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int i = from; i <= to; ++i) {
-      const float2 st = open_stats[i * 8 * NT + hh];
-      const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
-      sum = fmaf(st.y, f, sum);
-      const float* part = reinterpret_cast<const float*>(smem + i * F::WARP_BYTES) + hh * F::DP;
+      for (int i = from; i <= to; ++i) {
+        const float2 st = open_stats[i * 8 * NT + hh];
+        const float f = ex2_approx(st.x - ref);  // a part without weight: 2^-infinity, or o and l of 0
+        sum = fmaf(st.y, f, sum);
+        const float* part = reinterpret_cast<const float*>(smem + i * F::WARP_BYTES) + hh * F::DP;
 #pragma unroll
-      for (int e = 0; e < F::E; ++e)
-        if (e * 128 + lane * 4 < F::DP) {
-          const float4 v = *reinterpret_cast<const float4*>(part + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
-          acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
-          acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
-        }
+        for (int e = 0; e < F::E; ++e)
+          if (e * 128 + lane * 4 < F::DP) {
+            const float4 v = *reinterpret_cast<const float4*>(part + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
+            acc[e].x = fmaf(v.x, f, acc[e].x), acc[e].y = fmaf(v.y, f, acc[e].y);
+            acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
+          }
+      }
+      if constexpr (WHOLE) {  // that was the row
+        const int in_b = mine % R;
+        finish_row<QT, F::DP>(a, mine / R, in_b / a.chunks * a.group + in_b % a.chunks * (8 * NT) + hh, lane, top, sum, acc);
+      } else {
+        put_part<F::DP>(a, ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh, lane, top,
+                        sum, acc);
+      }
     }
-    if constexpr (WHOLE) {  // that was the row
-      const int in_b = mine % R;
-      finish_row<QT, F::DP>(a, mine / R, in_b / a.chunks * a.group + in_b % a.chunks * (8 * NT) + hh, lane, top, sum, acc);
-    } else {
-      put_part<F::DP>(a, ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh, lane, top,
-                      sum, acc);
-    }
+  }
+
+  // ---- the scores, where whole rows are here: a warp's share is the tokens that it has seen ----
+  if constexpr (WHOLE) {
+    if (!a.scores_here) return;
+    __syncthreads();  // the sums and logits of the CTA's warps
+    if (row_id >= B * R) return;
+    const int seq = row_id / R, kvh = row_id - seq * R, part = warp % a.per_row;
+    const int len = kv::cut_length(c, a.tab, a.lengths[seq], a.status);
+    const int first = first_token(a, len), tiles = tile_count(a, len);
+    const int t0 = (first / 16 + tiles * part / a.per_row) * 16;
+    const int t1 = min((first / 16 + tiles * (part + 1) / a.per_row) * 16, len);
+    const float* sum = a.stats + (int64_t)seq * a.q_heads + kvh * a.group;
+    auto log_of = [&](int i) { return sum[i] == -INFINITY ? INFINITY : sum[i]; };
+    if (a.fours) add_weights<4>(a, seq, kvh, first, len, t0, t1, lane, log_of);
+    else add_weights<1>(a, seq, kvh, first, len, t0, t1, lane, log_of);
   }
 }
 
@@ -935,8 +993,9 @@ int launch_attend(Args& a, cudaStream_t s) {
   a.ctas = sm_count(), a.warps = F::W;
   a.step_bytes = a.token_bytes * 32 / F::CR;
   // (no sequence can be longer than its row of the table)
-  a.per_row = warps_per_row(F::W, a.ctas, (int64_t)a.tab.sequences * a.c.heads * a.chunks,
-                            ceil_div((int64_t)a.tab.max_pages * a.c.page_size, 16));
+  const int64_t longest = ceil_div((int64_t)a.tab.max_pages * a.c.page_size, 16);
+  a.per_row = warps_per_row(F::W, a.ctas, (int64_t)a.tab.sequences * a.c.heads * a.chunks, longest);
+  a.scores_here = a.per_row && a.logits && a.chunks == 1;
   I8Q_PROF("paged_attention", s);
   return a.per_row ? kv::launch(attend_kernel<F, true>, (unsigned)a.ctas, F::W * 32, F::SMEM, 1, s, "paged_attention", a)
                    : kv::launch(attend_kernel<F, false>, (unsigned)a.ctas, F::W * 32, F::SMEM, 1, s, "paged_attention", a);
