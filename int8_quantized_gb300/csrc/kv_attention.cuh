@@ -992,8 +992,9 @@ template <class F>
 int launch_attend(Args& a, cudaStream_t s) {
   a.ctas = sm_count(), a.warps = F::W;
   a.step_bytes = a.token_bytes * 32 / F::CR;
-  // (no sequence can be longer than its row of the table)
-  const int64_t longest = ceil_div((int64_t)a.tab.max_pages * a.c.page_size, 16);
+  // (no sequence can be longer than its row of the table, and a window may begin and end inside a tile)
+  int64_t longest = ceil_div((int64_t)a.tab.max_pages * a.c.page_size, 16);
+  if (a.window) longest = std::min<int64_t>(longest, a.window / 16 + 2);
   a.per_row = warps_per_row(F::W, a.ctas, (int64_t)a.tab.sequences * a.c.heads * a.chunks, longest);
   a.scores_here = a.per_row && a.logits && a.chunks == 1;
   I8Q_PROF("paged_attention", s);

@@ -235,6 +235,23 @@ def test_attention_cut_rows_scores_in_one_launch_or_two(dev, G, page, B):
                         extra=extra // B)
 
 
+@pytest.mark.parametrize("G", [1, 9, 32, 33])
+@pytest.mark.parametrize("page", [6, 16])
+@pytest.mark.parametrize("extra", [4000, 140000])
+def test_attention_cut_rows_scores_without_window(dev, G, page, extra):
+    check_attention(dev, [900, 0, 77] * 3, 2 * G, 2, 64, page, "bf16", "s8", accumulate=True, extra=extra // 3)
+
+
+@pytest.mark.parametrize("cache,qtype", [("s8", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("page", [7, 16])
+@pytest.mark.parametrize("window", [1, 16, 17, 1000, 4500])
+@pytest.mark.parametrize("G", [4, 20])
+def test_attention_windows_of_long_sequences(dev, G, window, page, cache, qtype):
+    """Windows within what a block takes whole, and above."""
+    check_attention(dev, [5003, 0, 9000, 100, 16, 999], G, 1, 80, page, qtype, cache, window=window, seed=window,
+                    accumulate=True, extra=1000)
+
+
 def test_attention_cut_rows_over_many_sequences(dev):
     r = np.random.default_rng(5)
     check_attention(dev, [int(x) for x in r.integers(0, 200, 700)], 4, 2, 64, 16, "bf16", "s8", accumulate=True,
