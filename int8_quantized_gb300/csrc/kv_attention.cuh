@@ -37,14 +37,16 @@
 // the rows form one line, cut into equal parts, one per warp.  A row that
 // lies in one part is finished by that warp.  Of the others the warps of a
 // CTA join what they have in shared memory, leave m, l and o in the
-// workspace, and a second kernel joins those.  The split follows from the
-// lengths alone, so results repeat.
+// workspace, and a second kernel joins those.  Rows that cannot be long are not
+// cut: a CTA has them whole, or a cluster one, and there is no second kernel.
+// The split follows from the sizes and lengths alone, so results repeat.
 //
 // Measured: one sequence of 131072 tokens, 8 heads of 128, int8, 32 query
 // heads: 60 us a call, 277 MB, its tiles streaming at 6.5 TB/s between 5 us of
 // start and 6 of end; 64 sequences of 8192 with scores: 231 us, 1.14 GB.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -66,7 +68,8 @@ struct Heads {  // [sequences][heads][dim], strides in elements
 constexpr int kMaxSequences = 2048;  // of one launch: their line positions lie in shared memory
 constexpr int kRowCost = 4;          // of a row's start and end, in tiles
 constexpr int kMinPart = 4;          // tiles of a part of a row that is cut
-constexpr int kShort = 12;           // tiles a warp, up to which a CTA keeps whole rows
+constexpr int kShort = 12;           // tiles a warp, up to which rows may stay whole
+constexpr int kMostCtas = 8;         // of a cluster
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -84,6 +87,7 @@ struct Args {
   int heads_per_row;           // of a partial: 8 or 16
   int ctas, warps;             // of the first kernel
   int per_row;                 // warps that share a row, where rows are not cut; else 0
+  int cluster;                 // CTAs that share one then
   int* line;                   // [sequences + 1] start of each sequence on the line
   float2* part_stats;          // [ctas * warps][2][heads_per_row] (m, l)
   float* part_out;             // [ctas * warps][2][heads_per_row][dp]
@@ -122,13 +126,30 @@ __device__ __forceinline__ Cut cut_line(const Args& a, int n, int rows) {
   return c;
 }
 
-// Short rows: a CTA keeps whole rows, `k` warps (a divisor of its number) to
-// each, so that nothing is left to join.  0: a row may be too long for that,
-// or there are too many rows.
-inline int warps_per_row(int warps, int ctas, int64_t rows, int64_t longest) {
-  int k = warps;
+// Short rows: a CTA keeps whole rows, `per_row` warps (a divisor of its number)
+// to each, or a cluster of CTAs has one and joins its parts through their
+// shared memory, so that one launch does it all (one sequence of 4000 tokens, 4
+// heads: 11.6 us instead of 14.5, and with scores 13.7 instead of 21.5; of
+// 2000: 11.1, where one CTA a row took 18.5).  A tile a warp takes 1.2 us with a
+// CTA's warps all at work, somewhat more for fp32 queries; what cut rows need
+// more is worth 5 tiles (with scores 7; fp32 4 and 5), less one for a cluster's
+// exchange, and each SM has its even share of tiles then.  So rows stay whole while they have no
+// more tiles a warp than that, and no more than kShort: the table may be wider
+// than its sequences are long, some SMs' rows longer than others'.
+// per_row 0: a row may be too long for that, or there are too many rows.
+struct Share {
+  int per_row, cluster;
+};
+inline Share share_rows(int warps, int ctas, int64_t rows, int64_t longest, bool scores, bool wide) {
+  int k = warps, cluster = 1;
   while (k > 1 && (warps % k || rows > (int64_t)ctas * (warps / k))) --k;
-  return rows <= (int64_t)ctas * (warps / k) && longest <= k * kShort ? k : 0;
+  // (5 / 6: clusters of 8 do not fill every group of SMs)
+  while (k == warps && cluster < kMostCtas && rows * cluster * 2 <= ctas * 5 / 6 && longest > 2 * cluster * warps)
+    cluster *= 2;
+  const int64_t each = ceil_div(longest, (int64_t)k * cluster), even = rows * longest / ((int64_t)ctas * warps);
+  const int64_t most = std::min<int64_t>(kShort, even + (wide ? 4 + scores : 5 + 2 * scores) - (cluster > 1));
+  if (rows > (int64_t)ctas * (warps / k) || each > most) return {0, 1};
+  return {k * cluster, cluster};
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -386,12 +407,16 @@ __device__ __forceinline__ void add_weights(const Args& a, int b, int kvh, int f
   }
 }
 
-// WHOLE: rows are not cut (warps_per_row), else they follow the line.
-template <class F, bool WHOLE>
+// CUT: the rows follow the line; WHOLE: a CTA has whole rows, SHARED: a cluster
+// has one (share_rows).  (One kernel for the last two cost every short call 0.4
+// us.)
+enum Split { CUT, WHOLE, SHARED };
+template <class F, Split SPLIT>
 __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_constant__ Args a) {
   using QT = typename F::QT;
   constexpr bool S8 = F::S8;
   constexpr int NT = F::NT;
+  constexpr bool LINE = SPLIT == CUT;
   extern __shared__ __align__(16) unsigned char smem[];
   int* line = reinterpret_cast<int*>(smem + F::W * F::WARP_BYTES);
   float2* open_stats = reinterpret_cast<float2*>(line + kMaxSequences + 4);  // [W][8 NT], 16-byte aligned
@@ -407,7 +432,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 
   // ---- the line: where each sequence starts ----
   if (lane == 0) open_row[warp] = -1;
-  if (!WHOLE || (a.logits && !a.scores_here && blockIdx.x == 0)) {  // (the scores' kernel follows it too)
+  if (LINE || (a.logits && !a.scores_here && blockIdx.x == 0)) {  // (the scores' kernel follows it too)
     int run = 0;
     for (int b0 = 0; b0 < B; b0 += F::W * 32) {
       const int b = b0 + threadIdx.x;
@@ -438,10 +463,12 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       for (int b = threadIdx.x; b <= B; b += F::W * 32) a.line[b] = line[b];
   }
   // where this warp begins: units x .. x_end of the line, or its part of row `row_id`
-  const int row_id = WHOLE ? warp / a.per_row * a.ctas + blockIdx.x : 0;
+  const int rank = SPLIT == SHARED ? blockIdx.x % a.cluster : 0;  // in the cluster
+  const int row_id = LINE ? 0 : SPLIT == SHARED ? blockIdx.x / a.cluster : warp / a.per_row * a.ctas + blockIdx.x;
+  const int row_part = LINE ? 0 : SPLIT == SHARED ? rank * F::W + warp : warp % a.per_row;
   Cut cut{};
   int w = 0, x = 0, x_end = 0, b = 0;
-  if constexpr (WHOLE) {
+  if constexpr (!LINE) {
     x_end = row_id < B * R;
     b = row_id / R;
   } else {
@@ -470,7 +497,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
   const int D = c.dim;
 
   for (; x < x_end; ++b) {
-    const int b_end = WHOLE ? x_end : min(line[b + 1], x_end);
+    const int b_end = !LINE ? x_end : min(line[b + 1], x_end);
     const int len = kv::cut_length(c, a.tab, a.lengths[b], a.status);
     const int first = first_token(a, len), tile0 = first / 16;
     const int cost = tile_count(a, len) + kRowCost;
@@ -478,10 +505,10 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
     while (x < b_end) {
       int row, begin, end, seg_end;
       bool starts, ends;
-      if constexpr (WHOLE) {
-        const int part = warp % a.per_row, tiles = cost - kRowCost;
+      if constexpr (!LINE) {
+        const int tiles = cost - kRowCost;
         row = row_id - b * R;
-        begin = tiles * part / a.per_row, end = tiles * (part + 1) / a.per_row;
+        begin = tiles * row_part / a.per_row, end = tiles * (row_part + 1) / a.per_row;
         starts = ends = a.per_row == 1;
         seg_end = x_end;
       } else {
@@ -961,9 +988,17 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             acc[e].z = fmaf(v.z, f, acc[e].z), acc[e].w = fmaf(v.w, f, acc[e].w);
           }
       }
-      if constexpr (WHOLE) {  // that was the row
+      if constexpr (SPLIT == WHOLE) {  // that was the row
         const int in_b = mine % R;
         finish_row<QT, F::DP>(a, mine / R, in_b / a.chunks * a.group + in_b % a.chunks * (8 * NT) + hh, lane, top, sum, acc);
+      } else if constexpr (SPLIT == SHARED) {  // the CTA's part of it, in the place of the first warp's
+        __syncwarp();
+        if (lane == 0) open_stats[hh] = make_float2(top, sum);
+#pragma unroll
+        for (int e = 0; e < F::E; ++e)
+          if (e * 128 + lane * 4 < F::DP)
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + hh * F::DP +
+                                       ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4))) = acc[e];
       } else {
         put_part<F::DP>(a, ((int64_t)(blockIdx.x * cut.per_cta + from) * 2 + open_head[from]) * (8 * NT) + hh, lane, top,
                         sum, acc);
@@ -971,16 +1006,56 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
     }
   }
 
+  // ---- the parts of a cluster's CTAs, a warp of any of them per head ----
+  if constexpr (SPLIT == SHARED) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int seq = row_id / R, in_b = row_id - seq * R, chunk = in_b % a.chunks * (8 * NT);
+    const int heads = min(8 * NT, a.group - chunk);
+    cluster.sync();
+#pragma unroll 1
+    for (int hh = rank * F::W + warp; hh < heads; hh += a.cluster * F::W) {
+      float2 st = make_float2(-INFINITY, 0.0f);
+      if (lane < a.cluster) st = cluster.map_shared_rank(open_stats, lane)[hh];
+      float top = st.x;
+#pragma unroll
+      for (int i = 1; i < kMostCtas; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      top = __shfl_sync(0xffffffffu, top, 0);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float f = ex2_approx(st.x - ref);
+      float sum = 0.0f;
+      float4 acc[F::E];
+#pragma unroll
+      for (int e = 0; e < F::E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < kMostCtas; ++r) {
+        if (r >= a.cluster) break;
+        const float fr = __shfl_sync(0xffffffffu, f, r);
+        sum = fmaf(__shfl_sync(0xffffffffu, st.y, r), fr, sum);
+        const float* part = reinterpret_cast<const float*>(cluster.map_shared_rank(smem, r)) + hh * F::DP;
+#pragma unroll
+        for (int e = 0; e < F::E; ++e)
+          if (e * 128 + lane * 4 < F::DP) {
+            const float4 v = *reinterpret_cast<const float4*>(part + ((e * 128 + lane * 4) ^ (hh / 2 % 4 * 4)));
+            acc[e].x = fmaf(v.x, fr, acc[e].x), acc[e].y = fmaf(v.y, fr, acc[e].y);
+            acc[e].z = fmaf(v.z, fr, acc[e].z), acc[e].w = fmaf(v.w, fr, acc[e].w);
+          }
+      }
+      finish_row<QT, F::DP>(a, seq, in_b / a.chunks * a.group + chunk + hh, lane, top, sum, acc);
+    }
+    cluster.sync();  // no CTA leaves while another reads its part; and the sums are there for the scores
+  }
+
   // ---- the scores, where whole rows are here: a warp's share is the tokens that it has seen ----
-  if constexpr (WHOLE) {
+  if constexpr (!LINE) {
     if (!a.scores_here) return;
     __syncthreads();  // the sums and logits of the CTA's warps
     if (row_id >= B * R) return;
-    const int seq = row_id / R, kvh = row_id - seq * R, part = warp % a.per_row;
+    const int seq = row_id / R, kvh = row_id - seq * R;
     const int len = kv::cut_length(c, a.tab, a.lengths[seq], a.status);
     const int first = first_token(a, len), tiles = tile_count(a, len);
-    const int t0 = (first / 16 + tiles * part / a.per_row) * 16;
-    const int t1 = min((first / 16 + tiles * (part + 1) / a.per_row) * 16, len);
+    const int t0 = (first / 16 + tiles * row_part / a.per_row) * 16;
+    const int t1 = min((first / 16 + tiles * (row_part + 1) / a.per_row) * 16, len);
     const float* sum = a.stats + (int64_t)seq * a.q_heads + kvh * a.group;
     auto log_of = [&](int i) { return sum[i] == -INFINITY ? INFINITY : sum[i]; };
     if (a.fours) add_weights<4>(a, seq, kvh, first, len, t0, t1, lane, log_of);
@@ -995,11 +1070,14 @@ int launch_attend(Args& a, cudaStream_t s) {
   // (no sequence can be longer than its row of the table, and a window may begin and end inside a tile)
   int64_t longest = ceil_div((int64_t)a.tab.max_pages * a.c.page_size, 16);
   if (a.window) longest = std::min<int64_t>(longest, a.window / 16 + 2);
-  a.per_row = warps_per_row(F::W, a.ctas, (int64_t)a.tab.sequences * a.c.heads * a.chunks, longest);
+  const int64_t rows = (int64_t)a.tab.sequences * a.c.heads * a.chunks;
+  const Share share = share_rows(F::W, a.ctas, rows, longest, a.logits != nullptr, F::WIDE);
+  a.per_row = share.per_row, a.cluster = share.cluster;
   a.scores_here = a.per_row && a.logits && a.chunks == 1;
+  const unsigned blocks = a.cluster > 1 ? (unsigned)(rows * a.cluster) : (unsigned)a.ctas;
   I8Q_PROF("paged_attention", s);
-  return a.per_row ? kv::launch(attend_kernel<F, true>, (unsigned)a.ctas, F::W * 32, F::SMEM, 1, s, "paged_attention", a)
-                   : kv::launch(attend_kernel<F, false>, (unsigned)a.ctas, F::W * 32, F::SMEM, 1, s, "paged_attention", a);
+  const auto kernel = !a.per_row ? attend_kernel<F, CUT> : a.cluster == 1 ? attend_kernel<F, WHOLE> : attend_kernel<F, SHARED>;
+  return kv::launch(kernel, blocks, F::W * 32, F::SMEM, a.cluster, s, "paged_attention", a);
 }
 
 template <class QT, bool S8, int DP>

@@ -252,6 +252,15 @@ def test_attention_windows_of_long_sequences(dev, G, window, page, cache, qtype)
                     accumulate=True, extra=1000)
 
 
+@pytest.mark.parametrize("cache,qtype", [("s8", "bf16"), ("bf16", "bf16"), ("s8", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("D", [64, 112, 256])
+@pytest.mark.parametrize("G", [1, 9, 20])
+def test_attention_rows_shared_by_neighbouring_blocks(dev, G, D, cache, qtype):
+    """Few rows of middling length, by two to eight blocks each."""
+    for lens in ([640], [1500, 0, 37, 2900], [700] * 20):
+        check_attention(dev, lens, G, 1, D, 16, qtype, cache, seed=G, accumulate=True)
+
+
 def test_attention_cut_rows_over_many_sequences(dev):
     r = np.random.default_rng(5)
     check_attention(dev, [int(x) for x in r.integers(0, 200, 700)], 4, 2, 64, 16, "bf16", "s8", accumulate=True,
