@@ -854,6 +854,9 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             l[nt][j] += s[nt][j] + s[nt][2 + j];
           }
 
+        // The next copies go where these keys lie: every lane has read its scales
+        // and the mask by then (votes order no memory).
+        __syncwarp();
         send_values(i + F::AHEAD, free_slot);
         copy_wait<2 * F::AHEAD>();
         __syncwarp();
