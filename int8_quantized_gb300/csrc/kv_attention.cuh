@@ -22,12 +22,14 @@
 //    of 32 bytes, as the fragments lie, held the kernel to 4.3 TB/s);
 //  - the order of the summation index is free, so both operands use the one
 //    in which 16-byte pieces hold a lane's fragments;
-//  - a byte with its sign bit flipped, code + 128, is a subnormal number of
-//    fp16 and of bf16 as it lies: one LOP3 makes two of them.  Keys enter so,
-//    and the sum starts at what the 128s add up to (fp32 queries subtract
-//    them exactly); the query is scaled by a power of two to at most 2.  A
-//    bf16 fma turns two values into exact codes; bf16 because the weights that
-//    multiply them need its range;
+//  - a byte with its sign bit flipped, code + 128, is part of an fp16 or bf16
+//    number as it lies: one LOP3 and one subtraction or fma make two exact
+//    codes.  Keys become fp16, and the query is scaled by a power of two to at
+//    most 2; values become bf16, because the weights that multiply them need
+//    its range.  (Keys entered as code + 128, the 128s taken from the sum, save
+//    the subtraction and no time, but a row with one large channel has codes of
+//    about 1 elsewhere, and their sum kept the rounding of the 128s: 2e-5 of it
+//    at 128 elements.);
 //  - the running maximum moves only when a score exceeds it by 2^8: p stays
 //    below 2^8, and most tiles need no reduction over the lanes;
 //  - value scales multiply p (in fp32) before it is split into bf16 parts.
@@ -194,8 +196,6 @@ __device__ __forceinline__ uint32_t codes_fp16(uint32_t w) {
   asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
   return r;
 }
-//  as fp16 numbers u 2^-24: u alone, the mantissa of a subnormal;
-__device__ __forceinline__ uint32_t codes_raised(uint32_t w) { return (w & 0x00ff00ffu) ^ 0x00800080u; }
 //  as bf16 numbers code 2^-6: u alone is u 2^-133 there (7 bits of mantissa,
 //  the eighth the lowest of the exponent), times 2^127, minus 128 2^-6.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
@@ -220,11 +220,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&r)[N]) {
       if (i + 1 < N) x -= __low2float(h), y -= __high2float(h);
     }
   }
-}
-
-__device__ __forceinline__ float fp16_sum(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return f.x + f.y;
 }
 
 // N consecutive elements of a q row as they lie in memory, and in fp32.
@@ -282,9 +277,6 @@ struct Form {
   // 16 bits, far below its own rounding, since one part's 2^-9 is not.
   static constexpr int NQ = WIDE ? (S8 ? 2 : 3) : 1;
   static constexpr int NP = WIDE ? 3 : 2;
-  // int8 keys as code + 128, the 128 taken from the sum: half the work of
-  // exact codes, for sums rounded at four times their size
-  static constexpr bool RAISED = S8 && !WIDE;
   static constexpr int ES = S8 ? 1 : 2;
   static constexpr int KS = DP / 16;           // steps of the first product
   static constexpr int MT = DP / 16;           // row blocks of the second
@@ -667,7 +659,6 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
       // ---- the query heads, as the columns of the first product ----
       uint2 q_reg[F::Q_REG ? F::NQ * NT * F::KS : 1];
       float factor[NT][2];  // of the scores of heads 2 tig and 2 tig + 1
-      float base[NT][2];    // where their sums start: what the codes' 128 add up to, subtracted
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float v[F::PK][N];
@@ -692,10 +683,8 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < N; ++i) v[j][i] *= down;
         }
-        if constexpr (F::RAISED) f *= 0x1p24f;
         factor[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
         factor[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
-        float total = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < F::KS; ++ks) {
           const float* e = S8 ? &v[ks / 4][ks % 4 * 4] : &v[ks / 2][ks % 2 * 4];
@@ -703,7 +692,6 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           // int8 codes come as (0, 2) and (1, 3) of a word
           split2<S8, F::NQ>(e[0], S8 ? e[2] : e[1], r0);
           split2<S8, F::NQ>(S8 ? e[1] : e[2], e[3], r1);
-          if constexpr (F::RAISED) total += fp16_sum(r0[0]) + fp16_sum(r1[0]);
 #pragma unroll
           for (int i = 0; i < F::NQ; ++i) {
             const int at_q = (i * NT + nt) * F::KS + ks;
@@ -711,13 +699,6 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             else q_smem[at_q * 32] = make_uint2(r0[i], r1[i]);
           }
         }
-        if constexpr (F::RAISED) {
-          total += __shfl_xor_sync(0xffffffffu, total, 1);
-          total += __shfl_xor_sync(0xffffffffu, total, 2);
-          total *= -0x1p-17f;  // -128 2^-24
-        }
-        base[nt][0] = __shfl_sync(0xffffffffu, total, 8 * tig);
-        base[nt][1] = __shfl_sync(0xffffffffu, total, 8 * tig + 4);
       }
 
       // ---- the tiles ----
@@ -746,7 +727,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = F::RAISED ? base[nt][j & 1] : 0.0f, rest[nt][j] = 0.0f;
+          for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f, rest[nt][j] = 0.0f;
 #pragma unroll
         for (int j = 0; j < F::PK; ++j) {
           const unsigned char* piece = slot + (k_at ^ (j & 1) * 64) + j / 2 * 128;  // place(g, j * 4 + tig)
@@ -757,10 +738,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           for (int k = 0; k < (S8 ? 4 : 2); ++k) {
             const int ks = j * (S8 ? 4 : 2) + k;
             uint32_t a0, a1, a2, a3;
-            if constexpr (F::RAISED) {
-              a0 = codes_raised(w0[k]), a2 = codes_raised(w0[k] >> 8);
-              a1 = codes_raised(w1[k]), a3 = codes_raised(w1[k] >> 8);
-            } else if constexpr (S8) {
+            if constexpr (S8) {
               a0 = codes_fp16(w0[k]), a2 = codes_fp16(w0[k] >> 8);
               a1 = codes_fp16(w1[k]), a3 = codes_fp16(w1[k] >> 8);
             } else {

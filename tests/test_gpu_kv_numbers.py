@@ -1,0 +1,78 @@
+"""How exactly attention holds its numbers: inputs on which a cut made on the
+way shows, since ordinary ones hide it behind the outputs' own rounding.
+
+Tolerances, with u = 2^-24.  Scores: a sum of D products in any order, rounded
+or cut at each step, is off by at most 2 D u sum |q k|, and the factors
+(scale, softmax_scale, log2 e) add 4 u |s|.  Weights: the exponential is good
+to 2^-21, and sums of L weights to 2 L u, where nothing else is said."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import int8_quantized_gb300 as q
+from test_gpu_kv_cache import TYPES, U, gen, host, make_cache, make_table, reference_attention
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(dev, c, table, lens, qx, scale=None, accumulate=False, window=0):
+    out, lse = torch.full_like(qx, 7.0), torch.full(qx.shape[:2], 7.0, device=dev)
+    q.paged_attention(c, table, torch.tensor(lens, dtype=torch.int32, device=dev), qx, out, lse=lse,
+                      softmax_scale=scale, accumulate=accumulate, window=window)
+    q.sync_status()
+    return out, lse
+
+
+# ---- scores ----
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_of_keys_with_one_large_channel(dev, D, G, qtype):
+    """Channel 3 takes the whole range of the codes, and the others hold 0, 1
+    and 2 (a row is scaled by its largest element); the query has one sign and
+    elements of 2^-10 to 1.  The sum goes by D / 16 steps of the tensor pipe,
+    each at most 4 u of it off (16 products and what was there, cut to one
+    length), so D / 4 u where the general bound allows 2 D u."""
+    g = gen(D + G)
+    lens = [1, 7, 40, 300]
+    table, pages, _ = make_table(g, dev, lens, 16, extra=1000 if G == 16 else 0)
+    c = make_cache(g, dev, pages, 1, 16, D, "s8")
+    c.k.copy_(torch.randint(0, 3, c.k.shape, generator=g, dtype=torch.int8))
+    c.k[..., 3] = 127
+    c.k_scale.fill_(0.25)
+    qx = torch.exp2(-10 * torch.rand((4, G, D), generator=g)).to(TYPES[qtype]).to(dev)
+    qx[..., 3] = 0
+    before = host(c.score)
+    out, lse = attend(dev, c, table, lens, qx, accumulate=True)
+    _, want, _, err, probs = reference_attention(c, table, lens, qx, 0, D ** -0.5)
+    err *= (D / 4 + 4) / (2 * D + 4)  # (no product is negative: sum |q k| is |s|)
+    off = np.abs(host(lse) - want)
+    tol = err + 2.0 ** -21 + 2 * np.array(lens)[:, None] * U + 2.0 ** -22 * np.abs(want)
+    assert np.all(off <= tol), float((off / tol).max())
+    score, stol = before.copy(), 2.0 ** -22 * np.abs(before)
+    for (b, h), (pg, at, p) in probs.items():
+        score[pg, 0, at] += p
+        stol[pg, 0, at] += p * (3 * err[b, h] + 2.0 ** -20 + 2 * lens[b] * U)
+    off = np.abs(host(c.score) - score)
+    assert np.all(off <= stol), float((off / np.maximum(stol, 1e-30)).max())
+
+
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cache,log2", [("s8", -100), ("s8", -40), ("s8", 60), ("s8", 100), ("s8", 110), ("bf16", -100),
+                                        ("bf16", -40), ("bf16", 60), ("bf16", 100)])
+def test_scores_of_very_large_and_small_queries(dev, log2, qtype, cache):
+    """Powers of two taken from the keys and given to the query change nothing
+    (while all products with the keys' scales, and the keys, are normal numbers)."""
+    g = gen(7)
+    table, pages, _ = make_table(g, dev, [50], 16)
+    c = make_cache(g, dev, pages, 1, 16, 64, cache)
+    qx = torch.randn((1, 4, 64), generator=g).to(TYPES[qtype]).to(dev)
+    want, wlse = attend(dev, c, table, [50], qx)
+    if cache == "s8":
+        c.k_scale.mul_(2.0 ** -log2)
+    else:
+        c.k.mul_(2.0 ** -log2)
+    out, lse = attend(dev, c, table, [50], qx * 2.0 ** log2)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
