@@ -24,8 +24,8 @@
 //    in which 16-byte pieces hold a lane's fragments;
 //  - a byte with its sign bit flipped, code + 128, is part of an fp16 or bf16
 //    number as it lies: one LOP3 and one subtraction or fma make two exact
-//    codes.  Keys become fp16, and the query is scaled by a power of two to at
-//    most 2; values become bf16, because the weights that multiply them need
+//    codes.  Keys become fp16, and the query is scaled by a power of two into
+//    fp16's range; values become bf16, because the weights that multiply them need
 //    its range.  (Keys entered as code + 128, the 128s taken from the sum, save
 //    the subtraction and no time, but a row with one large channel has codes of
 //    about 1 elsewhere, and their sum kept the rounding of the 128s: 2e-5 of it
@@ -205,7 +205,10 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return r;
 }
 
-// x as the sum of `N` 16-bit floats, the largest first; two values a word.
+// x as the sum of `N` 16-bit floats, the largest first; two values a word.  A
+// second fp16 part is held 2^11 times as large, so that it is a normal number
+// where the first is.
+constexpr float kPartGain = 2048.0f;
 template <bool HALF, int N>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&r)[N]) {
 #pragma unroll
@@ -213,7 +216,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&r)[N]) {
     if constexpr (HALF) {
       const __half2 h = __floats2half2_rn(x, y);
       r[i] = *reinterpret_cast<const uint32_t*>(&h);
-      if (i + 1 < N) x -= __low2float(h), y -= __high2float(h);
+      if (i + 1 < N) x = (x - __low2float(h)) * kPartGain, y = (y - __high2float(h)) * kPartGain;
     } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
       r[i] = *reinterpret_cast<const uint32_t*>(&h);
@@ -272,8 +275,8 @@ struct Form {
   static constexpr bool S8 = S8_;
   static constexpr int DP = DP_, NT = NT_;
   static constexpr bool WIDE = std::is_same<QT, float>::value;
-  // 16-bit parts of q (fp16 of 11 bits, or bf16 of 8) and of the weights
-  // (bf16).  A bf16 query is exact in one; of the weights a bf16 output gets
+  // 16-bit parts of q (fp16 of 11 bits and a sign, or bf16 of 8) and of the
+  // weights (bf16).  A bf16 query is exact in one; of the weights a bf16 output gets
   // 16 bits, far below its own rounding, since one part's 2^-9 is not.
   static constexpr int NQ = WIDE ? (S8 ? 2 : 3) : 1;
   static constexpr int NP = WIDE ? 3 : 2;
@@ -666,8 +669,9 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         for (int j = 0; j < F::PK; ++j) q_raw[nt][j].to_float(v[j]);
         float f = a.scale * kLog2e;
         if constexpr (S8) {
-          // by a power of two to [1, 2): fp16 then holds every element to
-          // 2^-25 of the largest
+          // the largest by a power of two to [2^13, 2^14): elements down to
+          // 2^-27 of it are normal numbers of fp16, and two parts hold them to
+          // 2^-24 of themselves (smaller ones: to 2^-49 of the largest)
           uint32_t most = 0;
 #pragma unroll
           for (int j = 0; j < F::PK; ++j)
@@ -675,9 +679,9 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
             for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(fabsf(v[j][i])));
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          most = min(most & 0x7f800000u, 0x7e800000u);
-          const float down = most ? __uint_as_float(0x7f000000u - most) : 1.0f;
-          if (most) f *= __uint_as_float(most);
+          most = min(max(most & 0x7f800000u, 0x10000000u), 0x7e800000u);  // 2^-95 to 2^126: both powers are normal
+          const float down = __uint_as_float(0x7f000000u + (13u << 23) - most);
+          f *= __uint_as_float(most) * 0x1p-13f;
 #pragma unroll
           for (int j = 0; j < F::PK; ++j)
 #pragma unroll
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (fabsf(rest[nt][j]) < INFINITY) s[nt][j] += rest[nt][j];
+              if (fabsf(rest[nt][j]) < INFINITY) s[nt][j] = fmaf(rest[nt][j], S8 ? 1.0f / kPartGain : 1.0f, s[nt][j]);
         }
         const float* scales = reinterpret_cast<const float*>(slot + 16 * F::ROW);
         float k0 = 1.0f, k1 = 1.0f, f0 = 1.0f, f1 = 1.0f;  // scales of tokens g and g + 8, keys and values

@@ -76,3 +76,21 @@ def test_scores_of_very_large_and_small_queries(dev, log2, qtype, cache):
         c.k.mul_(2.0 ** -log2)
     out, lse = attend(dev, c, table, [50], qx * 2.0 ** log2)
     assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ratio", [10, 16, 20, 24])
+def test_scores_of_queries_with_one_large_element(dev, ratio, qtype):
+    """One element of the query is 2^ratio times the others, where the keys are 0."""
+    g = gen(ratio)
+    lens = [1, 30]
+    table, pages, _ = make_table(g, dev, lens, 16)
+    c = make_cache(g, dev, pages, 1, 16, 64, "s8")
+    c.k[..., 5] = 0
+    qx = torch.randn((2, 4, 64), generator=g).to(TYPES[qtype]).to(dev)
+    qx[..., 5] = 2.0 ** ratio
+    out, lse = attend(dev, c, table, lens, qx)
+    _, want, _, err, _ = reference_attention(c, table, lens, qx, 0, 0.125)
+    off = np.abs(host(lse) - want)
+    tol = err + 2.0 ** -21 + 2 * np.array(lens)[:, None] * U + 2.0 ** -22 * np.abs(want)
+    assert np.all(off <= tol), float((off / tol).max())
