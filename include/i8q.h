@@ -599,10 +599,9 @@ int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* table, const 
  * that enters a sequence's sums makes their results NaN or infinite, and no
  * other sequence's.  lengths (device int32) above max_pages * page_size are cut to
  * that and reported like the other indices.  Nothing past lengths[b] is
- * read.  Sums, maxima and statistics are fp32.  bf16 queries: the weights
- * p_t enter the second product in 16 bits; fp32 queries: q and p_t in 24
- * (over I8Q_S8 pages q's elements below 2^-27 of its largest in fewer, to
- * 2^-49 of that one).  workspace: at least
+ * read.  Sums, maxima and statistics are fp32, and q and p_t enter the
+ * products in 24 bits (over I8Q_S8 pages q's elements below 2^-27 of its
+ * largest in fewer: fp32 to 2^-49 of that one, bf16 to 2^-38).  workspace: at least
  * i8q_paged_attention_workspace_size bytes, 256-byte aligned, not shared by
  * calls that may run at the same time; its contents need not be kept.
  * Results do not depend on the run: no atomics order the sums.

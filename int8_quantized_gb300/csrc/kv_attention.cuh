@@ -276,10 +276,12 @@ struct Form {
   static constexpr int DP = DP_, NT = NT_;
   static constexpr bool WIDE = std::is_same<QT, float>::value;
   // 16-bit parts of q (fp16 of 11 bits and a sign, or bf16 of 8) and of the
-  // weights (bf16).  A bf16 query is exact in one; of the weights a bf16 output gets
-  // 16 bits, far below its own rounding, since one part's 2^-9 is not.
+  // weights (bf16): together the 24 bits of an fp32 number.  A bf16 query is
+  // exact in one.  (Two parts of the weights lost 2^-18 of values that cancel;
+  // 64 sequences of 8192 took 230 us with them, 240 with three, shorter calls
+  // the same.)
   static constexpr int NQ = WIDE ? (S8 ? 2 : 3) : 1;
-  static constexpr int NP = WIDE ? 3 : 2;
+  static constexpr int NP = 3;
   static constexpr int ES = S8 ? 1 : 2;
   static constexpr int KS = DP / 16;           // steps of the first product
   static constexpr int MT = DP / 16;           // row blocks of the second

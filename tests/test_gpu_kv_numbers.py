@@ -94,3 +94,30 @@ def test_scores_of_queries_with_one_large_element(dev, ratio, qtype):
     off = np.abs(host(lse) - want)
     tol = err + 2.0 ** -21 + 2 * np.array(lens)[:, None] * U + 2.0 ** -22 * np.abs(want)
     assert np.all(off <= tol), float((off / tol).max())
+
+
+# ---- weights ----
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weighted_values_that_cancel(dev, D, G, qtype):
+    """Equal scores, and three tokens whose values add up to nothing: a c + b c
+    - (a + b) c.  What is left is what the products with a, b and a + b lost,
+    at most 2^-24 of each, and the sums' 3 u."""
+    B = 64
+    g = gen(D)
+    table, pages, _ = make_table(g, dev, [3] * B, 16)
+    c = make_cache(g, dev, pages, 1, 16, D, "s8")
+    c.k.zero_()
+    tab = table[:, 0].long()
+    code = torch.randint(1, 128, (B, D), generator=g, dtype=torch.int8).to(dev)
+    for t, sign in enumerate((1, 1, -1)):
+        c.v[tab, 0, t] = code * sign
+    a = (torch.randint(1 << 22, 1 << 23, (2, B), generator=g).double() * 2.0 ** -24).to(dev)  # 23 bits: a + b is exact
+    c.v_scale[tab, 0, 0], c.v_scale[tab, 0, 1], c.v_scale[tab, 0, 2] = a[0].float(), a[1].float(), (a[0] + a[1]).float()
+    qx = torch.randn((B, G, D), generator=g).to(TYPES[qtype]).to(dev)
+    out, _ = attend(dev, c, table, [3] * B, qx)
+    weight = (2 / 3 * (a[0] + a[1])[:, None] * code.double()).cpu().numpy()[:, None]
+    off = np.abs(host(out))
+    tol = (2.0 ** -24 + 3 * U) * weight + 1e-30
+    assert np.all(off <= tol), float((off / tol).max())
