@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) join_and_score_kernel(const __grid_consta
 
 int width_of(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 int groups_of(int group) { return group <= 8 ? 1 : 2; }
-int most_warps(bool s8, int dp, int nt) { return s8 && dp <= 128 && nt == 1 ? 16 : dp <= 128 && (nt == 1 || dp == 64) ? 12 : 8; }
+int most_warps(bool s8, int dp, int nt) { return s8 && dp == 64 && nt == 1 ? 16 : dp <= 128 && (nt == 1 || dp == 64) ? 12 : 8; }
 
 // Most that one sequence takes of the line.
 int64_t line_length(const Cache& c, const Table& tab, int64_t q_heads) {

@@ -179,6 +179,12 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// a += x and b += y in one instruction.
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 s, d;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tadd.rn.f32x2 s, s, d;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
 // 8 x 8 transpose of 16-bit values over the warp (a lane holds two
 // neighbours of row lane / 4).
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -296,10 +302,11 @@ struct Form {
   static constexpr int Q_WORDS = NQ * NT * KS * 2;
   static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
-  // Warps: 16 of 128 registers where they suffice (1 x 131072 tokens: 60 us,
-  // as with 12 of 168, and 64 x 8192: 205 us against 211), else 12 (of 16
-  // heads of 64: 37 us against 45 with 8; of 128: 41 against 29), 8 or 4 of 255.
-  static constexpr int W = NT == 1 && S8 && DP <= 128 && !WIDE                               ? 16
+  // Warps: 16 of 128 registers where they suffice (int8 heads of 64, 64 x
+  // 8192 tokens: 143 us against 155 with 12 of 168; of 128, 301 against 249),
+  // else 12 (of 16 heads of 64: 37 us against 45 with 8; of 128: 41 against 29),
+  // 8 or 4 of 255.
+  static constexpr int W = NT == 1 && S8 && DP == 64 && !WIDE                               ? 16
                            : (NT == 1 && (S8 ? DP <= 128 : DP == 64)) || (DP == 64 && !WIDE) ? 12
                            : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024                          ? 8
                                                                                              : 4;
@@ -857,16 +864,14 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (F::WIDE) {  // a tile's sum by itself, then rounded to the whole
-              float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            // a tile's sum by itself, then rounded to the whole: the tensor pipe
+            // cuts its sums, always downwards (a row's 860 tiles lost 10^-4 of
+            // values of one sign that way; 64 x 8192 tokens took 240 us, not 249)
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int p = F::NP - 1; p >= 0; --p) mma<false>(x, a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[mt][nt][j] += x[j];
-            } else {
-#pragma unroll
-              for (int p = 0; p < F::NP; ++p) mma<false>(o[mt][nt], a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
-            }
+            for (int p = F::NP - 1; p >= 0; --p) mma<false>(x, a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
+            add2(o[mt][nt][0], o[mt][nt][1], x[0], x[1]);
+            add2(o[mt][nt][2], o[mt][nt][3], x[2], x[3]);
           }
         };
 #pragma unroll

@@ -121,3 +121,50 @@ def test_weighted_values_that_cancel(dev, D, G, qtype):
     off = np.abs(host(out))
     tol = (2.0 ** -24 + 3 * U) * weight + 1e-30
     assert np.all(off <= tol), float((off / tol).max())
+
+
+@pytest.mark.parametrize("cache", ["s8", "bf16"])
+@pytest.mark.parametrize("G", [4, 16])
+def test_sums_of_long_rows_are_rounded(dev, G, cache):
+    """256 sequences of 131072 tokens (the same few pages over and over) of two
+    scores, so that weights have all their bits, and values of one sign but
+    for one token's, which takes their sum away.  Sums that are rounded are off
+    by u sqrt(n) or so (n <= 8192 tiles), with 8 for the tails; sums that are
+    cut lose u / 2 and more at every step, always downwards."""
+    g = gen(3)
+    L, D, page, B = 131072, 64, 128, 256
+    pages = 9
+    c = make_cache(g, dev, pages, 1, page, D, cache, score=False)
+    table = torch.randint(0, 8, (B, L // page), generator=g, dtype=torch.int32)
+    table[:, 0] = 8
+    c.k.zero_()
+    c.k[:, 0, 0, 0] = 1
+    w = torch.ones((pages, page), dtype=torch.float64)
+    w[:, 0] = math.exp(5.59375 / 8)
+    if cache == "s8":
+        c.k_scale.fill_(1.0)
+        c.v.fill_(93)
+        c.v_scale.copy_(0.5 + torch.rand(c.v_scale.shape, generator=g) / 2)
+        one = c.v_scale.double().cpu()[:, 0] * 93
+    else:
+        c.v.copy_((0.5 + torch.rand(c.v.shape[:3], generator=g) / 2)[..., None].to(torch.bfloat16))
+        one = c.v[:, 0, :, 0].double().cpu()
+    # the first token of each sequence (page 8) takes their mean sum away, the rest is the reference's
+    away = float((one * w).sum(-1)[:8].mean() * (L // page) / w[8, 0])
+    if cache == "s8":
+        c.v[8, 0, 0] = -127
+        c.v_scale[8, 0, 0] = away / 127
+        one[8, 0] = -127 * c.v_scale[8, 0, 0].double().cpu()
+    else:
+        c.v[8, 0, 0] = -away
+        one[8, 0] = c.v[8, 0, 0, 0].double().cpu()
+    total = w.sum(-1)[table.long()].sum(-1)
+    want = (one * w).sum(-1)[table.long()].sum(-1) / total
+    weight = (one.abs() * w).sum(-1)[table.long()].sum(-1) / total
+    qx = torch.randn((B, G, D), generator=g)
+    qx[..., 0] = 5.59375
+    qx = qx.to(torch.bfloat16).to(dev)
+    out, _ = attend(dev, c, table.to(dev), [L] * B, qx)
+    off = (out.double().cpu() - want[:, None, None]).abs()
+    tol = (8 * math.sqrt(8192) * U * weight + 2.0 ** -8 * want.abs())[:, None, None]
+    assert bool((off <= tol).all()), float((off / tol).max())
