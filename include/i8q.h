@@ -516,7 +516,8 @@ int i8q_dq_lstm_state_codes(const void* workspace, int64_t T, int64_t batch, int
  *   code  = saturate(rint(x / scale)),    value = code * scale,
  * each operation rounded once in fp32.  I8Q_BF16 pools hold the values
  * rounded to bf16 and have no scales.  A row that holds an infinity or a NaN
- * gets a scale that is one, so that what attends to it is not finite either.
+ * gets a scale that is one.  The scores of a key whose scale is not finite
+ * are NaN, and so is what attends to it: its value has infinity times 0.
  *
  * Page numbers, sequence numbers, token indices and positions are device
  * data.  One outside its range is never followed: the token it names is left

@@ -785,7 +785,11 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
         }
         const float* scales = reinterpret_cast<const float*>(slot + 16 * F::ROW);
         float k0 = 1.0f, k1 = 1.0f, f0 = 1.0f, f1 = 1.0f;  // scales of tokens g and g + 8, keys and values
-        if constexpr (S8) k0 = scales[g], k1 = scales[g + 8], f0 = scales[g + 16], f1 = scales[g + 24];
+        if constexpr (S8) {
+          k0 = scales[g], k1 = scales[g + 8], f0 = scales[g + 16], f1 = scales[g + 24];
+          // an infinite scale times a code of 0 is NaN, whatever the sum of the others
+          k0 += k0 - k0, k1 += k1 - k1;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

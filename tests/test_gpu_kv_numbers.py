@@ -168,3 +168,32 @@ def test_sums_of_long_rows_are_rounded(dev, G, cache):
     off = (out.double().cpu() - want[:, None, None]).abs()
     tol = (8 * math.sqrt(8192) * U * weight + 2.0 ** -8 * want.abs())[:, None, None]
     assert bool((off <= tol).all()), float((off / tol).max())
+
+
+# ---- what is not finite ----
+@pytest.mark.parametrize("qtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("D", [64, 80])
+def test_an_infinite_key_is_not_passed_over(dev, D, bad, sign, qtype):
+    """A key with an infinite element, written by kv_append beside finite
+    values: its scale is infinite, and what attends to it is not finite,
+    whatever the sign of the query there."""
+    g = gen(0)
+    table, pages, _ = make_table(g, dev, [8, 8], 16)
+    c = make_cache(g, dev, pages, 2, 16, D, "s8")
+    k, v = torch.randn((16, 2, D), generator=g), torch.randn((16, 2, D), generator=g)
+    k[3, 1, 17] = bad
+    seq = torch.arange(16, device=dev, dtype=torch.int32) // 8
+    index = torch.arange(16, device=dev, dtype=torch.int32) % 8
+    c.score.fill_(1.0)
+    q.kv_append(c, table, seq, index, k.to(dev), v.to(dev))
+    qx = torch.randn((2, 4, D), generator=g).to(TYPES[qtype]).to(dev)
+    qx[..., 17] = sign
+    out, lse = attend(dev, c, table, [8, 8], qx, accumulate=True)
+    good = torch.ones((2, 4), dtype=torch.bool, device=dev)
+    good[0, 2:] = False
+    assert torch.equal(torch.isfinite(lse), good)
+    assert torch.equal(torch.isfinite(out), good[..., None].expand_as(out))
+    score = c.score[table[:, 0].long(), :, :8]
+    assert torch.isfinite(score[1]).all() and torch.isfinite(score[0, 0]).all() and not torch.isfinite(score[0, 1]).any()
