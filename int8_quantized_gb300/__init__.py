@@ -49,6 +49,15 @@ def _dev(t, name, dtype=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _workspace(size, device, stream):
+    """`size` bytes for a call on `stream`, in that stream's order: a block of another one's may still be in use by what
+    that one has queued."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _i64_array(vals):
     vals = list(int(v) for v in vals)
     return (ctypes.c_int64 * max(1, len(vals)))(*vals)
@@ -249,7 +258,7 @@ def qlinearconv(x, x_scale, x_zero_point, w, w_scale, w_zero_point, y_scale, y_z
     if workspace is None:
         need = int(_L().i8q_qlinearconv_workspace_size(xs, ws, p, s, d, int(group)))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+            workspace = _workspace(need, y.device, stream)
     check(_L().i8q_qlinearconv(_dev(x, "x"), _TORCH_TYPE[x.dtype], xs, float(x_scale), int(x_zero_point),
                                _dev(w, "w"), _TORCH_TYPE[w.dtype], ws, _dev(w_scale, "w_scale", torch.float32),
                                _dev(w_zero_point, "w_zero_point"), w_scale.numel(), float(y_scale),
@@ -291,7 +300,7 @@ def qgemm(A, a_scale, a_zero_point, B, b_scale, Y, b_zero_point=None, C=None, al
     if not quant and Y.dtype != torch.float32:
         raise TypeError("Y must be float32 when y_scale is None")
     if workspace is None:
-        workspace = torch.empty(qgemm_workspace_size(M, N, K), dtype=torch.uint8, device=Y.device)
+        workspace = _workspace(qgemm_workspace_size(M, N, K), Y.device, stream)
     check(_L().i8q_qgemm(_dev(A, "A"), _TORCH_TYPE[A.dtype], int(bool(transA)), M, K, float(a_scale),
                          int(a_zero_point), _dev(B, "B"), _TORCH_TYPE[B.dtype], int(bool(transB)), N,
                          _dev(b_scale, "b_scale", torch.float32), _dev(b_zero_point, "b_zero_point"),
@@ -320,7 +329,7 @@ def matmul_integer_to_float(A, B, a_scale, b_scale, Y, a_zero_point=None, b_zero
         if z is not None and z.dtype != t.dtype:
             raise TypeError(f"{n} must have the dtype of its operand")
     if workspace is None:
-        workspace = torch.empty(matmul_integer_workspace_size(M, N, K), dtype=torch.uint8, device=Y.device)
+        workspace = _workspace(matmul_integer_workspace_size(M, N, K), Y.device, stream)
     check(_L().i8q_matmul_integer_to_float(
         _dev(A, "A"), _TORCH_TYPE[A.dtype], M, K, _dev(B, "B"), _TORCH_TYPE[B.dtype], N,
         _dev(a_scale, "a_scale", torch.float32), _dev(a_zero_point, "a_zero_point"), a_scale.numel(),
@@ -342,7 +351,7 @@ def dynamic_quantize_matmul(A, B, b_scale, Y, b_zero_point=None, bias=None, a_sc
     if b_zero_point is not None and b_zero_point.dtype != B.dtype:
         raise TypeError("b_zero_point must have B's dtype")
     if workspace is None:
-        workspace = torch.empty(matmul_integer_workspace_size(M, N, K), dtype=torch.uint8, device=Y.device)
+        workspace = _workspace(matmul_integer_workspace_size(M, N, K), Y.device, stream)
     check(_L().i8q_dynamic_quantize_matmul(
         _dev(A, "A", torch.float32), M, K, _dev(B, "B"), _TORCH_TYPE[B.dtype], N, _dev(b_scale, "b_scale", torch.float32),
         _dev(b_zero_point, "b_zero_point"), b_scale.numel(), _dev(bias, "bias", torch.float32),
@@ -542,10 +551,7 @@ def paged_attention(cache, page_table, lengths, q, out, lse=None, softmax_scale=
     D, dtype = cache.shape[3], q.dtype
     B, heads = page_table.shape[0], q.shape[1]
     if workspace is None:
-        workspace = torch.empty(paged_attention_workspace_size(cache, page_table, heads, accumulate),
-                                dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)  # allocated on the current stream, used on that one
+        workspace = _workspace(paged_attention_workspace_size(cache, page_table, heads, accumulate), q.device, stream)
     if lse is not None and lse.shape != (B, heads):
         raise ValueError(f"lse must be [{B}, {heads}]")
     check(_L().i8q_paged_attention(cache._ref, ctypes.byref(_page_table(page_table)), _i32(lengths, "lengths", B),
