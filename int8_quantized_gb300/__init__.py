@@ -32,8 +32,10 @@ def _L():
 def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
-    # torch.cuda.current_stream().cuda_stream, without the object (2.9 us a call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    # torch.cuda.current_stream().cuda_stream, without the object (2.9 us a call); current_device initialises CUDA as
+    # that does, and says so where it cannot (a forked child, a torch without CUDA)
+    device = torch.cuda.current_device()
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))
 
 
 def _dev(t, name, dtype=None):
