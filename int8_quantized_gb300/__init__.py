@@ -418,6 +418,8 @@ class KVCache:
                 raise TypeError(f"{name} must be a CUDA tensor of 4 axes")
         if k.dtype not in (torch.int8, torch.bfloat16) or v.dtype != k.dtype:
             raise TypeError("k and v must both be int8 or both be bfloat16")
+        if v.device != k.device:
+            raise TypeError("v must be a tensor beside k")
         if k.shape != v.shape or k.stride() != v.stride():
             raise ValueError("k and v must have the same shape and strides")
         if k.stride(3) != 1:
