@@ -401,6 +401,11 @@ def qlinear_unary(op, X, x_scale, x_zero_point, y_scale, y_zero_point, Y, alpha=
     return Y
 
 
+def _strides(t):
+    """Strides of the axes that have more than one place (the others' mean nothing)."""
+    return [s for s, n in zip(t.stride(), t.shape) if n > 1]
+
+
 class KVCache:
     """A paged key/value cache: the pools of pages that a serving program
     keeps (i8q_kv_cache), checked once.
@@ -420,7 +425,7 @@ class KVCache:
             raise TypeError("k and v must both be int8 or both be bfloat16")
         if v.device != k.device:
             raise TypeError("v must be a tensor beside k")
-        if k.shape != v.shape or k.stride() != v.stride():
+        if k.shape != v.shape or _strides(k) != _strides(v):
             raise ValueError("k and v must have the same shape and strides")
         if k.stride(3) != 1:
             raise ValueError("head_dim must be contiguous")
@@ -428,7 +433,7 @@ class KVCache:
         for t, name in per:
             if not isinstance(t, torch.Tensor) or t.device != k.device or t.dtype != torch.float32:
                 raise TypeError(f"{name} must be a float32 tensor beside k")
-            if t.shape != k.shape[:3] or t.stride() != per[0][0].stride():
+            if t.shape != k.shape[:3] or _strides(t) != _strides(per[0][0]):
                 raise ValueError(f"{name} must be [pages, kv_heads, page_size], of the others' strides")
         if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
             raise ValueError("an int8 cache needs k_scale and v_scale, a bfloat16 cache has none")

@@ -28,25 +28,28 @@ int check_cache(const i8q_kv_cache* c, const char* who, Cache& out) {
   const int64_t st[3] = {c->page_stride, c->head_stride, c->token_stride};
   const int64_t ss[3] = {c->scale_page_stride, c->scale_head_stride, c->scale_token_stride};
   for (int i = 0; i < 3; ++i) {
-    if (ext[i] > 1 && st[i] < c->head_dim)
+    if (ext[i] == 1) continue;  // never multiplied
+    if (st[i] < c->head_dim)
       return fail(I8Q_ERR_INVALID_ARG, w + ": cache rows overlap (a stride is below head_dim)");
     if (st[i] % unit != 0) return fail(I8Q_ERR_INVALID_ARG, w + ": cache strides must be multiples of 16 bytes");
-    if ((c->k_scale || c->score) && ext[i] > 1 && ss[i] < 1)
+    if ((c->k_scale || c->score) && ss[i] < 1)
       return fail(I8Q_ERR_INVALID_ARG, w + ": scale strides must be positive");
   }
   if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16)
     return fail(I8Q_ERR_INVALID_ARG, w + ": cache pools must be 16-byte aligned");
+  // (an axis of one place has the stride 0, and the kernels' rules on alignment need not look at it)
+  const auto stride = [&](int i, const int64_t* s) { return ext[i] == 1 ? 0 : s[i]; };
   out = Cache{c->k,
               c->v,
               c->k_scale,
               c->v_scale,
               c->score,
-              c->page_stride,
-              c->head_stride,
-              c->token_stride,
-              c->scale_page_stride,
-              c->scale_head_stride,
-              c->scale_token_stride,
+              stride(0, st),
+              stride(1, st),
+              stride(2, st),
+              stride(0, ss),
+              stride(1, ss),
+              stride(2, ss),
               (int)c->pages,
               (int)c->kv_heads,
               (int)c->page_size,
