@@ -390,7 +390,10 @@ __device__ __forceinline__ void add_weights(const Args& a, int b, int kvh, int f
     float p[V] = {};
     // a logit outside the sequence or its window is -infinity: no weight
     if constexpr (V == 4) {
-      float4 s = *reinterpret_cast<const float4*>(score);
+      // (scores past the length or before the window are not this call's to write, even unchanged)
+      const bool whole = t >= first && t + 4 <= len;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (whole) s = *reinterpret_cast<const float4*>(score);
 #pragma unroll 4
       for (int i = 0; i < a.group; ++i) {
         const float r = log_of(i);
@@ -398,11 +401,14 @@ __device__ __forceinline__ void add_weights(const Args& a, int b, int kvh, int f
         p[0] += ex2_approx(l.x - r), p[1] += ex2_approx(l.y - r);
         p[2] += ex2_approx(l.z - r), p[3] += ex2_approx(l.w - r);
       }
-      if (t >= first) s.x += p[0];
-      if (t + 1 >= first && t + 1 < len) s.y += p[1];
-      if (t + 2 >= first && t + 2 < len) s.z += p[2];
-      if (t + 3 >= first && t + 3 < len) s.w += p[3];
-      *reinterpret_cast<float4*>(score) = s;
+      if (whole) {
+        s.x += p[0], s.y += p[1], s.z += p[2], s.w += p[3];
+        *reinterpret_cast<float4*>(score) = s;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (t + j >= first && t + j < len) score[j] += p[j];
+      }
     } else {
 #pragma unroll 4
       for (int i = 0; i < a.group; ++i) p[0] += ex2_approx(logit[i * a.logit_pitch] - log_of(i));
