@@ -260,6 +260,22 @@ Layout layout_of(const Cache& c, const Table& tab, bool s8, int64_t q_heads, int
   return l;
 }
 
+// What the workspace's size and the call itself refuse alike, and the device forms of the structs.
+int check_sizes(const i8q_kv_cache* cache, const i8q_page_table* table, int64_t q_heads, int accumulate, const char* who,
+                Cache& c, Table& tab) {
+  int rc = kv::check_cache(cache, who, c);
+  if (rc == I8Q_OK) rc = kv::check_table(table, c, who, tab);
+  if (rc != I8Q_OK) return rc;
+  const std::string w = who;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads)
+    return fail(I8Q_ERR_INVALID_ARG, w + ": q_heads must be a multiple of kv_heads, in range");
+  if (tab.sequences * q_heads > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, w + ": sequences * q_heads out of range");
+  if (accumulate && !c.score) return fail(I8Q_ERR_INVALID_ARG, w + ": accumulate needs a cache that keeps scores");
+  if (line_length(c, tab, q_heads) > INT32_MAX)
+    return fail(I8Q_ERR_UNSUPPORTED, w + ": max_pages * page_size * kv_heads out of range");
+  return I8Q_OK;
+}
+
 }  // namespace
 }  // namespace i8q
 
@@ -269,13 +285,7 @@ extern "C" size_t i8q_paged_attention_workspace_size(const i8q_kv_cache* cache, 
                                                      int64_t q_heads, int accumulate) {
   Cache c;
   Table tab;
-  if (kv::check_cache(cache, "paged_attention_workspace_size", c) != I8Q_OK ||
-      kv::check_table(table, c, "paged_attention_workspace_size", tab) != I8Q_OK)
-    return 0;
-  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads || tab.sequences * q_heads > INT32_MAX) {
-    fail(I8Q_ERR_INVALID_ARG, "paged_attention_workspace_size: q_heads must be a multiple of kv_heads, in range");
-    return 0;
-  }
+  if (check_sizes(cache, table, q_heads, accumulate, "paged_attention_workspace_size", c, tab) != I8Q_OK) return 0;
   return (size_t)layout_of(c, tab, cache->type == I8Q_S8, q_heads, accumulate).bytes;
 }
 
@@ -285,25 +295,15 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
                                    float* lse, float softmax_scale, int64_t window, int accumulate, void* workspace,
                                    size_t ws_bytes, void* stream) {
   Args a{};
-  int rc = kv::check_cache(cache, "paged_attention", a.c);
-  if (rc == I8Q_OK) rc = kv::check_table(table, a.c, "paged_attention", a.tab);
+  int rc = check_sizes(cache, table, q_heads, accumulate, "paged_attention", a.c, a.tab);
   if (rc != I8Q_OK) return rc;
   if (type != I8Q_F32 && type != I8Q_BF16)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: type must be I8Q_F32 or I8Q_BF16");
   if (!lengths || !q || !out) return fail(I8Q_ERR_INVALID_ARG, "paged_attention: lengths, q or out is NULL");
-  if (q_heads < 1 || q_heads > 65535 || q_heads % a.c.heads)
-    return fail(I8Q_ERR_INVALID_ARG, "paged_attention: q_heads must be a multiple of kv_heads");
-  if (a.tab.sequences * q_heads > INT32_MAX)
-    return fail(I8Q_ERR_INVALID_ARG, "paged_attention: sequences * q_heads out of range");
   if (window < 0) return fail(I8Q_ERR_INVALID_ARG, "paged_attention: window must not be negative");
   if (!(softmax_scale == softmax_scale)) return fail(I8Q_ERR_INVALID_ARG, "paged_attention: softmax_scale is NaN");
-  if (accumulate && !a.c.score)
-    return fail(I8Q_ERR_INVALID_ARG, "paged_attention: accumulate needs a cache that keeps scores");
   const bool s8 = cache->type == I8Q_S8;
-  const int64_t longest = line_length(a.c, a.tab, q_heads);
-  if (longest > INT32_MAX)
-    return fail(I8Q_ERR_UNSUPPORTED, "paged_attention: max_pages * page_size * kv_heads out of range");
-  const int slice = (int)std::min<int64_t>(kMaxSequences, INT32_MAX / longest);
+  const int slice = (int)std::min<int64_t>(kMaxSequences, INT32_MAX / line_length(a.c, a.tab, q_heads));
   const Layout l = layout_of(a.c, a.tab, s8, q_heads, accumulate);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < (size_t)l.bytes)
     return fail(I8Q_ERR_INVALID_ARG, "paged_attention: workspace is NULL, unaligned or too small");
