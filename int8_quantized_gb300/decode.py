@@ -26,6 +26,8 @@ class DecodeAttention:
                  capacity, budget, sink=4, recent=32, page_size=16):
         if not 0 < budget < capacity:
             raise ValueError("budget must be below capacity")
+        if sink < 0 or recent < 0 or sink + recent > budget:
+            raise ValueError("sink + recent must be within 0 .. budget")
         dev = w_qkv.device
         self.B, self.Hq, self.H, self.D = sequences, q_heads, kv_heads, head_dim
         self.capacity, self.budget, self.sink, self.recent, self.page = capacity, budget, sink, recent, page_size
@@ -60,12 +62,12 @@ class DecodeAttention:
         """Cut sequence b to its budget; returns the kept tokens' indices [kv_heads, budget]."""
         dev = self.table.device
         need = -(-self.budget // self.page)
-        new = [self.free.pop() for _ in range(need)]
+        new = self.free[-need:]
         new_table = torch.tensor([new], dtype=torch.int32, device=dev)
         kept = torch.empty((1, self.H, self.budget), dtype=torch.int32, device=dev)
         q.kv_evict(self.cache, self.table[b:b + 1], torch.tensor([self.length[b]], dtype=torch.int32, device=dev),
                    new_table, kept, sink=self.sink, recent=self.recent)
-        self.free += self.owned[b]
+        self.free = self.free[:-need] + self.owned[b]
         self.owned[b], self.length[b] = new, min(self.length[b], self.budget)
         self.table[b].fill_(-1)
         self.table[b, :need] = new_table[0]
@@ -94,8 +96,10 @@ class DecodeAttention:
 
 
 def random_layer(sequences=4, hidden=1024, q_heads=16, kv_heads=4, head_dim=64, capacity=96, budget=64, positions=4096,
-                 seed=0, device="cuda"):
-    """A DecodeAttention with random weights."""
+                 seed=0, device="cuda", sink=None, recent=None):
+    """A DecodeAttention with random weights; sink and recent: 4 and 32, or what the budget has room for."""
+    sink = min(4, budget) if sink is None else sink
+    recent = min(32, budget - sink) if recent is None else recent
     g = torch.Generator(device=device)
     g.manual_seed(seed)
 
@@ -107,7 +111,8 @@ def random_layer(sequences=4, hidden=1024, q_heads=16, kv_heads=4, head_dim=64, 
     turn = torch.arange(positions, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(pairs) / pairs)
     return DecodeAttention(*weight(hidden, (q_heads + 2 * kv_heads) * head_dim), *weight(q_heads * head_dim, hidden),
                            turn.cos().float().to(device), turn.sin().float().to(device), sequences=sequences,
-                           q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, capacity=capacity, budget=budget)
+                           q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, capacity=capacity, budget=budget,
+                           sink=sink, recent=recent)
 
 
 def main():
