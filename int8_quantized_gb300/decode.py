@@ -76,6 +76,8 @@ class DecodeAttention:
     def step(self, x, out):
         """x, out: bf16 [sequences, hidden], the next token of every sequence."""
         dev = x.device
+        if max(self.position) >= self.cos.shape[0]:
+            raise ValueError("a sequence has no position left in cos and sin")
         for b in range(self.B):
             if self.length[b] == self.capacity:
                 self.evict(b)

@@ -45,3 +45,17 @@ def test_a_refused_eviction_keeps_the_pages(dev):
     layer.step(x, out)
     assert layer.length == [13, 13]
     q.sync_status()
+
+
+@pytest.mark.gpu
+def test_a_step_past_the_last_position_is_refused(dev):
+    layer = decode.random_layer(sequences=2, hidden=128, q_heads=4, kv_heads=2, head_dim=64, positions=17)
+    x = torch.randn((2, 128), device=dev).to(torch.bfloat16)
+    out = torch.empty_like(x)
+    for _ in range(17):
+        layer.step(x, out)
+    before = state(layer)
+    with pytest.raises(ValueError, match="position"):
+        layer.step(x, out)
+    assert same(state(layer), before)
+    q.sync_status()
