@@ -542,7 +542,7 @@ typedef struct i8q_kv_cache {
 typedef struct i8q_page_table {
   const int32_t* table; /* [sequences][max_pages], rows `stride` entries apart; */
   int64_t sequences;    /* entries past a sequence's last token are not read */
-  int64_t max_pages;    /* max_pages * page_size < 2^31 */
+  int64_t max_pages;    /* max_pages * page_size <= 2^31 - 2^16 */
   int64_t stride;
 } i8q_page_table;
 
@@ -627,7 +627,7 @@ size_t i8q_paged_attention_workspace_size(const i8q_kv_cache* cache, const i8q_p
  * once this call is done); a new page must not be one of them.
  * kept: device int32 [sequences, kv_heads, budget], the kept tokens'
  * indices, -1 from n on.  new_lengths: device int32 [sequences], or NULL.
- * sink + recent <= budget.  A kept token that new_table's rows have no place
+ * sink + recent <= budget <= 2^31 - 2^16.  A kept token that new_table's rows have no place
  * for (n above its max_pages * page_size) is not copied, and reported like
  * an index out of range.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */

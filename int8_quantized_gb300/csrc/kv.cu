@@ -62,8 +62,8 @@ int check_table(const i8q_page_table* t, const Cache& c, const char* who, Table&
   if (!t || !t->table) return fail(I8Q_ERR_INVALID_ARG, w + ": page table is NULL");
   if (t->sequences < 1 || t->sequences > 65536 || t->max_pages < 1)
     return fail(I8Q_ERR_INVALID_ARG, w + ": page table has no rows or columns, or too many");
-  if (t->max_pages > INT32_MAX / c.page_size)
-    return fail(I8Q_ERR_INVALID_ARG, w + ": max_pages * page_size must be below 2^31");
+  if (t->max_pages > kMostTokens / c.page_size)
+    return fail(I8Q_ERR_INVALID_ARG, w + ": max_pages * page_size must be at most 2^31 - 2^16");
   if (t->sequences > 1 && t->stride < t->max_pages)
     return fail(I8Q_ERR_INVALID_ARG, w + ": page table rows overlap");
   out = Table{t->table, t->stride, (int)t->sequences, (int)t->max_pages};

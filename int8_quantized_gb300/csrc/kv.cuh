@@ -14,6 +14,10 @@ constexpr uint32_t ST_KV_INDEX = 1u << 31;
 
 namespace kv {
 
+// The most tokens that a row of a page table names, and that an eviction
+// keeps: counters of 32 bits step past the end by up to 2^15 of them.
+constexpr int64_t kMostTokens = (1LL << 31) - (1 << 16);
+
 struct Cache {
   void* k;
   void* v;

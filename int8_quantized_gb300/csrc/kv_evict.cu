@@ -401,7 +401,8 @@ extern "C" int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* tab
   if (a.to.sequences != a.tab.sequences)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: table and new_table differ in sequences");
   const int64_t heads = (int64_t)a.tab.sequences * a.c.heads;
-  if (budget < 1 || budget > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "kv_evict: budget must be 1 .. 2^31 - 1");
+  if (budget < 1 || budget > kv::kMostTokens)
+    return fail(I8Q_ERR_INVALID_ARG, "kv_evict: budget must be 1 .. 2^31 - 2^16");
   if (heads > INT32_MAX / 16 || heads * ceil_div(budget, kRows) > INT32_MAX)
     return fail(I8Q_ERR_INVALID_ARG, "kv_evict: sequences * kv_heads * budget out of range");
   if (sink < 0 || recent < 0 || sink > budget || recent > budget - sink)
