@@ -240,7 +240,7 @@ struct Piece {
     for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ void load_any(const T* p) {  // at any alignment
-    T e[N];
+    alignas(16) T e[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) e[i] = p[i];
 #pragma unroll
