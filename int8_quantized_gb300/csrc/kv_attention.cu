@@ -314,7 +314,7 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
   a.q_heads = (int)q_heads;
   a.group = a.q_heads / a.c.heads;
   a.window = (int)std::min<int64_t>(window, INT32_MAX);
-  a.dp = l.dp, a.heads_per_row = l.heads_per_row;
+  a.heads_per_row = l.heads_per_row;
   a.chunks = (int)ceil_div(a.group, a.heads_per_row);
   char* ws = static_cast<char*>(workspace);
   a.line = reinterpret_cast<int*>(ws + l.line);

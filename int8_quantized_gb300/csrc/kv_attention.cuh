@@ -85,14 +85,13 @@ struct Args {
   int q_heads, group, chunks;  // group: query heads of a key/value head; chunks: rows that share one
   int window;
   int aligned_q, aligned_out;  // 16-byte loads of q rows, paired stores of out rows
-  int dp;                      // row pitch of the partial outputs
   int heads_per_row;           // of a partial: 8 or 16
   int ctas, warps;             // of the first kernel
   int per_row;                 // warps that share a row, where rows are not cut; else 0
   int cluster;                 // CTAs that share one then
   int* line;                   // [sequences + 1] start of each sequence on the line
   float2* part_stats;          // [ctas * warps][2][heads_per_row] (m, l)
-  float* part_out;             // [ctas * warps][2][heads_per_row][dp]
+  float* part_out;             // [ctas * warps][2][heads_per_row][DP of the form]
   float* logits;               // [sequences][q_heads][logit_pitch], or null
   int64_t logit_pitch;
   float* stats;                // [sequences][q_heads] m + log2 l (with logits)
