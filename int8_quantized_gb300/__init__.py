@@ -508,6 +508,8 @@ def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions
     i8q_kv_append.  Returns q_out."""
     if (cos is None) != (sin is None) or (cos is None) != (positions is None):
         raise ValueError("positions, cos and sin come together")
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
     tokens, dtype = k.shape[0], k.dtype
     _, H, _, D = cache.shape
     rot = None

@@ -29,6 +29,24 @@ def test_a_torch_without_cuda_says_so(monkeypatch):
         q._stream()
 
 
+def test_q_out_without_q(monkeypatch):
+    """It came back as it was, as if turned."""
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: 0
+
+    monkeypatch.setattr(q, "_L", lambda: Library())
+    monkeypatch.setattr(q, "_page_table", lambda t, *a: q._lib.PageTableStruct())
+    monkeypatch.setattr(q, "_rows", lambda *a: (None, 0, 0))
+    monkeypatch.setattr(q, "_i32", lambda *a: None)
+    monkeypatch.setattr(q, "_stream", lambda s=None: None)
+    cache = type("Cache", (), {"_ref": None, "shape": (1, 1, 16, 64)})()
+    k = torch.zeros((2, 1, 64))
+    assert q.kv_append(cache, None, None, None, k, k) is None
+    with pytest.raises(ValueError, match="q_out"):
+        q.kv_append(cache, None, None, None, k, k, q_out=torch.zeros((2, 4, 64)))
+
+
 class OnDevice(torch.Tensor):
     """A CPU tensor that says it lies on a GPU."""
     is_cuda = property(lambda self: True)
