@@ -347,8 +347,8 @@ extern "C" int i8q_paged_attention(const i8q_kv_cache* cache, const i8q_page_tab
     const int heads = a.tab.sequences * a.q_heads;
     const bool few = heads <= 2 * sm_count();
     const unsigned joins = (unsigned)(few ? heads : ceil_div(heads, 8)), scores = 16 * (unsigned)sm_count();
-    // Both in one launch where there is not much to score: 24 x 2500 tokens of 16 heads take 37 us instead of 40;
-    // with twice the registers of the scores alone 64 x 8192 of 8 heads would take 237 instead of 231.
+    // Both in one launch where there is not much to score: 24 x 2500 tokens of 16 heads take 35 us instead of 38;
+    // with twice the registers of the scores alone 64 x 8192 of 8 heads would take 249 instead of 244.
     const int64_t tokens = (int64_t)a.tab.sequences * a.c.heads * a.tab.max_pages * a.c.page_size;
     if (!a.per_row && accumulate && a.group <= 32 && tokens <= 1 << 21) {
       I8Q_PROF("paged_attention_join_and_scores", s);

@@ -44,8 +44,8 @@
 // The split follows from the sizes and lengths alone, so results repeat.
 //
 // Measured: one sequence of 131072 tokens, 8 heads of 128, int8, 32 query
-// heads: 60 us a call, 277 MB, its tiles streaming at 6.5 TB/s between 5 us of
-// start and 6 of end; 64 sequences of 8192 with scores: 231 us, 1.14 GB.
+// heads: 62 us a call, 277 MB (each further 131072 tokens 48 us, 5.8 TB/s; of
+// bf16 83 us, 6.5 TB/s); 64 sequences of 8192 with scores: 245 us, 1.14 GB.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -130,13 +130,14 @@ __device__ __forceinline__ Cut cut_line(const Args& a, int n, int rows) {
 // Short rows: a CTA keeps whole rows, `per_row` warps (a divisor of its number)
 // to each, or a cluster of CTAs has one and joins its parts through their
 // shared memory, so that one launch does it all (one sequence of 4000 tokens, 4
-// heads: 11.6 us instead of 14.5, and with scores 13.7 instead of 21.5; of
-// 2000: 11.1, where one CTA a row took 18.5).  A tile a warp takes 1.2 us with a
-// CTA's warps all at work, somewhat more for fp32 queries; what cut rows need
-// more is worth 5 tiles (with scores 7; fp32 4 and 5), less one for a cluster's
-// exchange, and each SM has its even share of tiles then.  So rows stay whole while they have no
-// more tiles a warp than that, and no more than kShort: the table may be wider
-// than its sequences are long, some SMs' rows longer than others'.
+// heads: 11.3 us instead of 14.4, and with scores 13.4 instead of 21.4; of
+// 2000: 9.5 instead of 14.5).  A tile a warp takes 0.9 to 1.6 us with a CTA's
+// warps all at work; what cut rows need more is worth 5 tiles (with scores 7;
+// fp32 4 and 5), less one for a cluster's exchange, and each SM has its even
+// share of tiles then.  So rows stay whole while they have no more tiles a warp
+// than that, and no more than kShort: the table may be wider than its sequences
+// are long, some SMs' rows longer than others'.  (At the edge: 10 x 3000 tokens
+// of 4 heads 18.2 us whole, 18.4 cut.)
 // per_row 0: a row may be too long for that, or there are too many rows.
 struct Share {
   int per_row, cluster;
@@ -302,9 +303,10 @@ struct Form {
   static constexpr bool Q_REG = Q_WORDS <= 32;                 // q fragments in registers
   static constexpr int Q_BYTES = Q_REG ? 0 : Q_WORDS * 128;
   // Warps: 16 of 128 registers where they suffice (int8 heads of 64, 64 x
-  // 8192 tokens: 143 us against 155 with 12 of 168; of 128, 301 against 249),
-  // else 12 (of 16 heads of 64: 37 us against 45 with 8; of 128: 41 against 29),
-  // 8 or 4 of 255.
+  // 8192 tokens: 143 us against 155 with 12 of 168; of 128 with scores: 301
+  // against 249), else 12 (64 x 8192 of 4 heads: 8 query heads of 128 to each
+  // 111 us against 132 with 8 warps, 16 of 64 107 against 126; but 16 of 128 283
+  // against 154), 8 or 4 of 255.
   static constexpr int W = NT == 1 && S8 && DP == 64 && !WIDE                               ? 16
                            : (NT == 1 && (S8 ? DP <= 128 : DP == 64)) || (DP == 64 && !WIDE) ? 12
                            : 8 * (Q_BYTES + 3 * SLOT) <= 208 * 1024                          ? 8
@@ -875,7 +877,8 @@ __global__ void __launch_bounds__(F::W * 32, 1) attend_kernel(const __grid_const
           for (int nt = 0; nt < NT; ++nt) {
             // a tile's sum by itself, then rounded to the whole: the tensor pipe
             // cuts its sums, always downwards (a row's 860 tiles lost 10^-4 of
-            // values of one sign that way; 64 x 8192 tokens took 240 us, not 249)
+            // values of one sign that way; 64 x 8192 tokens with scores took 240
+            // us so, and 249 with rounded sums)
             float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int p = F::NP - 1; p >= 0; --p) mma<false>(x, a0, a1, a2, a3, b0[nt][p], b1[nt][p]);
