@@ -578,6 +578,28 @@ int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* table, const 
                   int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, void* q_out,
                   int64_t q_out_token_stride, int64_t q_out_head_stride, const i8q_rotary* rotary, void* stream);
 
+/* Norms of the heads of q and k, each row by its root mean square:
+ *   m = (sum of the head_dim squares) / head_dim, rounded once to fp32 (the sum
+ *       in 48 bits at least, in fp64 where fp32's range does not hold it),
+ *   r = 1 / sqrt(m + eps),   y = (x * r) * weight,
+ * each operation rounded once in fp32. */
+typedef struct i8q_head_norm {
+  const void* q_weight; /* device [head_dim] of `type`; NULL: q is left as it is */
+  const void* k_weight; /* the same of k */
+  int type;             /* I8Q_F32 | I8Q_BF16 */
+  float eps;            /* >= 0, finite */
+} i8q_head_norm;
+
+/* i8q_kv_append with the heads of q and k normalized before they are turned,
+ * in the same pass (norm NULL, or without weights: i8q_kv_append itself).
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+int i8q_kv_append_norm(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq,
+                       const int32_t* index, int64_t tokens, int type, const void* k, int64_t k_token_stride,
+                       int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                       const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, void* q_out,
+                       int64_t q_out_token_stride, int64_t q_out_head_stride, const i8q_rotary* rotary,
+                       const i8q_head_norm* norm, void* stream);
+
 /* Read tokens back: k_out and v_out [tokens, kv_heads, head_dim] of `type`
  * (I8Q_F32 | I8Q_BF16) receive the values of token index[t] of sequence
  * seq[t] (rows with seq < 0 are not written).

@@ -497,33 +497,52 @@ def _rotary(positions, cos, sin, pair_axis, interleaved, tokens):
 
 
 def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions=None, cos=None, sin=None,
-              pair_axis=None, interleaved=False, stream=None):
+              pair_axis=None, interleaved=False, q_norm=None, k_norm=None, norm_eps=1e-6, stream=None):
     """Write tokens into the cache: token t becomes token index[t] of
     sequence seq[t] (int32; seq < 0: left out).  k, v [tokens, kv_heads,
     head_dim] fp32 or bf16, any token and head strides; q, q_out [tokens,
     q_heads, head_dim] of the same type (q_out may be q).  With cos and sin
     (fp32 [rows, pairs]) and positions (int32 [axes, tokens], or [tokens])
     q and k are turned first; pair_axis: the axis of each pair (default 0);
-    interleaved: pairs are (2j, 2j+1) instead of (j, j + pairs).  See
-    i8q_kv_append.  Returns q_out."""
+    interleaved: pairs are (2j, 2j+1) instead of (j, j + pairs).  With q_norm,
+    k_norm ([head_dim], both fp32 or both bf16; either may be None) each head
+    of q, k is first divided by the root of its mean square plus norm_eps and
+    multiplied by the weights.  See i8q_kv_append_norm.  Returns q_out."""
     if (cos is None) != (sin is None) or (cos is None) != (positions is None):
         raise ValueError("positions, cos and sin come together")
-    if q is None and q_out is not None:
-        raise ValueError("q_out needs q")
+    if q is None and (q_out is not None or q_norm is not None):
+        raise ValueError("q_out and q_norm need q")
     tokens, dtype = k.shape[0], k.dtype
     _, H, _, D = cache.shape
     rot = None
     if cos is not None:
         rot = ctypes.byref(_rotary(positions, cos, sin, pair_axis, interleaved, tokens))
+    norm = None if q_norm is None and k_norm is None else ctypes.byref(_head_norm(q_norm, k_norm, norm_eps, D))
     qs, qo, heads = (None, 0, 0), (None, 0, 0), 0
     if q is not None:
         heads = q.shape[1]
         qs, qo = _rows(q, "q", (tokens, heads, D), dtype), _rows(q_out, "q_out", (tokens, heads, D), dtype)
-    check(_L().i8q_kv_append(cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", tokens),
-                             _i32(index, "index", tokens), tokens, _float_type(k), *_rows(k, "k", (tokens, H, D), dtype),
-                             *_rows(v, "v", (tokens, H, D), dtype), *qs, heads, *qo, rot, _stream(stream)),
-          "kv_append")
+    check(_L().i8q_kv_append_norm(
+        cache._ref, ctypes.byref(_page_table(page_table)), _i32(seq, "seq", tokens), _i32(index, "index", tokens), tokens,
+        _float_type(k), *_rows(k, "k", (tokens, H, D), dtype), *_rows(v, "v", (tokens, H, D), dtype), *qs, heads, *qo, rot,
+        norm, _stream(stream)), "kv_append")
     return q_out
+
+
+def _head_norm(q_norm, k_norm, eps, dim):
+    dtypes = set()
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is None:
+            continue
+        if not isinstance(t, _Tensor) or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous CUDA tensor")
+        if t.shape != (dim,):
+            raise ValueError(f"{name} must be [{dim}]")
+        dtypes.add(t.dtype)
+        kind = _float_type(t)
+    if len(dtypes) > 1:
+        raise TypeError("q_norm and k_norm must have one dtype")
+    return _lib.HeadNormStruct(*(None if t is None else t.data_ptr() for t in (q_norm, k_norm)), kind, eps)
 
 
 def _float_type(t):

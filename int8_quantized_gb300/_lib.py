@@ -43,7 +43,13 @@ class RotaryStruct(ctypes.Structure):
                 ("rows", _i64), ("pairs", _i64), ("pair_axis", ctypes.c_char_p), ("interleaved", _i)]
 
 
-_cache, _table, _rotary = (ctypes.POINTER(c) for c in (KVCacheStruct, PageTableStruct, RotaryStruct))
+class HeadNormStruct(ctypes.Structure):
+    """i8q_head_norm"""
+    _fields_ = [("q_weight", _p), ("k_weight", _p), ("type", _i), ("eps", _f)]
+
+
+_cache, _table, _rotary, _norm = (ctypes.POINTER(c) for c in (KVCacheStruct, PageTableStruct, RotaryStruct,
+                                                              HeadNormStruct))
 
 # name -> (restype, argtypes); mirrors include/i8q.h
 SIGNATURES = {
@@ -87,6 +93,8 @@ SIGNATURES = {
     "i8q_dq_lstm_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i]),
     "i8q_kv_append": (_i, [_cache, _table, _p, _p, _i64, _i, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p,
                            _i64, _i64, _rotary, _p]),
+    "i8q_kv_append_norm": (_i, [_cache, _table, _p, _p, _i64, _i, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64,
+                                _p, _i64, _i64, _rotary, _norm, _p]),
     "i8q_kv_gather": (_i, [_cache, _table, _p, _p, _i64, _i, _p, _i64, _i64, _p, _i64, _i64, _p]),
     "i8q_paged_attention": (_i, [_cache, _table, _p, _i, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, _f, _i64, _i, _p,
                                  _sz, _p]),

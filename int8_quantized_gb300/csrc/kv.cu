@@ -1,5 +1,6 @@
 // kv.cu -- writing a paged key/value cache (rotary positions, int8 rows) and
 // reading it back, and the argument checks of all cache entry points.
+#include <cmath>
 #include <string>
 
 #include "kv.cuh"
@@ -133,13 +134,69 @@ __device__ __forceinline__ void store1(T* p, float v) {
   else *p = __float2bfloat16_rn(v);
 }
 
+// Norms of the heads of q and k (a NULL weight: that one is left as it is).
+struct Norm {
+  const void* q;
+  const void* k;
+  int bf16;
+  float eps;
+};
+__device__ __forceinline__ float weight_at(const Norm& n, const void* w, int e) {
+  return n.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]) : static_cast<const float*>(w)[e];
+}
+
+// a + b = sum + low, exactly (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float a, float b, float& low) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  low = __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v));
+  return s;
+}
+
+// 1 / sqrt(mean of squares + eps) of a row of dim elements, N of them in each
+// of the L lanes `lanes` (0 where a lane has fewer).  The sum of squares is
+// held as a sum of two fp32 numbers (48 bits: 10 instructions an element,
+// where fp64's one has 1/64 of the rate), so that the mean rounds once and
+// the row's codes do not depend on the order of its sum.  A sum outside
+// fp32's comfortable range, a zero row and one with an infinity or a NaN are
+// summed in fp64.
+template <int L, int N>
+__device__ __forceinline__ float inverse_rms(const float (&x)[N], int dim, float eps, uint32_t lanes) {
+  float s = 0.0f, low = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float p = __fmul_rn(x[i], x[i]), rest = __fmaf_rn(x[i], x[i], -p);
+    float e;
+    s = two_sum(s, p, e);
+    low = __fadd_rn(low, __fadd_rn(e, rest));
+  }
+#pragma unroll
+  for (int m = 1; m < L; m <<= 1) {
+    const float other = __shfl_xor_sync(lanes, s, m), other_low = __shfl_xor_sync(lanes, low, m);
+    float e;
+    s = two_sum(s, other, e);
+    low = __fadd_rn(__fadd_rn(low, other_low), e);
+  }
+  const float d = (float)dim, quotient = __fdiv_rn(s, d);
+  // s - quotient d is a fp32 number
+  float mean = __fadd_rn(quotient, __fdiv_rn(__fadd_rn(__fmaf_rn(-quotient, d, s), low), d));
+  if (!(s > 0x1p-60f && s < 0x1p126f)) {  // the same for the row's lanes: sums of the same two numbers in each step
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t += (double)x[i] * (double)x[i];
+#pragma unroll
+    for (int m = 1; m < L; m <<= 1) t += __shfl_xor_sync(lanes, t, m);
+    mean = (float)(t / dim);
+  }
+  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
+}
+
 // Rows of any alignment: one warp per row of q, k or v, lane l turns pairs
 // l, l + 32, ...  (16384 tokens of 48 rows of 128: 484 us, where rows that can
 // be read four elements at a time take 76 below.)
 template <class T, bool S8>
 __global__ void __launch_bounds__(256)
 append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
-              Rows q, Rows qo, Rows k, Rows v, Rotary r, uint32_t* status) {
+              Rows q, Rows qo, Rows k, Rows v, Rotary r, Norm norm, uint32_t* status) {
   const int lane = threadIdx.x & 31;
   const int per = q.heads + 2 * c.heads;
   const int half = c.dim / 2;
@@ -166,18 +223,32 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
     const Rows& in = which == 0 ? q : (which == 1 ? k : v);
     const T* src = static_cast<const T*>(in.p) + t * in.token + head * in.head;
     const int turned = which == 2 ? 0 : r.pairs;
-    float y[I8Q_KV_MAX_HEAD_DIM / 32];
+    float y[I8Q_KV_MAX_HEAD_DIM / 32] = {};
     int at[I8Q_KV_MAX_HEAD_DIM / 32];
     uint32_t most = 0;
 #pragma unroll
     for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 64; ++u) {
       const int j = lane + 32 * u;
       if (j < half) {
-        const bool rot = j < turned;
-        const bool split = rot && !r.interleaved;
+        const bool split = j < turned && !r.interleaved;
         const int e1 = split ? j : 2 * j, e2 = split ? j + r.pairs : 2 * j + 1;
-        float x1 = load1(src + e1), x2 = load1(src + e2);
-        if (rot) {
+        y[2 * u] = load1(src + e1), y[2 * u + 1] = load1(src + e2);
+        at[2 * u] = e1, at[2 * u + 1] = e2;
+      }
+    }
+    const void* weight = which == 0 ? norm.q : which == 1 ? norm.k : nullptr;
+    if (weight) {
+      const float inverse = inverse_rms<32>(y, c.dim, norm.eps, 0xffffffffu);
+#pragma unroll
+      for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 32; ++u)
+        if (lane + 32 * (u / 2) < half) y[u] = __fmul_rn(__fmul_rn(y[u], inverse), weight_at(norm, weight, at[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 64; ++u) {
+      const int j = lane + 32 * u;
+      if (j < half) {
+        float x1 = y[2 * u], x2 = y[2 * u + 1];
+        if (j < turned) {
           const int a = (r.axis[j >> 4] >> ((j & 15) * 2)) & 3;
           const int64_t g = (int64_t)r.positions[a * r.position_stride + t] * r.pairs + j;
           const float cs = r.cos[g], sn = r.sin[g];
@@ -186,7 +257,6 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
           x1 = y1;
         }
         y[2 * u] = x1, y[2 * u + 1] = x2;
-        at[2 * u] = e1, at[2 * u + 1] = e2;
         most = max(most, max(__float_as_uint(fabsf(x1)), __float_as_uint(fabsf(x2))));
       }
     }
@@ -291,10 +361,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
 // 128: 76 us, against 82 with 128 threads and 130 with 256).  The sums of two
 // products are scalar: the compiler fuses a paired sum with its products.
 constexpr int kUnitThreads = 64;
-template <class T, bool S8, int L>
+template <class T, bool S8, int L, bool NORM>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,
-                    Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, uint32_t* status) {
+                    Rows q, Rows qo, Rows k, Rows v, const __grid_constant__ Rotary r, Norm norm, uint32_t* status) {
   constexpr int G = kUnitThreads / L, NQ = 2;  // rows of q that a lane has in flight, beside one of k and one of v
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
@@ -325,6 +395,17 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   };
   send_kv(slot);
   send_q(slot);
+  const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
+  // the weights of a lane's elements, for all heads
+  float wq[8], wk[8];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = j < 4 ? h1 + j : h2 + j - 4;
+      wq[j] = norm.q && in_row ? weight_at(norm, norm.q, e) : 0.0f;
+      wk[j] = norm.k && in_row ? weight_at(norm, norm.k, e) : 0.0f;
+    }
+  }
   const int b = seq[t], i = index[t];
   const uint32_t axis = r.axis[u >> 2 & 7] >> ((u & 3) * 8) & 0xffu;  // two bits a pair
   int pos[4] = {0, 0, 0, 0};
@@ -357,10 +438,17 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   if (!ok && threadIdx.x == 0) kv::report_index(status);
   if (ok) ok = kv::find(c, tab, b, i, page, off, status);
   if (!ok) return;
-  auto turned = [&](const Four<T> (&x)[2], float (&y)[8], bool really) {
+  auto values = [&](const Four<T> (&x)[2], float (&y)[8]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = x[0].at(j), y[4 + j] = x[1].at(j);
-    if (!really) return;
+  };
+  auto normed = [&](float (&y)[8], const float (&w)[8]) {  // by all lanes of a row
+    const float inverse = inverse_rms<L>(y, c.dim, norm.eps, lanes);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(y[j], inverse), w[j]);
+  };
+  auto turned = [&](float (&y)[8]) {
+    if (!turns) return;
     // pair j: elements j of the two halves, or two neighbours
     if (r.interleaved) {
 #pragma unroll
@@ -374,17 +462,20 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   for (int head = slot; head < q.heads;) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
-      if (head + n * step < q.heads && in_row) {
-        float y[8];
-        turned(xq[n], y, turns);
+      if (head + n * step < q.heads && (NORM || in_row)) {
+        float y[8] = {};
+        if (in_row) values(xq[n], y);
+        if constexpr (NORM) {
+          if (norm.q) normed(y, wq);
+        }
+        turned(y);
         T* o = o_row + (head + n * step) * qo.head;
-        store4(o + h1, y), store4(o + h2, y + 4);
+        if (in_row) store4(o + h1, y), store4(o + h2, y + 4);
       }
     head += NQ * step;
     send_q(head);
   }
   const int64_t at = kv::row_at(c, page, 0, off), scale_at = kv::scale_at(c, page, 0, off);
-  const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
   auto put = [&](void* pool, float* scale, const float (&y)[8], int p1, int p2, int64_t dst, int64_t sc) {
     if constexpr (!S8) {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(pool) + dst;
@@ -410,9 +501,13 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   for (int head = slot; head < c.heads;) {  // (the same for the L lanes of a row)
     const int64_t dst = at + head * c.head_stride, sc = scale_at + head * c.s_head;
     float y[8] = {};
-    if (in_row) turned(xk, y, turns);
+    if (in_row) values(xk, y);
+    if constexpr (NORM) {
+      if (norm.k) normed(y, wk);
+    }
+    turned(y);
     put(c.k, c.ks, y, h1, h2, dst, sc);
-    if (in_row) turned(xv, y, false);
+    if (in_row) values(xv, y);
     put(c.v, c.vs, y, e1, e2, dst, sc);
     if (c.score && u == 0) c.score[sc] = 0.0f;
     head += step;
@@ -546,12 +641,12 @@ int with_types(int type, int cache_type, F f) {
 
 using namespace i8q;
 
-extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq,
-                             const int32_t* index, int64_t tokens, int type, const void* k, int64_t k_token_stride,
-                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
-                             const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
-                             void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
-                             const i8q_rotary* rotary, void* stream) {
+extern "C" int i8q_kv_append_norm(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq,
+                                  const int32_t* index, int64_t tokens, int type, const void* k, int64_t k_token_stride,
+                                  int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                  const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                                  void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                  const i8q_rotary* rotary, const i8q_head_norm* norm, void* stream) {
   Cache c;
   Table tab;
   int rc = kv::check_cache(cache, "kv_append", c);
@@ -583,6 +678,18 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
     r.rows = (int)rotary->rows, r.pairs = (int)rotary->pairs, r.axes = (int)rotary->axes;
     r.interleaved = rotary->interleaved != 0;
   }
+  Norm n{};
+  if (norm && (norm->q_weight || norm->k_weight)) {
+    if (norm->type != I8Q_F32 && norm->type != I8Q_BF16)
+      return fail(I8Q_ERR_INVALID_ARG, "kv_append: the norms' type must be I8Q_F32 or I8Q_BF16");
+    if (!(norm->eps >= 0.0f) || std::isinf(norm->eps))
+      return fail(I8Q_ERR_INVALID_ARG, "kv_append: the norms' eps must be finite and not negative");
+    if (norm->q_weight && !q_heads) return fail(I8Q_ERR_INVALID_ARG, "kv_append: a norm of q needs q");
+    const uintptr_t es = norm->type == I8Q_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(norm->q_weight) % es || reinterpret_cast<uintptr_t>(norm->k_weight) % es)
+      return fail(I8Q_ERR_INVALID_ARG, "kv_append: the norms' weights are not aligned to their type");
+    n = Norm{norm->q_weight, norm->k_weight, norm->type == I8Q_BF16, norm->eps};
+  }
   if (tokens == 0) return I8Q_OK;
   uint32_t* status = device_status_word();
   if (!status) return fail(I8Q_ERR_CUDA, "kv_append: no status word");
@@ -604,15 +711,30 @@ extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* ta
         // at least
         const int64_t most = ceil_div(std::max<int64_t>(q_heads, c.heads), kUnitThreads / L);
         const int splits = (int)std::max<int64_t>(1, std::min(most, 16 * sm_count() / tokens));
-        return kv::launch(append_units_kernel<T, decltype(s8)::value, L>, (unsigned)(tokens * splits), kUnitThreads, 0, 1, s,
-                          "kv_append", c, tab, seq, index, splits, rq, ro, rk, rv, r, status);
+        auto run = [&](auto kernel) {
+          return kv::launch(kernel, (unsigned)(tokens * splits), kUnitThreads, 0, 1, s, "kv_append", c, tab, seq, index,
+                            splits, rq, ro, rk, rv, r, n, status);
+        };
+        constexpr bool S8 = decltype(s8)::value;
+        return n.q || n.k ? run(append_units_kernel<T, S8, L, true>) : run(append_units_kernel<T, S8, L, false>);
       });
     const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (q_heads + 2 * c.heads), 8), (int64_t)sm_count() * 64);
     append_kernel<T, decltype(s8)::value>
-        <<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rq, ro, rk, rv, r, status);
+        <<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rq, ro, rk, rv, r, n, status);
     I8Q_LAUNCH_CHECK("kv_append");
     return I8Q_OK;
   });
+}
+
+extern "C" int i8q_kv_append(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq,
+                             const int32_t* index, int64_t tokens, int type, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                             void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                             const i8q_rotary* rotary, void* stream) {
+  return i8q_kv_append_norm(cache, table, seq, index, tokens, type, k, k_token_stride, k_head_stride, v, v_token_stride,
+                            v_head_stride, q, q_token_stride, q_head_stride, q_heads, q_out, q_out_token_stride,
+                            q_out_head_stride, rotary, nullptr, stream);
 }
 
 extern "C" int i8q_kv_gather(const i8q_kv_cache* cache, const i8q_page_table* table, const int32_t* seq,
