@@ -29,6 +29,7 @@
  *  [DQL]  ONNX Runtime contrib schemas, "DequantizeLinear" ver 1.
  *  [QLC]  onnx-light docs, "QLinearConv" (since version 10): inputs, bias
  *         rule, type constraints.
+ *  [NBITS] ONNX Runtime contrib schemas, "MatMulNBits": bits = 4.
  *  [LSTM] ONNX Runtime contrib schemas, "DynamicQuantizeLSTM": attributes,
  *         inputs X, W, R, B, initial_h, initial_c, W/R scale and zero point,
  *         outputs Y, Y_h, Y_c.
@@ -385,6 +386,40 @@ int i8q_dynamic_quantize_matmul(const float* A, int64_t M, int64_t K, const void
 /* Scratch bytes of i8q_matmul_integer_to_float / i8q_dynamic_quantize_matmul
  * for M x N x K (0 for sizes below 1). */
 size_t i8q_matmul_integer_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* ========================================================================
+ * MatMulNBits [NBITS]: products of a few rows of activations with weights of
+ * 4 bits, what a model that answers a token at a time spends its time on.
+ *   Y[m][n] = sum_k A[m][k] (q[n][k] - z[n][k / block_size]) s[n][k / block_size] + bias[n]
+ *   B: device uint8 [N][blocks][block_size / 2], blocks = ceil(K / block_size);
+ *   two codes to a byte, the even k in the low half.  scales: device [N]
+ *   [blocks] of scale_type (I8Q_F32 | I8Q_BF16).  zero_points: device uint8
+ *   [N][ceil(blocks / 2)], two to a byte, the even block in the low half, or
+ *   NULL (8).  block_size 16, 32, 64, 128 or 256 (the schema's bits = 4; its
+ *   other sizes, g_idx and float zero points are not taken).
+ * The matrix is laid out once, by i8q_matmul_nbits_pack, into a buffer of
+ * i8q_matmul_nbits_packed_size bytes (0 for arguments that the others
+ * refuse), 16-byte aligned, that belongs to the caller; B, scales and
+ * zero_points are not read again.
+ * Errors: INVALID_ARG, UNSUPPORTED (block_size), CUDA. */
+size_t i8q_matmul_nbits_packed_size(int64_t N, int64_t K, int64_t block_size, int scale_type, int has_zero);
+
+int i8q_matmul_nbits_pack(int64_t N, int64_t K, int64_t block_size, const uint8_t* B, const void* scales, int scale_type,
+                          const uint8_t* zero_points, void* packed, size_t packed_bytes, void* stream);
+
+/* A: device (M, K) of `type` (I8Q_F32 | I8Q_BF16), rows lda elements apart; Y:
+ * (M, N) of the same type, rows ldy apart; bias: device fp32 [N], or NULL.
+ * N .. has_zero as the matrix was packed with.  Any M; the call is made for
+ * few rows: it reads the matrix again for every 32 of them (8 of fp32).
+ * Weights and activations enter the products exactly (fp32 activations in
+ * three parts of 8 bits), a block's products are summed by the tensor pipe
+ * (for fp32, 16 of them) and blocks in fp32, rounded; the order does not
+ * depend on the run.  Y is rounded once at the end.  A row that holds an
+ * infinity or a NaN gives such values in that row alone.  No workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED (block_size), CUDA. */
+int i8q_matmul_nbits(const void* A, int type, int64_t M, int64_t lda, const void* packed, size_t packed_bytes, int64_t N,
+                     int64_t K, int64_t block_size, int scale_type, int has_zero, const float* bias, void* Y, int64_t ldy,
+                     void* stream);
 
 /* ========================================================================
  * Quantized elementwise operators [QEW].  Scales and zero points are

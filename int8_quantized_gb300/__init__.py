@@ -17,7 +17,7 @@ from ._lib import (ACT_GELU, ACT_IDENTITY, ACT_RELU, BF16, F32, LSTM_BIDIRECTION
 
 __all__ = ["QGemmDyn", "quantize_linear", "dequantize_linear", "qlinearconv", "qlinearconv_workspace_size",
            "dq_lstm_forward", "dq_lstm_forward_ex", "dq_lstm_state_codes", "dq_lstm_workspace_size", "sync_status",
-           "KVCache", "kv_append", "kv_gather", "kv_evict", "paged_attention", "paged_attention_workspace_size",
+           "MatMulNBits", "KVCache", "kv_append", "kv_gather", "kv_evict", "paged_attention", "paged_attention_workspace_size",
            "version", "I8QError", "last_error",
            "F32", "BF16", "S8", "U8", "S32", "ACT_IDENTITY", "ACT_RELU", "ACT_GELU", "NO_AXIS",
            "LSTM_FORWARD", "LSTM_REVERSE", "LSTM_BIDIRECTIONAL"]
@@ -361,6 +361,67 @@ def dynamic_quantize_matmul(A, B, b_scale, Y, b_zero_point=None, bias=None, a_sc
         _dev(a_zero_point_out, "a_zero_point_out", torch.uint8), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)), "dynamic_quantize_matmul")
     return Y
+
+
+class MatMulNBits:
+    """A matrix of 4-bit weights and its products with a few rows of
+    activations (i8q_matmul_nbits): the ONNX Runtime contrib operator.
+
+    B uint8 [N, blocks, block_size / 2], blocks = ceil(K / block_size), two
+    codes to a byte; scales fp32 or bf16 [N, blocks] (or flat); zero_points
+    uint8 [N, ceil(blocks / 2)] (or flat), two to a byte, or None (8); bias
+    fp32 [N] or None.  The matrix is laid out once, here (on `stream`, or the
+    current one); afterwards B, scales and zero_points may go."""
+
+    def __init__(self, B, scales, K, block_size, zero_points=None, bias=None, stream=None):
+        N, blocks = B.shape[0], -(-K // block_size)
+        if B.dtype != torch.uint8 or B.numel() != N * blocks * (block_size // 2):
+            raise ValueError(f"B must be uint8 [{N}, {blocks}, {block_size // 2}]")
+        if scales.numel() != N * blocks:
+            raise ValueError(f"scales must be [{N}, {blocks}]")
+        if zero_points is not None and zero_points.numel() != N * -(-blocks // 2):
+            raise ValueError(f"zero_points must be [{N}, {-(-blocks // 2)}]")
+        if bias is not None and bias.shape != (N,):
+            raise ValueError(f"bias must be [{N}]")
+        self._scale_type = _float_type(scales)
+        ptrs = (_dev(B, "B"), _dev(scales, "scales"), _dev(zero_points, "zero_points", torch.uint8),
+                _dev(bias, "bias", torch.float32))
+        self.device = B.device
+        if any(t is not None and t.device != B.device for t in (scales, zero_points, bias)):
+            raise ValueError("B, scales, zero_points and bias must lie on one device")
+        _on_current(B, "B")
+        self.N, self.K, self.block_size, self.bias = N, K, block_size, bias
+        self._zero = int(zero_points is not None)
+        size = int(_L().i8q_matmul_nbits_packed_size(N, K, block_size, self._scale_type, self._zero))
+        if size == 0:
+            raise I8QError(_lib.ERR_UNSUPPORTED, "matmul_nbits_packed_size")
+        self.packed = _workspace(size, B.device, stream)
+        check(_L().i8q_matmul_nbits_pack(N, K, block_size, ptrs[0], ptrs[1], self._scale_type, ptrs[2],
+                                         self.packed.data_ptr(), size, _stream(stream)), "matmul_nbits_pack")
+        self._args = (self.packed.data_ptr(), size, N, K, block_size, self._scale_type, self._zero, ptrs[3])
+
+    def forward(self, A, Y, stream=None):
+        """Y [rows, N] = A [rows, K] times the matrix, both fp32 or both bf16,
+        rows of any stride.  Returns Y."""
+        if not isinstance(A, _Tensor) or not isinstance(Y, _Tensor) or A.device != self.device or Y.device != self.device:
+            raise TypeError(f"A and Y must be tensors on {self.device}")
+        if Y.dtype != A.dtype:
+            raise TypeError("A and Y must have one dtype")
+        if A.dim() != 2 or A.shape[1] != self.K or Y.shape != (A.shape[0], self.N):
+            raise ValueError(f"A must be [rows, {self.K}] and Y [rows, {self.N}]")
+        (lda, one), (ldy, also) = A.stride(), Y.stride()
+        if (one != 1 and self.K > 1) or (also != 1 and self.N > 1):
+            raise ValueError("A and Y must have contiguous rows")
+        _on_current(A, "A")
+        check(_L().i8q_matmul_nbits(A.data_ptr(), _float_type(A), A.shape[0], lda, *self._args, Y.data_ptr(), ldy,
+                                    _stream(stream)), "matmul_nbits")
+        return Y
+
+
+def _on_current(t, name):
+    """The kernels run on the current device."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lies on {t.device}, which is not the current device")
 
 
 QLINEAR_ADD, QLINEAR_MUL = 0, 1

@@ -80,6 +80,9 @@ SIGNATURES = {
     "i8q_matmul_integer_to_float": (_i, [_p, _i, _i64, _i64, _p, _i, _i64, _p, _p, _sz, _p, _p, _sz, _p, _p, _p, _sz,
                                          _p]),
     "i8q_dynamic_quantize_matmul": (_i, [_p, _i64, _i64, _p, _i, _i64, _p, _p, _sz, _p, _p, _p, _p, _p, _sz, _p]),
+    "i8q_matmul_nbits_packed_size": (_sz, [_i64, _i64, _i64, _i, _i]),
+    "i8q_matmul_nbits_pack": (_i, [_i64, _i64, _i64, _p, _p, _i, _p, _p, _sz, _p]),
+    "i8q_matmul_nbits": (_i, [_p, _i, _i64, _i64, _p, _sz, _i64, _i64, _i64, _i, _i, _p, _p, _i64, _p]),
     "i8q_matmul_integer_workspace_size": (_sz, [_i64, _i64, _i64]),
     "i8q_dq_lstm_forward_ex": (_i, [_p, _i64, _i64, _i64, _i64, _i, _p, _p, _i, _p, _p, _sz, _p, _p, _sz, _p, _p, _p,
                                     _p, _p, _f, _i, _p, _sz, _p, _sz, _p, _sz, _p, _p, _p, _p, _sz, _p]),

@@ -1,0 +1,441 @@
+// nbits.cu -- MatMulNBits [NBITS]: products of a few rows of fp32 or bf16
+// activations with weights of 4 bits that have a scale, and perhaps a zero
+// point, per block of their row:
+//   Y[m][n] = sum_k A[m][k] (q[n][k] - z[n][k / block]) s[n][k / block] + bias[n].
+#include <cooperative_groups.h>
+
+#include <string>
+
+#include "nbits.cuh"
+
+namespace i8q {
+namespace {
+
+namespace cg = cooperative_groups;
+using nbits::kCodeBytes;
+using nbits::kTileK;
+using nbits::kTileN;
+using nbits::Shape;
+
+constexpr int64_t kMost = INT32_MAX - 65536;  // of N, K and M: indices of 32 bits step past them by a tile or two
+
+int check_shape(int64_t N, int64_t K, int64_t block, int scale_type, bool has_zero, const char* who, Shape& out) {
+  const std::string w = who;
+  if (N < 1 || K < 1 || N > kMost || K > kMost) return fail(I8Q_ERR_INVALID_ARG, w + ": N and K must be 1 .. 2^31 - 2^16");
+  if (scale_type != I8Q_F32 && scale_type != I8Q_BF16)
+    return fail(I8Q_ERR_INVALID_ARG, w + ": scales must be I8Q_F32 or I8Q_BF16");
+  if (block != 16 && block != 32 && block != 64 && block != 128 && block != 256)
+    return fail(I8Q_ERR_UNSUPPORTED, w + ": block_size must be 16, 32, 64, 128 or 256");
+  out.N = N, out.K = K, out.block = (int)block;
+  out.scale_size = scale_type == I8Q_F32 ? 4 : 2, out.has_zero = has_zero;
+  out.strips = ceil_div(N, kTileN), out.chunks = ceil_div(K, kTileK);
+  out.per = kTileK / (int)std::min<int64_t>(block, kTileK);
+  out.tile_bytes = kCodeBytes + kTileN * out.per * (out.scale_size + (has_zero ? 1 : 0));
+  return I8Q_OK;
+}
+
+// ---- layout -------------------------------------------------------------
+// A CTA a tile: a thread writes one word of codes, then shares of the scales
+// and zero points.  Once per matrix; nothing depends on its speed.
+__global__ void __launch_bounds__(256)
+pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ scales, const uint8_t* __restrict__ zeros,
+            uint8_t* __restrict__ packed) {
+  kv::wait_previous_kernel();
+  const int64_t blocks = (s.K + s.block - 1) / s.block;
+  const int64_t row_bytes = blocks * (s.block / 2), zero_bytes = (blocks + 1) / 2;
+  for (int64_t tile = blockIdx.x; tile < s.strips * s.chunks; tile += gridDim.x) {
+    const int64_t strip = tile / s.chunks, chunk = tile - strip * s.chunks;
+    uint8_t* to = packed + tile * s.tile_bytes;
+    {
+      const int half = threadIdx.x / 128, lane = threadIdx.x / 4 % 32, b = threadIdx.x % 4;
+      const int64_t n = strip * kTileN + 8 * half + lane / 4;
+      uint32_t word = 0;
+      for (int st = 0; st < 2; ++st)
+        for (int j = 0; j < 4; ++j) {
+          const int64_t k = chunk * kTileK + 32 * b + 16 * st + 4 * (lane % 4) + j;
+          // past the matrix: code 0, which no activation or a scale of 0 meets
+          const uint32_t code = n < s.N && k < s.K ? B[n * row_bytes + k / 2] >> (4 * (k & 1)) & 15u : 0u;
+          word |= code << 4 * (2 * st + j / 2 + 4 * (j % 2));
+        }
+      reinterpret_cast<uint32_t*>(to)[threadIdx.x] = word;
+    }
+    for (int i = threadIdx.x; i < kTileN * s.per; i += blockDim.x) {
+      const int64_t n = strip * kTileN + i / s.per, block = (chunk * kTileK + i % s.per * (kTileK / s.per)) / s.block;
+      const bool in = n < s.N && block < blocks;
+      if (s.scale_size == 4)
+        reinterpret_cast<float*>(to + kCodeBytes)[i] = in ? static_cast<const float*>(scales)[n * blocks + block] : 0.0f;
+      else
+        reinterpret_cast<uint16_t*>(to + kCodeBytes)[i] = in ? static_cast<const uint16_t*>(scales)[n * blocks + block] : 0;
+      if (s.has_zero)
+        to[kCodeBytes + kTileN * s.per * s.scale_size + i] =
+            in ? zeros[n * zero_bytes + block / 2] >> (4 * (block & 1)) & 15u : 8u;
+    }
+  }
+}
+
+// ---- product ------------------------------------------------------------
+struct Args {
+  Shape s;
+  const uint8_t* packed;
+  const void* A;
+  int64_t lda;
+  int a_aligned;  // four neighbouring activations can be read at once
+  const float* bias;
+  void* Y;
+  int64_t ldy;
+  int M;
+  int wk, wf;     // warps along k, strips at a time: wk * wf warps
+  int clusters;   // of a tile of rows
+};
+
+// Tiles of a warp's ring, one of which is being read while the others arrive.
+constexpr int ring_depth(int nt) { return nt == 4 ? 4 : 6; }
+constexpr int kRound = 16;  // groups of strips between two meetings of a cluster
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// Two codes at nibbles 0 and 4 of w as bf16 numbers less their zero point:
+// 0x43 over a byte c < 128 is 128 + c, and 128 + z is subtracted exactly.
+__device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t zero) {
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+  return r;
+}
+
+// A fragment of activations: four neighbours of row m from k on, as bf16
+// pairs; fp32 in three parts of 8 bits cut off one after the other, which are
+// all of its 24 (an infinity or a NaN in the first part alone).
+template <class T>
+struct Fragment;
+template <>
+struct Fragment<__nv_bfloat16> {
+  static constexpr int kParts = 1;
+  uint32_t b[1][2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, bool live, bool aligned) {
+    b[0][0] = b[0][1] = 0;
+    if (!live) return;
+    if (aligned && k + 4 <= K) {
+      const uint2 v = *reinterpret_cast<const uint2*>(row + k);
+      b[0][0] = v.x, b[0][1] = v.y;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k + j < K)
+        b[0][j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[k + j] << (16 * (j & 1));
+  }
+};
+template <>
+struct Fragment<float> {
+  static constexpr int kParts = 3;
+  uint32_t b[3][2];
+  __device__ __forceinline__ void load(const float* row, int k, int K, bool live, bool aligned) {
+    float x[4] = {};
+    if (live) {
+      if (aligned && k + 4 <= K) {
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(row + k);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < K) x[j] = row[k + j];
+      }
+    }
+    uint32_t part[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = __float_as_uint(x[j]);
+      const bool odd = (u & 0x7f800000u) == 0x7f800000u;
+      // a NaN keeps a bit of its mantissa
+      part[0][j] = (u >> 16) | (odd && (u & 0x7fffffu) ? 0x40u : 0u);
+      const float r1 = odd ? 0.0f : __fsub_rn(x[j], __uint_as_float(u & 0xffff0000u));
+      part[1][j] = __float_as_uint(r1) >> 16;
+      const float r2 = __fsub_rn(r1, __uint_as_float(__float_as_uint(r1) & 0xffff0000u));
+      part[2][j] = __float_as_uint(r2) >> 16;
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) b[p][0] = part[p][0] | part[p][1] << 16, b[p][1] = part[p][2] | part[p][3] << 16;
+  }
+};
+
+__device__ __forceinline__ void store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// A warp has the activations of its share of k (at most C chunks of 128; C 0:
+// read again for each tile) in registers, as the fragments of the products,
+// and streams the tiles of one strip of 16 outputs after the other through a
+// ring of its own in shared memory, each lane copying what it will read.  The
+// warps of a strip add their sums up in shared memory, those of a cluster's
+// CTAs through it.  NT: tiles of 8 rows.  G: the block, at most 128.  The
+// products of a block are summed by the tensor pipe from 0 and enter the row's
+// sum by a rounded fma with the block's scale (the pipe cuts sums instead of
+// rounding them; for fp32 activations only one step's 16 products are left to
+// it).
+template <class T, int NT, int C, int G>
+__global__ void __launch_bounds__(512, 1)
+nbits_kernel(const __grid_constant__ Args a) {
+  constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128, kDepth = ring_depth(NT), kAhead = kDepth - 1;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int S = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane & 3;
+  const int wk = warp % a.wk, wf = warp / a.wk;
+  const int cluster = blockIdx.x / S, rows0 = cluster / a.clusters * (8 * NT), c0 = cluster % a.clusters;
+  const int chunks = (int)a.s.chunks, strips = (int)a.s.strips;
+  const int parts = a.wk * S, part = rank * a.wk + wk;
+  const int c_begin = (int)((int64_t)part * chunks / parts), cw = (int)((int64_t)(part + 1) * chunks / parts) - c_begin;
+  const int groups = (strips + a.wf - 1) / a.wf, ng = (groups - c0 + a.clusters - 1) / a.clusters;
+  uint8_t* const ring = smem + (size_t)warp * kDepth * a.s.tile_bytes;
+  float* const partial = reinterpret_cast<float*>(smem + (size_t)a.wk * a.wf * kDepth * a.s.tile_bytes);
+  float* const held = partial + 2 * a.wk * a.wf * kOut;
+
+  kv::next_kernel_may_start();
+  kv::wait_previous_kernel();
+
+  // the ring's next tile: group ig of this warp, chunk ic of it
+  int ig = 0, ic = 0, slot_in = 0;
+  const int meta = (a.s.tile_bytes - kCodeBytes) / 16;
+  auto send = [&] {
+    if (cw && ig < ng) {
+      const int strip = (c0 + ig * a.clusters) * a.wf + wf;
+      if (strip < strips) {
+        const uint8_t* from = a.packed + ((int64_t)strip * chunks + c_begin + ic) * a.s.tile_bytes;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + slot_in * a.s.tile_bytes;
+        copy16(to + lane * 16, from + lane * 16);
+        copy16(to + 512 + lane * 16, from + 512 + lane * 16);
+        for (int i = lane; i < meta; i += 32) copy16(to + kCodeBytes + i * 16, from + kCodeBytes + i * 16);
+      }
+      if (++ic == cw) ic = 0, ++ig;
+    }
+    commit();
+    slot_in = slot_in + 1 == kDepth ? 0 : slot_in + 1;
+  };
+  for (int i = 0; i < kAhead; ++i) send();
+
+  const T* const A = static_cast<const T*>(a.A);
+  Fragment<T> x[C ? C : 1][8][NT];
+  auto load_x = [&](int slot, int c) {
+#pragma unroll
+    for (int st = 0; st < 8; ++st)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int m = rows0 + nt * 8 + g;
+        x[slot][st][nt].load(A + (int64_t)m * a.lda, (c_begin + c) * kTileK + st * 16 + 4 * t, (int)a.s.K,
+                             c < cw && m < a.M, a.a_aligned);
+      }
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) load_x(c, c);
+
+  int slot = 0;
+  auto tile = [&](const Fragment<T> (&xc)[8][NT], float (&y)[NT][4]) {
+    wait_copies<kAhead - 1>();
+    __syncwarp();  // the scales and zero points were copied by other lanes, and all have read the tile before
+    send();
+    const uint8_t* const at = ring + slot * a.s.tile_bytes;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    const uint4 q0 = *reinterpret_cast<const uint4*>(at + lane * 16), q1 = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
+    float s0[kPer], s1[kPer];
+    if (a.s.scale_size == 4) {
+      const float* sc = reinterpret_cast<const float*>(at + kCodeBytes);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s0[i] = sc[g * kPer + i], s1[i] = sc[(g + 8) * kPer + i];
+    } else {
+      const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(at + kCodeBytes);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s0[i] = __bfloat162float(sc[g * kPer + i]), s1[i] = __bfloat162float(sc[(g + 8) * kPer + i]);
+    }
+    uint32_t z0[kPer], z1[kPer];
+    const uint8_t* zs = at + kCodeBytes + kTileN * kPer * a.s.scale_size;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      z0[i] = z1[i] = 0x43084308u;
+      if (a.s.has_zero) z0[i] = 0x43004300u | zs[g * kPer + i] * 0x10001u, z1[i] = 0x43004300u | zs[(g + 8) * kPer + i] * 0x10001u;
+    }
+    const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
+    float acc[NT][4] = {};
+#pragma unroll
+    for (int st = 0; st < 8; ++st) {
+      const int i = st * 16 / G;
+      const uint32_t v0 = w0[st / 2] >> (8 * (st & 1)), v1 = w1[st / 2] >> (8 * (st & 1));
+      const uint32_t f[4] = {pair(v0, z0[i]), pair(v1, z1[i]), pair(v0 >> 4, z0[i]), pair(v1 >> 4, z1[i])};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int p = kParts - 1; p >= 0; --p) mma(acc[nt], f, xc[st][nt].b[p]);
+      }
+      if (kParts > 1 || (st + 1) * 16 % G == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          y[nt][0] = __fmaf_rn(acc[nt][0], s0[i], y[nt][0]), y[nt][1] = __fmaf_rn(acc[nt][1], s0[i], y[nt][1]);
+          y[nt][2] = __fmaf_rn(acc[nt][2], s1[i], y[nt][2]), y[nt][3] = __fmaf_rn(acc[nt][3], s1[i], y[nt][3]);
+          acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+        }
+      }
+    }
+  };
+
+  T* const Y = static_cast<T*>(a.Y);
+  auto put = [&](int group, int e, float v) {  // e: strip of the group, row, output
+    const int m = rows0 + e % kOut / 16;
+    const int64_t n = ((int64_t)(c0 + group * a.clusters) * a.wf + e / kOut) * kTileN + e % 16;
+    if (m >= a.M || n >= a.s.N) return;
+    if (a.bias) v = __fadd_rn(v, a.bias[n]);
+    store(Y + (int64_t)m * a.ldy + n, v);
+  };
+
+  for (int gi = 0; gi < ng; ++gi) {
+    const bool live = (c0 + gi * a.clusters) * a.wf + wf < strips;
+    float y[NT][4] = {};
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c < cw) {
+          if (live) tile(x[c], y);
+          else send(), slot = slot + 1 == kDepth ? 0 : slot + 1;
+        }
+    } else {
+      for (int c = 0; c < cw; ++c) {
+        load_x(0, c);
+        if (live) tile(x[0], y);
+        else send(), slot = slot + 1 == kDepth ? 0 : slot + 1;
+      }
+    }
+    float* const mine = partial + (gi & 1) * a.wk * a.wf * kOut;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      *reinterpret_cast<float4*>(mine + ((wf * a.wk + wk) * NT + nt) * 128 + lane * 4) =
+          make_float4(y[nt][0], y[nt][1], y[nt][2], y[nt][3]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.wf * kOut; e += blockDim.x) {
+      const int m = e % kOut / 16, f = e % 16;
+      const float* p = mine + (e / kOut * a.wk * NT + m / 8) * 128 + ((f & 7) * 4 + (m & 7) / 2) * 4 + (m & 1) + 2 * (f / 8);
+      float v = 0.0f;
+      for (int w = 0; w < a.wk; ++w) v = __fadd_rn(v, p[w * kOut]);
+      if (S == 1) put(gi, e, v);
+      else held[(gi % kRound) * a.wf * kOut + e] = v;
+    }
+    if (S > 1 && (gi % kRound == kRound - 1 || gi == ng - 1)) {
+      cg::this_cluster().sync();
+      const int first = gi / kRound * kRound, n = (gi - first + 1) * a.wf * kOut;
+      for (int e = rank * blockDim.x + threadIdx.x; e < n; e += S * blockDim.x) {
+        float v = 0.0f;
+        for (int r = 0; r < S; ++r) v = __fadd_rn(v, cg::this_cluster().map_shared_rank(held, r)[e]);
+        put(first + e / (a.wf * kOut), e % (a.wf * kOut), v);
+      }
+      cg::this_cluster().sync();
+    }
+  }
+}
+
+constexpr int kWarps = 16;
+
+template <class T, int NT, int C>
+int run_block(Args& a, int S, cudaStream_t s) {
+  const int warps = a.wk * a.wf;
+  const int64_t row_tiles = ceil_div(a.M, 8 * NT), groups = ceil_div(a.s.strips, a.wf);
+  a.clusters = (int)std::min<int64_t>(groups, std::max<int64_t>(1, sm_count() / S / row_tiles));
+  const int smem = warps * ring_depth(NT) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
+  if (row_tiles * a.clusters * S > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: too many rows");
+  auto run = [&](auto kernel) {
+    return kv::launch(kernel, (unsigned)(row_tiles * a.clusters * S), 32 * warps, smem, S, s, "matmul_nbits", a);
+  };
+  switch (a.s.per) {
+    case 8: return run(nbits_kernel<T, NT, C, 16>);
+    case 4: return run(nbits_kernel<T, NT, C, 32>);
+    case 2: return run(nbits_kernel<T, NT, C, 64>);
+    default: return run(nbits_kernel<T, NT, C, 128>);
+  }
+}
+
+int run_product(Args& a, int type, cudaStream_t s) {
+  const int64_t chunks = a.s.chunks;
+  a.wk = (int)std::min<int64_t>(kWarps, chunks);
+  a.wf = (int)std::max<int64_t>(1, std::min<int64_t>(kWarps / a.wk, ceil_div(a.s.strips, sm_count())));
+  int S = 1;
+  const auto share = [&] { return ceil_div(chunks, (int64_t)a.wk * S); };  // chunks of a warp
+  // the most rows a pass whose activations 8 clusters' CTAs hold
+  const int most = type == I8Q_F32 ? 1 : 4;
+  int nt = type == I8Q_F32 || a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
+  const auto room = [&] { return type == I8Q_F32 ? most : most / nt; };  // chunks that a warp's registers hold
+  while (nt > 1 && ceil_div(chunks, (int64_t)a.wk * 8) > room()) nt /= 2;
+  while (S < 8 && share() > room()) S *= 2;
+  while (S < 8 && a.s.strips * S * 2 <= sm_count() && chunks >= (int64_t)kWarps * S * 2) S *= 2;
+  const bool held = share() <= room();
+  if (type == I8Q_F32) return held ? run_block<float, 1, 1>(a, S, s) : run_block<float, 1, 0>(a, S, s);
+  using B = __nv_bfloat16;
+  if (!held) return run_block<B, 1, 0>(a, S, s);
+  const bool one = share() == 1;
+  if (nt == 4) return run_block<B, 4, 1>(a, S, s);
+  if (nt == 2) return one ? run_block<B, 2, 1>(a, S, s) : run_block<B, 2, 2>(a, S, s);
+  return share() <= 2 ? run_block<B, 1, 2>(a, S, s) : run_block<B, 1, 4>(a, S, s);
+}
+
+}  // namespace
+}  // namespace i8q
+
+using namespace i8q;
+
+extern "C" size_t i8q_matmul_nbits_packed_size(int64_t N, int64_t K, int64_t block_size, int scale_type, int has_zero) {
+  Shape s;
+  if (check_shape(N, K, block_size, scale_type, has_zero != 0, "matmul_nbits_packed_size", s) != I8Q_OK) return 0;
+  return (size_t)s.strips * (size_t)s.chunks * (size_t)s.tile_bytes;
+}
+
+extern "C" int i8q_matmul_nbits_pack(int64_t N, int64_t K, int64_t block_size, const uint8_t* B, const void* scales,
+                                     int scale_type, const uint8_t* zero_points, void* packed, size_t packed_bytes,
+                                     void* stream) {
+  Shape s;
+  const int rc = check_shape(N, K, block_size, scale_type, zero_points != nullptr, "matmul_nbits_pack", s);
+  if (rc != I8Q_OK) return rc;
+  if (!B || !scales || !packed) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: B, scales or packed is NULL");
+  if (reinterpret_cast<uintptr_t>(scales) % s.scale_size)
+    return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: scales are not aligned to their type");
+  if (reinterpret_cast<uintptr_t>(packed) % 16)
+    return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: packed must be 16-byte aligned");
+  if (packed_bytes < (size_t)s.strips * (size_t)s.chunks * (size_t)s.tile_bytes)
+    return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: packed is smaller than matmul_nbits_packed_size");
+  I8Q_PROF("matmul_nbits_pack", as_stream(stream));
+  const int64_t blocks = std::min<int64_t>(s.strips * s.chunks, 64 * (int64_t)sm_count());
+  pack_kernel<<<(unsigned)blocks, 256, 0, as_stream(stream)>>>(s, B, scales, zero_points, static_cast<uint8_t*>(packed));
+  I8Q_LAUNCH_CHECK("matmul_nbits_pack");
+  return I8Q_OK;
+}
+
+extern "C" int i8q_matmul_nbits(const void* A, int type, int64_t M, int64_t lda, const void* packed, size_t packed_bytes,
+                                int64_t N, int64_t K, int64_t block_size, int scale_type, int has_zero, const float* bias,
+                                void* Y, int64_t ldy, void* stream) {
+  Args a{};
+  const int rc = check_shape(N, K, block_size, scale_type, has_zero != 0, "matmul_nbits", a.s);
+  if (rc != I8Q_OK) return rc;
+  if (type != I8Q_F32 && type != I8Q_BF16) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: type must be I8Q_F32 or I8Q_BF16");
+  if (M < 0 || M > kMost) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: M must be 0 .. 2^31 - 2^16");
+  if (M == 0) return I8Q_OK;
+  if (!A || !packed || !Y) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: A, packed or Y is NULL");
+  if (M > 1 && (lda < K || ldy < N)) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: rows overlap (lda below K or ldy below N)");
+  const uintptr_t es = type == I8Q_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(A) % es || reinterpret_cast<uintptr_t>(Y) % es || reinterpret_cast<uintptr_t>(bias) % 4)
+    return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: A, Y or bias is not aligned to its type");
+  if (reinterpret_cast<uintptr_t>(packed) % 16) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: packed must be 16-byte aligned");
+  if (packed_bytes < (size_t)a.s.strips * (size_t)a.s.chunks * (size_t)a.s.tile_bytes)
+    return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: packed is smaller than matmul_nbits_packed_size");
+  a.packed = static_cast<const uint8_t*>(packed);
+  a.A = A, a.lda = lda, a.bias = bias, a.Y = Y, a.ldy = ldy, a.M = (int)M;
+  a.a_aligned = reinterpret_cast<uintptr_t>(A) % (4 * es) == 0 && (M == 1 || lda % 4 == 0);
+  cudaStream_t s = as_stream(stream);
+  I8Q_PROF("matmul_nbits", s);
+  return run_product(a, type, s);
+}
