@@ -693,6 +693,43 @@ int i8q_kv_evict(const i8q_kv_cache* cache, const i8q_page_table* table, const i
                  int32_t* new_lengths, void* stream);
 
 /* ========================================================================
+ * Sampling: the next token of each row of logits (not on the pages).
+ *   w_i = exp((x_i - max x) / temperature)
+ * and, in the order of falling logits (equal ones by index), the tokens are
+ *   top_k   the first top_k,
+ *   top_p   of those, the shortest run from the first on whose weights reach
+ *           top_p times the sum over the first top_k; one at least,
+ *   min_p   of those, the ones with w_i >= min_p.
+ * Of the tokens kept, the first one by index is taken at which the running sum
+ * of weights exceeds random times their whole sum; its logprob is the
+ * logarithm of its share of that sum.  Weights are whole multiples of 2^-42,
+ * off by less than that, and their sums exact: the choice depends neither on
+ * the run nor on the order of sums.
+ * NaN counts as -infinity; tokens of -infinity are never taken; where the
+ * largest is +infinity, all of +infinity weigh 1 and the others 0.  A row of
+ * nothing else than -infinity gives token -1 and logprob -infinity.
+ * temperature 0 takes the largest logit, the first of equal ones, with logprob
+ * 0.  A row with a temperature below 0, a random number outside [0, 1), a
+ * top_p below 0, a min_p outside [0, 1] or a NaN among them gives token -1 and
+ * logprob NaN, and i8q_sync_status reports I8Q_ERR_INVALID_ARG.
+ * ====================================================================== */
+#define I8Q_SAMPLE_MAX_VOCABULARY (1 << 20)
+
+typedef struct i8q_sampling { /* device [rows]; NULL: 1, off, off, off */
+  const float* temperature;
+  const int32_t* top_k;       /* <= 0 or above the vocabulary: off */
+  const float* top_p;         /* >= 1: off */
+  const float* min_p;         /* 0: off */
+} i8q_sampling;
+
+/* logits: device [rows][vocabulary] of `type` (I8Q_F32 | I8Q_BF16), rows
+ * row_stride elements apart; random: device fp32 [rows]; sampling may be NULL;
+ * tokens: device int32 [rows]; logprobs: device fp32 [rows], or NULL.
+ * Errors: INVALID_ARG, CUDA. */
+int i8q_sample(const void* logits, int type, int64_t rows, int64_t vocabulary, int64_t row_stride, const float* random,
+               const i8q_sampling* sampling, int32_t* tokens, float* logprobs, void* stream);
+
+/* ========================================================================
  * Measurement (not on the pages)
  * ====================================================================== */
 
@@ -718,6 +755,7 @@ int i8q_measure_int8_mma_peak(int64_t iters, void* stream, double* tops);
 /* Synchronize `stream` and report any error recorded by a device-side
  * bounded wait since the last call (I8Q_ERR_DEVICE_TIMEOUT), an index
  * outside its range that a key/value cache call met in device data
+ * or a sampling parameter outside its range
  * (I8Q_ERR_INVALID_ARG), or a pending CUDA error (I8Q_ERR_CUDA).  Clears the
  * recorded state. */
 int i8q_sync_status(void* stream);

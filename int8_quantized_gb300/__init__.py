@@ -17,7 +17,7 @@ from ._lib import (ACT_GELU, ACT_IDENTITY, ACT_RELU, BF16, F32, LSTM_BIDIRECTION
 
 __all__ = ["QGemmDyn", "quantize_linear", "dequantize_linear", "qlinearconv", "qlinearconv_workspace_size",
            "dq_lstm_forward", "dq_lstm_forward_ex", "dq_lstm_state_codes", "dq_lstm_workspace_size", "sync_status",
-           "MatMulNBits", "KVCache", "kv_append", "kv_gather", "kv_evict", "paged_attention", "paged_attention_workspace_size",
+           "MatMulNBits", "sample", "KVCache", "kv_append", "kv_gather", "kv_evict", "paged_attention", "paged_attention_workspace_size",
            "version", "I8QError", "last_error",
            "F32", "BF16", "S8", "U8", "S32", "ACT_IDENTITY", "ACT_RELU", "ACT_GELU", "NO_AXIS",
            "LSTM_FORWARD", "LSTM_REVERSE", "LSTM_BIDIRECTIONAL"]
@@ -669,6 +669,42 @@ def kv_evict(cache, page_table, lengths, new_table, kept, new_lengths=None, sink
                             None if new_lengths is None else _i32(new_lengths, "new_lengths", B), _stream(stream)),
           "kv_evict")
     return kept
+
+
+def _per_row(t, name, rows, dtype, device):
+    """Pointer of a contiguous [rows] tensor beside the logits, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if t.numel() != rows:
+        raise ValueError(f"{name} must have {rows} entries")
+    return t.data_ptr()
+
+
+def sample(logits, random, tokens, logprobs=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """The next token of each row of logits [rows, vocabulary] (fp32 or bf16,
+    rows of any stride) by its number of random (fp32 [rows], in [0, 1)):
+    tokens int32 [rows], logprobs fp32 [rows] or None.  temperature, top_p,
+    min_p: fp32 [rows], top_k int32 [rows], each None: off.  See i8q_sample.
+    Returns tokens."""
+    if not isinstance(logits, _Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocabulary]")
+    (rows, vocabulary), (stride, one), device = logits.shape, logits.stride(), logits.device
+    if one != 1 and vocabulary > 1:
+        raise ValueError("logits must have contiguous rows")
+    _on_current(logits, "logits")
+    settings = _lib.SamplingStruct(_per_row(temperature, "temperature", rows, _F32, device),
+                                   _per_row(top_k, "top_k", rows, _I32, device),
+                                   _per_row(top_p, "top_p", rows, _F32, device),
+                                   _per_row(min_p, "min_p", rows, _F32, device))
+    check(_L().i8q_sample(logits.data_ptr(), _float_type(logits), rows, vocabulary, stride,
+                          _per_row(random, "random", rows, _F32, device), ctypes.byref(settings),
+                          _per_row(tokens, "tokens", rows, _I32, device),
+                          _per_row(logprobs, "logprobs", rows, _F32, device), _stream(stream)), "sample")
+    return tokens
 
 
 def dq_lstm_workspace_size(T, batch, input_size, hidden, direction):

@@ -48,6 +48,11 @@ class HeadNormStruct(ctypes.Structure):
     _fields_ = [("q_weight", _p), ("k_weight", _p), ("type", _i), ("eps", _f)]
 
 
+class SamplingStruct(ctypes.Structure):
+    """i8q_sampling"""
+    _fields_ = [("temperature", _p), ("top_k", _p), ("top_p", _p), ("min_p", _p)]
+
+
 _cache, _table, _rotary, _norm = (ctypes.POINTER(c) for c in (KVCacheStruct, PageTableStruct, RotaryStruct,
                                                               HeadNormStruct))
 
@@ -103,6 +108,7 @@ SIGNATURES = {
                                  _sz, _p]),
     "i8q_paged_attention_workspace_size": (_sz, [_cache, _table, _i64, _i]),
     "i8q_kv_evict": (_i, [_cache, _table, _p, _table, _p, _i64, _i64, _i64, _p, _p]),
+    "i8q_sample": (_i, [_p, _i, _i64, _i64, _i64, _p, ctypes.POINTER(SamplingStruct), _p, _p, _p]),
     "i8q_sync_status": (_i, [_p]),
     "i8q_debug_wait_timeout": (_i, [_i, _i64, _p]),
     "i8q_profile_enable": (_i, [_i]),

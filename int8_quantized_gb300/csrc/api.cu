@@ -201,6 +201,10 @@ extern "C" int i8q_sync_status(void* stream) {
     if (h == ST_KV_INDEX)
       return fail(I8Q_ERR_INVALID_ARG,
                   "a key/value cache call met a page, sequence, token index, length or position outside its range");
+    if (h == ST_SAMPLE)
+      return fail(I8Q_ERR_INVALID_ARG, "sample met a temperature, top_p, min_p or random number outside its range");
+    if (h == (ST_KV_INDEX | ST_SAMPLE))
+      return fail(I8Q_ERR_INVALID_ARG, "a key/value cache call met an index, and sample a parameter, outside its range");
     return fail(I8Q_ERR_DEVICE_TIMEOUT, "a device-side bounded wait gave up (status " + std::to_string(h) + ")");
   }
   return I8Q_OK;

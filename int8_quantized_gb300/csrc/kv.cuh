@@ -11,6 +11,8 @@ namespace i8q {
 // The device status word's bit for an index out of range in a key/value
 // cache call's device data (the bits below belong to the bounded waits).
 constexpr uint32_t ST_KV_INDEX = 1u << 31;
+// ... and for a row's sampling parameters out of range.
+constexpr uint32_t ST_SAMPLE = 1u << 30;
 
 namespace kv {
 

@@ -1,0 +1,508 @@
+// sample.cu -- the next token of each row of logits: temperature, top-k,
+// top-p and min-p, then a choice by a given random number.
+#include <cooperative_groups.h>
+
+#include <cmath>
+#include <string>
+
+#include "kv.cuh"
+
+namespace i8q {
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---- weights --------------------------------------------------------------
+// A token's weight exp((x - max) / T) as a whole number of steps of 2^-42: the
+// sums that decide which tokens are kept and which one is taken are sums of
+// integers, exact in any order (2^20 of them fit 62 bits).  fp32 sums would
+// miss a token's border by 1e-7 of the whole, a width of several tokens of a
+// large vocabulary; fp64 has 1/64 of the rate.
+//
+// With y = (max - x) log2(e) / T = n + f, |f| <= 1/2, and j = rint(-512 f),
+// r = -f - j / 512:   2^-y = 2^-n 2^(j/512) 2^r.   2^(j/512) comes from a table
+// in two fp32 parts, 2^r - 1 = r ln2 + (r ln2)^2 / 2 + (r ln2)^3 / 6 (the next
+// term is below 2^-46); what must be known to more than 24 bits is carried as
+// the sum of two fp32 numbers.  Off by less than 2^-42 for every argument.
+constexpr int kWeightBits = 42;
+constexpr uint64_t kWhole = 1ull << kWeightBits;
+
+constexpr int kSteps = 512;
+constexpr double kLn2 = 0.693147180559945309417;
+
+constexpr double exp_series(double x) {
+  double sum = 1.0, term = 1.0;
+  for (int i = 1; i < 24; ++i) term *= x / i, sum += term;
+  return sum;
+}
+
+struct PowerTable {  // 2^(j / 512), j = -256 .. 256, in two parts
+  float hi[kSteps + 1], lo[kSteps + 1];
+  constexpr PowerTable() : hi(), lo() {
+    for (int j = 0; j <= kSteps; ++j) {
+      const double v = exp_series(kLn2 * (j - kSteps / 2) / kSteps);
+      hi[j] = (float)v, lo[j] = (float)(v - (double)hi[j]);
+    }
+  }
+};
+__device__ const PowerTable g_powers = PowerTable();
+
+struct Scale {
+  float max, half;  // the row's largest logit and its half (halves: a difference does not overflow)
+  float ch, cl;     // 2 log2(e) / T in two parts
+};
+
+__device__ __forceinline__ Scale make_scale(float max, float temperature) {
+  const double c = 2.0 / kLn2 / (double)temperature;
+  const float ch = (float)c;
+  return Scale{max, 0.5f * max, ch, isinf(ch) ? 0.0f : (float)(c - (double)ch)};
+}
+
+// powers: the table in shared memory.  0 for -infinity and NaN.
+__device__ __forceinline__ uint64_t weight(float x, const Scale& s, const float2* powers) {
+  if (x == s.max) return kWhole;
+  const float xh = -0.5f * x;
+  const float h = __fadd_rn(s.half, xh), hv = __fsub_rn(h, s.half);
+  const float hl = __fadd_rn(__fsub_rn(s.half, __fsub_rn(h, hv)), __fsub_rn(xh, hv));
+  const float p = __fmul_rn(h, s.ch);
+  if (!(p >= 0.0f && p < 43.5f)) return 0;
+  const float pl = __fmaf_rn(hl, s.ch, __fmaf_rn(h, s.cl, __fmaf_rn(h, s.ch, -p)));
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer
+  const float nm = __fadd_rn(p, kMagic);
+  const int n = __float_as_int(nm) - 0x4B400000;
+  const float v = __fsub_rn(__fsub_rn(nm, kMagic), p);
+  const float vh = __fsub_rn(v, pl), vl = __fsub_rn(__fsub_rn(v, vh), pl);
+  const float jm = __fmaf_rn(vh, (float)kSteps, kMagic);
+  const int j = __float_as_int(jm) - 0x4B400000;
+  const float r = __fmaf_rn(__fsub_rn(jm, kMagic), -1.0f / kSteps, vh);
+  constexpr float kLh = (float)kLn2, kLl = (float)(kLn2 - (double)kLh);
+  constexpr float kC2 = (float)(kLn2 * kLn2 / 2), kC3 = (float)(kLn2 * kLn2 * kLn2 / 6);
+  const float p1 = __fmul_rn(r, kLh);
+  const float e1 = __fmaf_rn(r, kLl, __fmaf_rn(r, kLh, -p1));
+  const float t2 = __fmaf_rn(vl, kLh, __fmaf_rn(__fmul_rn(r, r), __fmaf_rn(r, kC3, kC2), e1));
+  const float2 pw = powers[j + kSteps / 2];
+  const float m = __fmul_rn(pw.x, p1);
+  const float low = __fadd_rn(__fmaf_rn(pw.x, t2, __fmaf_rn(pw.x, p1, -m)), __fmaf_rn(pw.y, p1, pw.y));
+  const float sum = __fadd_rn(pw.x, m);
+  const float rest = __fadd_rn(__fsub_rn(m, __fsub_rn(sum, pw.x)), low);
+  constexpr float kHalfBits = 2097152.0f;  // 2^21
+  const float am = __fmaf_rn(sum, kHalfBits, kMagic);
+  const float d = __fmaf_rn(rest, kHalfBits, __fmaf_rn(sum, kHalfBits, -__fsub_rn(am, kMagic)));
+  const int a = __float_as_int(am) - 0x4B400000, b = __float_as_int(__fmaf_rn(d, kHalfBits, kMagic)) - 0x4B400000;
+  const uint64_t w = ((uint64_t)(uint32_t)a << 21) + (int64_t)b;
+  return (w + ((1ull << n) >> 1)) >> n;
+}
+
+// floor(f * sum) and whether something was cut off, 0 <= f < 1, sum < 2^63.
+__device__ __forceinline__ uint64_t share(float f, uint64_t sum, bool& cut) {
+  const uint32_t u = __float_as_uint(f), e = u >> 23;
+  const uint64_t mant = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int shift = 150 - (int)(e ? e : 1);  // f = mant 2^-shift, shift >= 24
+  const uint64_t hi = __umul64hi(mant, sum), lo = mant * sum;
+  uint64_t q, rest;
+  if (shift < 64) q = hi << (64 - shift) | lo >> shift, rest = lo << (64 - shift);
+  else if (shift == 64) q = hi, rest = lo;
+  else if (shift < 128) q = hi >> (shift - 64), rest = (hi << (128 - shift)) | lo;
+  else q = 0, rest = hi | lo;
+  cut = rest != 0;
+  return q;
+}
+
+// ---- keys -----------------------------------------------------------------
+// A logit as an unsigned number of the same order: NaN as -infinity, -0 as 0.
+// bf16 logits have 16 bits.
+template <class T>
+struct Key;
+template <>
+struct Key<float> {
+  static constexpr int kBits = 32, kVec = 4;
+  static __device__ __forceinline__ uint32_t of(float x) {
+    if (x != x) x = -INFINITY;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+  }
+};
+template <>
+struct Key<__nv_bfloat16> {
+  static constexpr int kBits = 16, kVec = 8;
+  static __device__ __forceinline__ uint32_t of(float x) { return Key<float>::of(x) >> 16; }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return Key<float>::value(k << 16 | ((k >> 15) ? 0u : 0xffffu));
+  }
+};
+
+struct Args {
+  const void* logits;
+  int64_t stride;
+  int V;
+  const float* random;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logprobs;
+  uint32_t* status;
+};
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kDigit = 11, kMostCtas = 8;
+
+struct Shared {
+  float2 powers[kSteps + 1];
+  uint32_t lo[kBins], hi[kBins];  // of this CTA
+  uint64_t total[kBins];          // of the row
+  uint64_t warp_sum[kWarps];
+  uint64_t best[kMostCtas];              // of each CTA of the cluster
+  uint64_t mass[kMostCtas][kWarps];      // kept weight of each warp's tokens, of all CTAs
+  uint32_t ties[kMostCtas][kWarps];      // and its tokens of the border's key
+  uint64_t before;
+  uint32_t bin;
+};
+
+__device__ __forceinline__ void add(Shared& sh, uint32_t bin, uint64_t w) {
+  const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
+  const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
+  if (high) atomicAdd(&sh.hi[bin], high);
+}
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += u;
+  }
+  return v;
+}
+
+// One row by a cluster of CTAs, a contiguous share of its tokens each, and of
+// that a contiguous share each warp.  The row is read again (from L2) by each
+// pass: the largest; counts by digits of the keys from the top (top-k); the
+// weights' sums by digits (top-p); the kept weight of each warp; the warp in
+// which the random number falls alone.
+template <class T>
+__global__ void __launch_bounds__(kThreads, 2)
+sample_kernel(const __grid_constant__ Args a) {
+  using K = Key<T>;
+  constexpr int kVec = K::kVec;
+  extern __shared__ __align__(16) uint8_t memory[];
+  Shared& sh = *reinterpret_cast<Shared*>(memory);
+  const auto cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int row = blockIdx.x / S, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const auto meet = [&] { S > 1 ? cluster.sync() : __syncthreads(); };
+  kv::next_kernel_may_start();
+  for (int i = threadIdx.x; i <= kSteps; i += kThreads) sh.powers[i] = make_float2(g_powers.hi[i], g_powers.lo[i]);
+  kv::wait_previous_kernel();
+
+  const T* const x = static_cast<const T*>(a.logits) + row * a.stride;
+  // vectors of 16 bytes: the first begins `skew` tokens before the row
+  const int skew = (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kVec);
+  const int vectors = (int)(((int64_t)a.V + skew + kVec - 1) / kVec);
+  const int part = rank * kWarps + warp, parts = S * kWarps;
+  const int v0 = (int)((int64_t)vectors * part / parts), v1 = (int)((int64_t)vectors * (part + 1) / parts);
+  auto load = [&](int v, float (&y)[kVec]) {
+    const int first = v * kVec - skew;
+    if (v < v1 && first >= 0 && first + kVec <= a.V) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + first);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        y[j] = kVec == 4 ? __uint_as_float(w[j & 3]) : __uint_as_float(j & 1 ? w[j / 2 & 3] & 0xffff0000u : w[j / 2 & 3] << 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        y[j] = v < v1 && first + j >= 0 && first + j < a.V ? (float)x[first + j] : -INFINITY;
+    }
+  };
+
+  // ---- the largest logit, and its first place ----
+  const float temperature = a.temperature ? a.temperature[row] : 1.0f, u = a.random[row];
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
+  int top_k = a.top_k ? a.top_k[row] : 0;
+  if (top_k <= 0 || top_k > a.V) top_k = a.V;
+  uint64_t best = 0;
+  for (int v = v0 + lane; v < v1; v += 32) {
+    float y[kVec];
+    load(v, y);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int i = v * kVec - skew + j;
+      if (i < 0 || i >= a.V) continue;
+      best = max(best, (uint64_t)K::of(y[j]) << 32 | (uint32_t)~i);
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
+  if (lane == 0) sh.warp_sum[warp] = best;
+  __syncthreads();
+  if (threadIdx.x < S) {
+    for (int w = 0; w < kWarps; ++w) best = max(best, sh.warp_sum[w]);
+    cluster.map_shared_rank(sh.best, threadIdx.x)[rank] = best;
+  }
+  meet();
+  best = 0;
+  for (int r = 0; r < S; ++r) best = max(best, sh.best[r]);
+  const float largest = K::value((uint32_t)(best >> 32));
+  const bool valid = temperature >= 0.0f && u >= 0.0f && u < 1.0f && top_p >= 0.0f && min_p >= 0.0f && min_p <= 1.0f;
+  if (!valid || temperature == 0.0f || largest == -INFINITY) {  // (the same for the whole cluster)
+    if (rank == 0 && threadIdx.x == 0) {
+      if (!valid) atomicOr(a.status, ST_SAMPLE);
+      const bool none = !valid || largest == -INFINITY;
+      a.tokens[row] = none ? -1 : (int)~(uint32_t)best;
+      if (a.logprobs) a.logprobs[row] = !valid ? NAN : none ? -INFINITY : 0.0f;
+    }
+    return;
+  }
+  const Scale scale = make_scale(largest, temperature);
+
+  // ---- the border: kept are the keys above it and the first `ties` of its own ----
+  uint32_t border = 0, ties = UINT32_MAX;
+  bool cut = false;
+  // Counts (or weights) of the tokens within the border so far by their
+  // digit of key bits [shift, shift + kDigit), prefix: the bits above.
+  auto histogram = [&](bool by_weight, int shift, uint32_t prefix) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+    __syncthreads();
+    const int above = shift + kDigit;
+    for (int v = v0 + lane; v < v1; v += 32) {
+      float y[kVec];
+      load(v, y);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t k = K::of(y[j]);
+        if (above < 32 && k >> above != prefix) continue;
+        if (!by_weight) {
+          const int i = v * kVec - skew + j;
+          if (i >= 0 && i < a.V) atomicAdd(&sh.lo[k >> shift & (kBins - 1)], 1u);
+        } else if (!cut || k > border) {
+          const uint64_t w = weight(y[j], scale, sh.powers);
+          if (w) add(sh, k >> shift & (kBins - 1), w);
+        }
+      }
+    }
+    if (by_weight && cut && rank == 0 && threadIdx.x == 0 && (above >= 32 || border >> above == prefix))
+      add(sh, border >> shift & (kBins - 1), ties * weight(K::value(border), scale, sh.powers));
+    meet();
+    for (int i = threadIdx.x; i < kBins / S; i += kThreads) {
+      const int b = rank * (kBins / S) + i;
+      uint64_t sum = 0;
+      for (int r = 0; r < S; ++r) {
+        const Shared* other = cluster.map_shared_rank(&sh, r);
+        sum += (uint64_t)other->hi[b] << 32 | other->lo[b];
+      }
+      for (int r = 0; r < S; ++r) cluster.map_shared_rank(&sh, r)->total[b] = sum;
+    }
+    meet();
+  };
+  // The digit in whose bin the sum from the top reaches target, and the sum before it.
+  auto find = [&](uint64_t target, uint32_t& bin, uint64_t& before) {
+    constexpr int kEach = kBins / kThreads;
+    uint64_t t[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) t[i] = sh.total[kBins - 1 - (threadIdx.x * kEach + i)], sum += t[i];
+    const uint64_t inclusive = warp_scan64(sum, lane);
+    if (lane == 31) sh.warp_sum[warp] = inclusive;
+    __syncthreads();
+    uint64_t at = inclusive - sum;
+    for (int w = 0; w < warp; ++w) at += sh.warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (at < target && target <= at + t[i]) sh.bin = kBins - 1 - (threadIdx.x * kEach + i), sh.before = at;
+      at += t[i];
+    }
+    __syncthreads();
+    bin = sh.bin, before = sh.before;
+    __syncthreads();
+  };
+  constexpr int kFirst = K::kBits - kDigit;
+  auto descend = [&](bool by_weight, uint64_t target, uint32_t& key, uint64_t& missing) {
+    // (the first histogram is there)
+    uint32_t bin;
+    uint64_t before;
+    find(target, bin, before);
+    target -= before;
+    key = bin;
+    for (int shift = kFirst; shift > 0;) {
+      const int bits = min(kDigit, shift);
+      shift -= bits;
+      // a last digit of fewer bits: the prefix's lowest bits lie in its bins too
+      const int lower = kDigit - bits;
+      histogram(by_weight, shift, key >> lower);
+      if (lower) {  // the bins that belong to the prefix
+        const uint32_t mine = key & ((1u << lower) - 1);
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+          if ((uint32_t)i >> bits != mine) sh.total[i] = 0;
+        __syncthreads();
+      }
+      find(target, bin, before);
+      target -= before;
+      key = key << bits | (bin & ((1u << bits) - 1));
+    }
+    missing = target;
+  };
+  if (top_k < a.V) {
+    uint64_t missing;
+    histogram(false, kFirst, 0);
+    descend(false, (uint64_t)top_k, border, missing);
+    ties = (uint32_t)missing, cut = true;
+  }
+  if (top_p < 1.0f) {
+    histogram(true, kFirst, 0);
+    uint64_t sum = 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sum += sh.total[i];
+    sum = warp_sum64(sum);
+    if (lane == 0) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < kWarps; ++w) sum += sh.warp_sum[w];
+    __syncthreads();
+    bool more;
+    uint64_t target = share(top_p, sum, more), missing;
+    target = max(target + more, (uint64_t)1);
+    uint32_t key;
+    descend(true, target, key, missing);
+    const uint64_t w = weight(K::value(key), scale, sh.powers);
+    border = key, ties = (uint32_t)((missing + w - 1) / w), cut = true;
+  }
+
+  // ---- the kept weight of each warp's tokens ----
+  bool more;
+  const uint64_t least = [&] {
+    if (min_p >= 1.0f) return kWhole;
+    const uint64_t q = share(min_p, kWhole, more);
+    return max(q + more, (uint64_t)1);
+  }();
+  uint64_t mass = 0;
+  uint32_t same = 0;
+  for (int v = v0 + lane; v < v1; v += 32) {
+    float y[kVec];
+    load(v, y);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const uint32_t k = K::of(y[j]);
+      if (cut && k <= border) {
+        same += k == border;
+        continue;
+      }
+      const uint64_t w = weight(y[j], scale, sh.powers);
+      if (w >= least) mass += w;
+    }
+  }
+  mass = warp_sum64(mass);
+  same = __reduce_add_sync(0xffffffffu, same);
+  if (lane < S) {
+    Shared* other = cluster.map_shared_rank(&sh, lane);
+    other->mass[rank][warp] = mass, other->ties[rank][warp] = same;
+  }
+  meet();
+  uint64_t tie_weight = cut ? weight(K::value(border), scale, sh.powers) : 0;
+  if (tie_weight < least) tie_weight = 0;
+  uint64_t sum = 0, before = 0;
+  uint32_t seen = 0, seen_before = 0;
+  for (int i = 0; i < parts; ++i) {
+    const uint32_t here = cut ? min(sh.ties[i / kWarps][i % kWarps], ties - seen) : 0;
+    if (i == part) before = sum, seen_before = seen;
+    sum += sh.mass[i / kWarps][i % kWarps] + here * tie_weight;
+    seen += here;
+    if (i == part) mass = sum;
+  }
+  const uint64_t target = share(u, sum, more);  // taken: the first token up to which the sum is above it
+  if (!(before <= target && target < mass)) return;
+
+  // ---- the token, by the warp that has it ----
+  uint64_t at = before;
+  uint32_t left = cut ? ties - seen_before : 0;
+  for (int vb = v0; vb < v1; vb += 32) {
+    const int v = vb + lane;
+    float y[kVec];
+    load(v, y);
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) mine += cut && K::of(y[j]) == border;
+    uint32_t earlier = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const uint32_t w = __shfl_up_sync(0xffffffffu, earlier, m);
+      if (lane >= m) earlier += w;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, earlier, 31);
+    earlier -= mine;
+    uint64_t w[kVec], total = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const uint32_t k = K::of(y[j]);
+      w[j] = 0;
+      if (cut && k <= border) {
+        if (k == border && earlier++ < left) w[j] = tie_weight;
+      } else {
+        w[j] = weight(y[j], scale, sh.powers);
+        if (w[j] < least) w[j] = 0;
+      }
+      total += w[j];
+    }
+    const uint64_t inclusive = warp_scan64(total, lane) + at;
+    const uint32_t past = __ballot_sync(0xffffffffu, inclusive > target);
+    if (past) {
+      if (lane == __ffs(past) - 1) {
+        uint64_t c = inclusive - total, chosen = 0;
+        int token = 0;
+#pragma unroll
+        for (int j = kVec - 1; j >= 0; --j) {  // from the last on: the first one past the target stays
+          uint64_t upto = c;
+          for (int i = 0; i <= j; ++i) upto += w[i];
+          if (upto > target) token = v * kVec - skew + j, chosen = w[j];
+        }
+        a.tokens[row] = token;
+        if (a.logprobs) {
+          // near 1 from what is missing to it
+          const float ratio = __fdiv_rn((float)chosen, (float)sum);
+          a.logprobs[row] = ratio > 0.5f ? log1pf(-__fdiv_rn((float)(sum - chosen), (float)sum)) : logf(ratio);
+        }
+      }
+      return;
+    }
+    at = __shfl_sync(0xffffffffu, inclusive, 31);
+    left -= min(left, all);
+  }
+}
+
+}  // namespace
+}  // namespace i8q
+
+using namespace i8q;
+
+extern "C" int i8q_sample(const void* logits, int type, int64_t rows, int64_t vocabulary, int64_t row_stride,
+                          const float* random, const i8q_sampling* sampling, int32_t* tokens, float* logprobs,
+                          void* stream) {
+  if (type != I8Q_F32 && type != I8Q_BF16) return fail(I8Q_ERR_INVALID_ARG, "sample: type must be I8Q_F32 or I8Q_BF16");
+  if (rows < 0 || rows > (1 << 24)) return fail(I8Q_ERR_INVALID_ARG, "sample: rows must be 0 .. 2^24");
+  if (vocabulary < 1 || vocabulary > I8Q_SAMPLE_MAX_VOCABULARY)
+    return fail(I8Q_ERR_INVALID_ARG, "sample: vocabulary must be 1 .. 2^20");
+  if (rows == 0) return I8Q_OK;
+  if (!logits || !random || !tokens) return fail(I8Q_ERR_INVALID_ARG, "sample: logits, random or tokens is NULL");
+  if (rows > 1 && row_stride < vocabulary) return fail(I8Q_ERR_INVALID_ARG, "sample: rows overlap (row_stride below vocabulary)");
+  const uintptr_t es = type == I8Q_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % es) return fail(I8Q_ERR_INVALID_ARG, "sample: logits are not aligned to their type");
+  uint32_t* status = device_status_word();
+  if (!status) return fail(I8Q_ERR_CUDA, "sample: no status word");
+  const i8q_sampling none{};
+  const i8q_sampling& p = sampling ? *sampling : none;
+  Args a{logits, row_stride, (int)vocabulary, random, p.temperature, p.top_k, p.top_p, p.min_p, tokens, logprobs, status};
+  // CTAs of a row: what two on each SM leave room for, of 4096 tokens at least
+  int S = 1;
+  while (S < kMostCtas && rows * S * 2 <= 2 * sm_count() && vocabulary >= 4096 * S * 2) S *= 2;
+  cudaStream_t s = as_stream(stream);
+  I8Q_PROF("sample", s);
+  auto run = [&](auto kernel) {
+    return kv::launch(kernel, (unsigned)(rows * S), kThreads, (int)sizeof(Shared), S, s, "sample", a);
+  };
+  return type == I8Q_F32 ? run(sample_kernel<float>) : run(sample_kernel<__nv_bfloat16>);
+}
