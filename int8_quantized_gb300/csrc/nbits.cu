@@ -108,6 +108,43 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// The same with a sum of 0 before it.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
+}
+
+// N scales or zero points of a tile's row, read as few words.
+template <class T, int N>
+struct Row {
+  static constexpr int kBytes = N * (int)sizeof(T), kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ Row() {  // zero points of 8
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0x08080808u;
+  }
+  __device__ __forceinline__ Row(const uint8_t* tile, int row) {
+    const uint8_t* p = tile + row * kBytes;
+    if constexpr (kBytes == 1) w[0] = *p;
+    else if constexpr (kBytes == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(w + i) = *reinterpret_cast<const uint4*>(p + 4 * i);
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ uint32_t pair(int i) const {  // 128 + zero point twice, as bf16
+    return __byte_perm(w[i / 4], 0x43434343u, 0x4040u + (i & 3) * 0x0101u);
+  }
+};
+
 // Two codes at nibbles 0 and 4 of w as bf16 numbers less their zero point:
 // 0x43 over a byte c < 128 is 128 + c, and 128 + z is subtracted exactly.
 __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t zero) {
@@ -180,12 +217,12 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2
 // and streams the tiles of one strip of 16 outputs after the other through a
 // ring of its own in shared memory, each lane copying what it will read.  The
 // warps of a strip add their sums up in shared memory, those of a cluster's
-// CTAs through it.  NT: tiles of 8 rows.  G: the block, at most 128.  The
-// products of a block are summed by the tensor pipe from 0 and enter the row's
-// sum by a rounded fma with the block's scale (the pipe cuts sums instead of
-// rounding them; for fp32 activations only one step's 16 products are left to
-// it).
-template <class T, int NT, int C, int G>
+// CTAs through it.  NT: tiles of 8 rows.  G: the block, at most 128.  S: the
+// scales' type.  The products of a block are summed by the tensor pipe from 0
+// and enter the row's sum by a rounded fma with the block's scale (the pipe
+// cuts sums instead of rounding them; for fp32 activations only one step's 16
+// products are left to it).
+template <class T, int NT, int C, int G, class ST>
 __global__ void __launch_bounds__(512, 1)
 nbits_kernel(const __grid_constant__ Args a) {
   constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128, kDepth = ring_depth(NT), kAhead = kDepth - 1;
@@ -194,34 +231,40 @@ nbits_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane & 3;
   const int wk = warp % a.wk, wf = warp / a.wk;
   const int cluster = blockIdx.x / S, rows0 = cluster / a.clusters * (8 * NT), c0 = cluster % a.clusters;
-  const int chunks = (int)a.s.chunks, strips = (int)a.s.strips;
+  const int rows = min(8 * NT, a.M - rows0);
+  const int chunks = (int)a.s.chunks, strips = (int)a.s.strips, tile_bytes = a.s.tile_bytes;
   const int parts = a.wk * S, part = rank * a.wk + wk;
   const int c_begin = (int)((int64_t)part * chunks / parts), cw = (int)((int64_t)(part + 1) * chunks / parts) - c_begin;
   const int groups = (strips + a.wf - 1) / a.wf, ng = (groups - c0 + a.clusters - 1) / a.clusters;
-  uint8_t* const ring = smem + (size_t)warp * kDepth * a.s.tile_bytes;
-  float* const partial = reinterpret_cast<float*>(smem + (size_t)a.wk * a.wf * kDepth * a.s.tile_bytes);
+  const int strip0 = c0 * a.wf + wf, strip_step = a.clusters * a.wf;
+  const int live = cw && strip0 < strips ? (strips - strip0 + strip_step - 1) / strip_step : 0;  // groups with a strip for this warp
+  uint8_t* const ring = smem + (size_t)warp * kDepth * tile_bytes;
+  float* const partial = reinterpret_cast<float*>(smem + (size_t)a.wk * a.wf * kDepth * tile_bytes);
   float* const held = partial + 2 * a.wk * a.wf * kOut;
 
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
 
-  // the ring's next tile: group ig of this warp, chunk ic of it
-  int ig = 0, ic = 0, slot_in = 0;
-  const int meta = (a.s.tile_bytes - kCodeBytes) / 16;
+  // the next tile to send for
+  const uint8_t* from = a.packed + ((int64_t)strip0 * chunks + c_begin) * tile_bytes + lane * 16;
+  const int64_t jump = ((int64_t)strip_step * chunks - cw) * tile_bytes;
+  int64_t left = (int64_t)live * cw;
+  int in_group = 0;
+  const uint32_t ring_begin = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16, ring_end = ring_begin + kDepth * tile_bytes;
+  uint32_t to = ring_begin;
+  const int meta = (tile_bytes - kCodeBytes) / 16;  // at most 40
   auto send = [&] {
-    if (cw && ig < ng) {
-      const int strip = (c0 + ig * a.clusters) * a.wf + wf;
-      if (strip < strips) {
-        const uint8_t* from = a.packed + ((int64_t)strip * chunks + c_begin + ic) * a.s.tile_bytes;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + slot_in * a.s.tile_bytes;
-        copy16(to + lane * 16, from + lane * 16);
-        copy16(to + 512 + lane * 16, from + 512 + lane * 16);
-        for (int i = lane; i < meta; i += 32) copy16(to + kCodeBytes + i * 16, from + kCodeBytes + i * 16);
-      }
-      if (++ic == cw) ic = 0, ++ig;
+    if (left > 0) {
+      copy16(to, from);
+      copy16(to + 512, from + 512);
+      if (lane < meta) copy16(to + kCodeBytes, from + kCodeBytes);
+      if (meta > 32 && lane + 32 < meta) copy16(to + kCodeBytes + 512, from + kCodeBytes + 512);
+      from += tile_bytes, --left;
+      if (++in_group == cw) in_group = 0, from += jump;
+      to += tile_bytes;
+      if (to == ring_end) to = ring_begin;
     }
     commit();
-    slot_in = slot_in + 1 == kDepth ? 0 : slot_in + 1;
   };
   for (int i = 0; i < kAhead; ++i) send();
 
@@ -232,116 +275,106 @@ nbits_kernel(const __grid_constant__ Args a) {
     for (int st = 0; st < 8; ++st)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int m = rows0 + nt * 8 + g;
-        x[slot][st][nt].load(A + (int64_t)m * a.lda, (c_begin + c) * kTileK + st * 16 + 4 * t, (int)a.s.K,
-                             c < cw && m < a.M, a.a_aligned);
+        const int m = nt * 8 + g;
+        x[slot][st][nt].load(A + (int64_t)(rows0 + m) * a.lda, (c_begin + c) * kTileK + st * 16 + 4 * t, (int)a.s.K,
+                             c < cw && m < rows, a.a_aligned);
       }
   };
 #pragma unroll
   for (int c = 0; c < C; ++c) load_x(c, c);
 
-  int slot = 0;
+  const uint8_t* at = ring;
   auto tile = [&](const Fragment<T> (&xc)[8][NT], float (&y)[NT][4]) {
     wait_copies<kAhead - 1>();
     __syncwarp();  // the scales and zero points were copied by other lanes, and all have read the tile before
     send();
-    const uint8_t* const at = ring + slot * a.s.tile_bytes;
-    slot = slot + 1 == kDepth ? 0 : slot + 1;
     const uint4 q0 = *reinterpret_cast<const uint4*>(at + lane * 16), q1 = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
-    float s0[kPer], s1[kPer];
-    if (a.s.scale_size == 4) {
-      const float* sc = reinterpret_cast<const float*>(at + kCodeBytes);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) s0[i] = sc[g * kPer + i], s1[i] = sc[(g + 8) * kPer + i];
-    } else {
-      const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(at + kCodeBytes);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) s0[i] = __bfloat162float(sc[g * kPer + i]), s1[i] = __bfloat162float(sc[(g + 8) * kPer + i]);
+    const Row<ST, kPer> s0(at + kCodeBytes, g), s1(at + kCodeBytes, g + 8);
+    Row<uint8_t, kPer> z0, z1;
+    if (a.s.has_zero) {
+      z0 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g);
+      z1 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g + 8);
     }
-    uint32_t z0[kPer], z1[kPer];
-    const uint8_t* zs = at + kCodeBytes + kTileN * kPer * a.s.scale_size;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      z0[i] = z1[i] = 0x43084308u;
-      if (a.s.has_zero) z0[i] = 0x43004300u | zs[g * kPer + i] * 0x10001u, z1[i] = 0x43004300u | zs[(g + 8) * kPer + i] * 0x10001u;
-    }
+    at += tile_bytes;
+    if (at == ring + kDepth * tile_bytes) at = ring;
     const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
-    float acc[NT][4] = {};
+    float acc[NT][4];
 #pragma unroll
     for (int st = 0; st < 8; ++st) {
       const int i = st * 16 / G;
       const uint32_t v0 = w0[st / 2] >> (8 * (st & 1)), v1 = w1[st / 2] >> (8 * (st & 1));
-      const uint32_t f[4] = {pair(v0, z0[i]), pair(v1, z1[i]), pair(v0 >> 4, z0[i]), pair(v1 >> 4, z1[i])};
+      const uint32_t f[4] = {pair(v0, z0.pair(i)), pair(v1, z1.pair(i)), pair(v0 >> 4, z0.pair(i)), pair(v1 >> 4, z1.pair(i))};
+      const bool first = kParts > 1 || st * 16 % G == 0, last = kParts > 1 || (st + 1) * 16 % G == 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int p = kParts - 1; p >= 0; --p) mma(acc[nt], f, xc[st][nt].b[p]);
+        for (int p = kParts - 1; p >= 0; --p) {
+          if (first && p == kParts - 1) mma_first(acc[nt], f, xc[st][nt].b[p]);
+          else mma(acc[nt], f, xc[st][nt].b[p]);
+        }
       }
-      if (kParts > 1 || (st + 1) * 16 % G == 0) {
+      if (last) {
+        const float u0 = s0.value(i), u1 = s1.value(i);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          y[nt][0] = __fmaf_rn(acc[nt][0], s0[i], y[nt][0]), y[nt][1] = __fmaf_rn(acc[nt][1], s0[i], y[nt][1]);
-          y[nt][2] = __fmaf_rn(acc[nt][2], s1[i], y[nt][2]), y[nt][3] = __fmaf_rn(acc[nt][3], s1[i], y[nt][3]);
-          acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+          y[nt][0] = __fmaf_rn(acc[nt][0], u0, y[nt][0]), y[nt][1] = __fmaf_rn(acc[nt][1], u0, y[nt][1]);
+          y[nt][2] = __fmaf_rn(acc[nt][2], u1, y[nt][2]), y[nt][3] = __fmaf_rn(acc[nt][3], u1, y[nt][3]);
         }
       }
     }
   };
 
   T* const Y = static_cast<T*>(a.Y);
-  auto put = [&](int group, int e, float v) {  // e: strip of the group, row, output
-    const int m = rows0 + e % kOut / 16;
-    const int64_t n = ((int64_t)(c0 + group * a.clusters) * a.wf + e / kOut) * kTileN + e % 16;
-    if (m >= a.M || n >= a.s.N) return;
+  auto put = [&](int group, int strip, int e, float v) {  // e: row and output
+    const int m = rows0 + e / 16;
+    const int64_t n = ((int64_t)(c0 + group * a.clusters) * a.wf + strip) * kTileN + e % 16;
+    if (n >= a.s.N) return;
     if (a.bias) v = __fadd_rn(v, a.bias[n]);
     store(Y + (int64_t)m * a.ldy + n, v);
   };
 
   for (int gi = 0; gi < ng; ++gi) {
-    const bool live = (c0 + gi * a.clusters) * a.wf + wf < strips;
     float y[NT][4] = {};
-    if constexpr (C > 0) {
+    if (gi < live) {
+      if constexpr (C > 0) {
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (c < cw) {
-          if (live) tile(x[c], y);
-          else send(), slot = slot + 1 == kDepth ? 0 : slot + 1;
-        }
-    } else {
-      for (int c = 0; c < cw; ++c) {
-        load_x(0, c);
-        if (live) tile(x[0], y);
-        else send(), slot = slot + 1 == kDepth ? 0 : slot + 1;
+        for (int c = 0; c < C; ++c)
+          if (c < cw) tile(x[c], y);
+      } else {
+        for (int c = 0; c < cw; ++c) load_x(0, c), tile(x[0], y);
       }
     }
-    float* const mine = partial + (gi & 1) * a.wk * a.wf * kOut;
+    // the sums of a strip's warps, two buffers in turn
+    float* const mine = partial + ((gi & 1) * a.wf + wf) * a.wk * kOut;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      *reinterpret_cast<float4*>(mine + ((wf * a.wk + wk) * NT + nt) * 128 + lane * 4) =
-          make_float4(y[nt][0], y[nt][1], y[nt][2], y[nt][3]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.wf * kOut; e += blockDim.x) {
-      const int m = e % kOut / 16, f = e % 16;
-      const float* p = mine + (e / kOut * a.wk * NT + m / 8) * 128 + ((f & 7) * 4 + (m & 7) / 2) * 4 + (m & 1) + 2 * (f / 8);
+      if (nt * 8 + 2 * t < rows)
+        *reinterpret_cast<float4*>(mine + wk * kOut + nt * 128 + lane * 4) = make_float4(y[nt][0], y[nt][1], y[nt][2], y[nt][3]);
+    asm volatile("bar.sync %0, %1;\n" ::"r"(wf), "r"(a.wk * 32) : "memory");
+    for (int e = wk * 32 + lane; e < rows * 16; e += a.wk * 32) {
+      const int m = e / 16, f = e % 16;
+      const float* p = mine + m / 8 * 128 + ((f & 7) * 4 + (m & 7) / 2) * 4 + (m & 1) + 2 * (f / 8);
       float v = 0.0f;
+#pragma unroll 4
       for (int w = 0; w < a.wk; ++w) v = __fadd_rn(v, p[w * kOut]);
-      if (S == 1) put(gi, e, v);
-      else held[(gi % kRound) * a.wf * kOut + e] = v;
+      if (S == 1) put(gi, wf, e, v);
+      else held[((gi % kRound) * a.wf + wf) * kOut + e] = v;
     }
     if (S > 1 && (gi % kRound == kRound - 1 || gi == ng - 1)) {
       cg::this_cluster().sync();
       const int first = gi / kRound * kRound, n = (gi - first + 1) * a.wf * kOut;
       for (int e = rank * blockDim.x + threadIdx.x; e < n; e += S * blockDim.x) {
+        if (e % kOut >= rows * 16) continue;
         float v = 0.0f;
         for (int r = 0; r < S; ++r) v = __fadd_rn(v, cg::this_cluster().map_shared_rank(held, r)[e]);
-        put(first + e / (a.wf * kOut), e % (a.wf * kOut), v);
+        put(first + e / (a.wf * kOut), e / kOut % a.wf, e % kOut, v);
       }
       cg::this_cluster().sync();
     }
   }
 }
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 16, kMostCtas = 8;
 
 template <class T, int NT, int C>
 int run_block(Args& a, int S, cudaStream_t s) {
@@ -353,34 +386,41 @@ int run_block(Args& a, int S, cudaStream_t s) {
   auto run = [&](auto kernel) {
     return kv::launch(kernel, (unsigned)(row_tiles * a.clusters * S), 32 * warps, smem, S, s, "matmul_nbits", a);
   };
-  switch (a.s.per) {
-    case 8: return run(nbits_kernel<T, NT, C, 16>);
-    case 4: return run(nbits_kernel<T, NT, C, 32>);
-    case 2: return run(nbits_kernel<T, NT, C, 64>);
-    default: return run(nbits_kernel<T, NT, C, 128>);
-  }
+  auto scaled = [&](auto scale) {
+    using ST = decltype(scale);
+    switch (a.s.per) {
+      case 8: return run(nbits_kernel<T, NT, C, 16, ST>);
+      case 4: return run(nbits_kernel<T, NT, C, 32, ST>);
+      case 2: return run(nbits_kernel<T, NT, C, 64, ST>);
+      default: return run(nbits_kernel<T, NT, C, 128, ST>);
+    }
+  };
+  return a.s.scale_size == 4 ? scaled(float()) : scaled(__nv_bfloat16());
 }
 
 int run_product(Args& a, int type, cudaStream_t s) {
   const int64_t chunks = a.s.chunks;
+  const int most = type == I8Q_F32 ? 1 : 4;  // chunks of one tile of rows that a warp's registers hold
+  int nt = type == I8Q_F32 || a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
+  while (nt > 1 && ceil_div(chunks, (int64_t)kWarps * kMostCtas) > most / nt) nt /= 2;
+  const int room = most / nt;
+  // Warps along k: as many as there are chunks; where strips go round for
+  // several at a time in a CTA, no more than hold k in their registers.
   a.wk = (int)std::min<int64_t>(kWarps, chunks);
+  const int64_t fewest = std::max<int64_t>(1, ceil_div(chunks, room));
+  if (fewest < a.wk && a.s.strips * fewest >= (int64_t)sm_count() * kWarps) a.wk = (int)fewest;
   a.wf = (int)std::max<int64_t>(1, std::min<int64_t>(kWarps / a.wk, ceil_div(a.s.strips, sm_count())));
   int S = 1;
   const auto share = [&] { return ceil_div(chunks, (int64_t)a.wk * S); };  // chunks of a warp
-  // the most rows a pass whose activations 8 clusters' CTAs hold
-  const int most = type == I8Q_F32 ? 1 : 4;
-  int nt = type == I8Q_F32 || a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
-  const auto room = [&] { return type == I8Q_F32 ? most : most / nt; };  // chunks that a warp's registers hold
-  while (nt > 1 && ceil_div(chunks, (int64_t)a.wk * 8) > room()) nt /= 2;
-  while (S < 8 && share() > room()) S *= 2;
-  while (S < 8 && a.s.strips * S * 2 <= sm_count() && chunks >= (int64_t)kWarps * S * 2) S *= 2;
-  const bool held = share() <= room();
+  while (S < kMostCtas && share() > room) S *= 2;
+  while (S < kMostCtas && a.s.strips * S * 2 <= sm_count() && chunks >= (int64_t)kWarps * S * 2) S *= 2;
+  if (S > 1) a.wf = 1;
+  const bool held = share() <= room;
   if (type == I8Q_F32) return held ? run_block<float, 1, 1>(a, S, s) : run_block<float, 1, 0>(a, S, s);
   using B = __nv_bfloat16;
   if (!held) return run_block<B, 1, 0>(a, S, s);
-  const bool one = share() == 1;
   if (nt == 4) return run_block<B, 4, 1>(a, S, s);
-  if (nt == 2) return one ? run_block<B, 2, 1>(a, S, s) : run_block<B, 2, 2>(a, S, s);
+  if (nt == 2) return share() == 1 ? run_block<B, 2, 1>(a, S, s) : run_block<B, 2, 2>(a, S, s);
   return share() <= 2 ? run_block<B, 1, 2>(a, S, s) : run_block<B, 1, 4>(a, S, s);
 }
 
