@@ -88,8 +88,10 @@ struct Args {
   int clusters;   // of a tile of rows
 };
 
-// Tiles of a warp's ring, one of which is being read while the others arrive.
-constexpr int ring_depth(int nt) { return nt == 4 ? 4 : 6; }
+// A warp's ring: stages of its tiles of one strip (or of one tile, where it
+// has no fixed number of them), one of which is read while the others arrive.
+constexpr int stage_tiles(int c) { return c ? c : 1; }
+constexpr int stages(int nt, int c) { return c == 4 ? 2 : c == 2 ? 3 : nt == 4 ? 4 : 6; }
 constexpr int kRound = 16;  // groups of strips between two meetings of a cluster
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -225,7 +227,8 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2
 template <class T, int NT, int C, int G, class ST>
 __global__ void __launch_bounds__(512, 1)
 nbits_kernel(const __grid_constant__ Args a) {
-  constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128, kDepth = ring_depth(NT), kAhead = kDepth - 1;
+  constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128;
+  constexpr int kStages = stages(NT, C), kTiles = stage_tiles(C);
   extern __shared__ __align__(16) uint8_t smem[];
   const int S = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane & 3;
@@ -238,35 +241,43 @@ nbits_kernel(const __grid_constant__ Args a) {
   const int groups = (strips + a.wf - 1) / a.wf, ng = (groups - c0 + a.clusters - 1) / a.clusters;
   const int strip0 = c0 * a.wf + wf, strip_step = a.clusters * a.wf;
   const int live = cw && strip0 < strips ? (strips - strip0 + strip_step - 1) / strip_step : 0;  // groups with a strip for this warp
-  uint8_t* const ring = smem + (size_t)warp * kDepth * tile_bytes;
-  float* const partial = reinterpret_cast<float*>(smem + (size_t)a.wk * a.wf * kDepth * tile_bytes);
+  uint8_t* const ring = smem + (size_t)warp * kStages * kTiles * tile_bytes;
+  float* const partial = reinterpret_cast<float*>(smem + (size_t)a.wk * a.wf * kStages * kTiles * tile_bytes);
   float* const held = partial + 2 * a.wk * a.wf * kOut;
 
   kv::next_kernel_may_start();
   kv::wait_previous_kernel();
 
-  // the next tile to send for
+  // the next stage to send for
   const uint8_t* from = a.packed + ((int64_t)strip0 * chunks + c_begin) * tile_bytes + lane * 16;
-  const int64_t jump = ((int64_t)strip_step * chunks - cw) * tile_bytes;
-  int64_t left = (int64_t)live * cw;
-  int in_group = 0;
-  const uint32_t ring_begin = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16, ring_end = ring_begin + kDepth * tile_bytes;
+  const int64_t jump = ((int64_t)strip_step * chunks - (C ? 0 : cw)) * tile_bytes;
+  int left = C ? live : live * cw, in_group = 0;  // (tiles of 1 KB at least: their number fits)
+  const uint32_t ring_begin = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+  const uint32_t ring_end = ring_begin + kStages * kTiles * tile_bytes;
   uint32_t to = ring_begin;
   const int meta = (tile_bytes - kCodeBytes) / 16;  // at most 40
+  const bool meta1 = lane < meta, meta2 = lane + 32 < meta;
   auto send = [&] {
     if (left > 0) {
-      copy16(to, from);
-      copy16(to + 512, from + 512);
-      if (lane < meta) copy16(to + kCodeBytes, from + kCodeBytes);
-      if (meta > 32 && lane + 32 < meta) copy16(to + kCodeBytes + 512, from + kCodeBytes + 512);
-      from += tile_bytes, --left;
-      if (++in_group == cw) in_group = 0, from += jump;
-      to += tile_bytes;
+#pragma unroll
+      for (int c = 0; c < kTiles; ++c) {
+        if (C && c >= cw) break;
+        const uint8_t* p = from + c * tile_bytes;
+        const uint32_t d = to + c * tile_bytes;
+        copy16(d, p);
+        copy16(d + 512, p + 512);
+        if (meta1) copy16(d + kCodeBytes, p + kCodeBytes);
+        if (meta2) copy16(d + kCodeBytes + 512, p + kCodeBytes + 512);
+      }
+      --left;
+      if (C) from += jump;
+      else if (from += tile_bytes; ++in_group == cw) in_group = 0, from += jump;
+      to += kTiles * tile_bytes;
       if (to == ring_end) to = ring_begin;
     }
     commit();
   };
-  for (int i = 0; i < kAhead; ++i) send();
+  for (int i = 0; i < kStages - 1; ++i) send();
 
   const T* const A = static_cast<const T*>(a.A);
   Fragment<T> x[C ? C : 1][8][NT];
@@ -284,10 +295,16 @@ nbits_kernel(const __grid_constant__ Args a) {
   for (int c = 0; c < C; ++c) load_x(c, c);
 
   const uint8_t* at = ring;
-  auto tile = [&](const Fragment<T> (&xc)[8][NT], float (&y)[NT][4]) {
-    wait_copies<kAhead - 1>();
-    __syncwarp();  // the scales and zero points were copied by other lanes, and all have read the tile before
+  auto next = [&] {
+    at += kTiles * tile_bytes;
+    if (at == ring + kStages * kTiles * tile_bytes) at = ring;
+  };
+  auto arrived = [&] {
+    wait_copies<kStages - 2>();
+    __syncwarp();  // the scales and zero points were copied by other lanes, and all have read the stage before
     send();
+  };
+  auto tile = [&](const Fragment<T> (&xc)[8][NT], const uint8_t* at, float (&y)[NT][4]) {
     const uint4 q0 = *reinterpret_cast<const uint4*>(at + lane * 16), q1 = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
     const Row<ST, kPer> s0(at + kCodeBytes, g), s1(at + kCodeBytes, g + 8);
     Row<uint8_t, kPer> z0, z1;
@@ -295,8 +312,6 @@ nbits_kernel(const __grid_constant__ Args a) {
       z0 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g);
       z1 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g + 8);
     }
-    at += tile_bytes;
-    if (at == ring + kDepth * tile_bytes) at = ring;
     const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
     float acc[NT][4];
 #pragma unroll
@@ -336,12 +351,19 @@ nbits_kernel(const __grid_constant__ Args a) {
   for (int gi = 0; gi < ng; ++gi) {
     float y[NT][4] = {};
     if (gi < live) {
+      arrived();
       if constexpr (C > 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (c < cw) tile(x[c], y);
+          if (c < cw) tile(x[c], at + c * tile_bytes, y);
+        next();
       } else {
-        for (int c = 0; c < cw; ++c) load_x(0, c), tile(x[0], y);
+        for (int c = 0; c < cw; ++c) {
+          load_x(0, c);
+          if (c) arrived();
+          tile(x[0], at, y);
+          next();
+        }
       }
     }
     // the sums of a strip's warps, two buffers in turn
@@ -381,7 +403,7 @@ int run_block(Args& a, int S, cudaStream_t s) {
   const int warps = a.wk * a.wf;
   const int64_t row_tiles = ceil_div(a.M, 8 * NT), groups = ceil_div(a.s.strips, a.wf);
   a.clusters = (int)std::min<int64_t>(groups, std::max<int64_t>(1, sm_count() / S / row_tiles));
-  const int smem = warps * ring_depth(NT) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
+  const int smem = warps * stages(NT, C) * stage_tiles(C) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
   if (row_tiles * a.clusters * S > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: too many rows");
   auto run = [&](auto kernel) {
     return kv::launch(kernel, (unsigned)(row_tiles * a.clusters * S), 32 * warps, smem, S, s, "matmul_nbits", a);
