@@ -410,7 +410,8 @@ int i8q_matmul_nbits_pack(int64_t N, int64_t K, int64_t block_size, const uint8_
 /* A: device (M, K) of `type` (I8Q_F32 | I8Q_BF16), rows lda elements apart; Y:
  * (M, N) of the same type, rows ldy apart; bias: device fp32 [N], or NULL.
  * N .. has_zero as the matrix was packed with.  Any M; the call is made for
- * few rows: it reads the matrix again for every 32 of them (8 of fp32).
+ * few rows: it reads the matrix again for every 64 of bf16 (8 where A is not
+ * 16-byte aligned or lda no multiple of 8), and for every 8 of fp32.
  * Weights and activations enter the products exactly (fp32 activations in
  * three parts of 8 bits), a block's products are summed by the tensor pipe
  * (for fp32, 16 of them) and blocks in fp32, rounded; the order does not

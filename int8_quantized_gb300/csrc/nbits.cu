@@ -12,10 +12,7 @@ namespace i8q {
 namespace {
 
 namespace cg = cooperative_groups;
-using nbits::kCodeBytes;
-using nbits::kTileK;
-using nbits::kTileN;
-using nbits::Shape;
+using namespace nbits;
 
 constexpr int64_t kMost = INT32_MAX - 65536;  // of N, K and M: indices of 32 bits step past them by a tile or two
 
@@ -47,15 +44,15 @@ pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ sca
     const int64_t strip = tile / s.chunks, chunk = tile - strip * s.chunks;
     uint8_t* to = packed + tile * s.tile_bytes;
     {
-      const int half = threadIdx.x / 128, lane = threadIdx.x / 4 % 32, b = threadIdx.x % 4;
-      const int64_t n = strip * kTileN + 8 * half + lane / 4;
+      const int b = threadIdx.x / 64, t = threadIdx.x % 4;
+      const int64_t n = strip * kTileN + threadIdx.x / 4 % 16;
       uint32_t word = 0;
       for (int st = 0; st < 2; ++st)
         for (int j = 0; j < 4; ++j) {
-          const int64_t k = chunk * kTileK + 32 * b + 16 * st + 4 * (lane % 4) + j;
+          const int64_t k = chunk * kTileK + 32 * b + 16 * st + 4 * t + j;
           // past the matrix: code 0, which no activation or a scale of 0 meets
           const uint32_t code = n < s.N && k < s.K ? B[n * row_bytes + k / 2] >> (4 * (k & 1)) & 15u : 0u;
-          word |= code << 4 * (2 * st + j / 2 + 4 * (j % 2));
+          word |= code << 4 * (st + 2 * (j / 2) + 4 * (j % 2));
         }
       reinterpret_cast<uint32_t*>(to)[threadIdx.x] = word;
     }
@@ -73,35 +70,10 @@ pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ sca
   }
 }
 
-// ---- product ------------------------------------------------------------
-struct Args {
-  Shape s;
-  const uint8_t* packed;
-  const void* A;
-  int64_t lda;
-  int a_aligned;  // four neighbouring activations can be read at once
-  const float* bias;
-  void* Y;
-  int64_t ldy;
-  int M;
-  int wk, wf;     // warps along k, strips at a time: wk * wf warps
-  int clusters;   // of a tile of rows
-};
-
 // A warp's ring: stages of its tiles of one strip (or of one tile, where it
 // has no fixed number of them), one of which is read while the others arrive.
 constexpr int stage_tiles(int c) { return c ? c : 1; }
-constexpr int stages(int nt, int c) { return c == 4 ? 2 : c == 2 ? 3 : nt == 4 ? 4 : 6; }
-constexpr int kRound = 16;  // groups of strips between two meetings of a cluster
-
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
+constexpr int stages(int c) { return c == 4 ? 2 : c == 2 ? 3 : 6; }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -117,35 +89,6 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
-
-// N scales or zero points of a tile's row, read as few words.
-template <class T, int N>
-struct Row {
-  static constexpr int kBytes = N * (int)sizeof(T), kWords = kBytes < 4 ? 1 : kBytes / 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ Row() {  // zero points of 8
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0x08080808u;
-  }
-  __device__ __forceinline__ Row(const uint8_t* tile, int row) {
-    const uint8_t* p = tile + row * kBytes;
-    if constexpr (kBytes == 1) w[0] = *p;
-    else if constexpr (kBytes == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
-    else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-    else {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(w + i) = *reinterpret_cast<const uint4*>(p + 4 * i);
-    }
-  }
-  __device__ __forceinline__ float value(int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-  }
-  __device__ __forceinline__ uint32_t pair(int i) const {  // 128 + zero point twice, as bf16
-    return __byte_perm(w[i / 4], 0x43434343u, 0x4040u + (i & 3) * 0x0101u);
-  }
-};
 
 // Two codes at nibbles 0 and 4 of w as bf16 numbers less their zero point:
 // 0x43 over a byte c < 128 is 128 + c, and 128 + z is subtracted exactly.
@@ -211,9 +154,6 @@ struct Fragment<float> {
   }
 };
 
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // A warp has the activations of its share of k (at most C chunks of 128; C 0:
 // read again for each tile) in registers, as the fragments of the products,
 // and streams the tiles of one strip of 16 outputs after the other through a
@@ -228,7 +168,7 @@ template <class T, int NT, int C, int G, class ST>
 __global__ void __launch_bounds__(512, 1)
 nbits_kernel(const __grid_constant__ Args a) {
   constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128;
-  constexpr int kStages = stages(NT, C), kTiles = stage_tiles(C);
+  constexpr int kStages = stages(C), kTiles = stage_tiles(C);
   extern __shared__ __align__(16) uint8_t smem[];
   const int S = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane & 3;
@@ -305,20 +245,24 @@ nbits_kernel(const __grid_constant__ Args a) {
     send();
   };
   auto tile = [&](const Fragment<T> (&xc)[8][NT], const uint8_t* at, float (&y)[NT][4]) {
-    const uint4 q0 = *reinterpret_cast<const uint4*>(at + lane * 16), q1 = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
+    uint32_t w0[4], w1[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      w0[b] = reinterpret_cast<const uint32_t*>(at)[b * 64 + lane];
+      w1[b] = reinterpret_cast<const uint32_t*>(at)[b * 64 + 32 + lane];
+    }
     const Row<ST, kPer> s0(at + kCodeBytes, g), s1(at + kCodeBytes, g + 8);
     Row<uint8_t, kPer> z0, z1;
     if (a.s.has_zero) {
       z0 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g);
       z1 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g + 8);
     }
-    const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
     float acc[NT][4];
 #pragma unroll
     for (int st = 0; st < 8; ++st) {
       const int i = st * 16 / G;
-      const uint32_t v0 = w0[st / 2] >> (8 * (st & 1)), v1 = w1[st / 2] >> (8 * (st & 1));
-      const uint32_t f[4] = {pair(v0, z0.pair(i)), pair(v1, z1.pair(i)), pair(v0 >> 4, z0.pair(i)), pair(v1 >> 4, z1.pair(i))};
+      const uint32_t v0 = w0[st / 2] >> (4 * (st & 1)), v1 = w1[st / 2] >> (4 * (st & 1));
+      const uint32_t f[4] = {pair(v0, z0.pair(i)), pair(v1, z1.pair(i)), pair(v0 >> 8, z0.pair(i)), pair(v1 >> 8, z1.pair(i))};
       const bool first = kParts > 1 || st * 16 % G == 0, last = kParts > 1 || (st + 1) * 16 % G == 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -396,14 +340,12 @@ nbits_kernel(const __grid_constant__ Args a) {
   }
 }
 
-constexpr int kWarps = 16, kMostCtas = 8;
-
 template <class T, int NT, int C>
 int run_block(Args& a, int S, cudaStream_t s) {
   const int warps = a.wk * a.wf;
   const int64_t row_tiles = ceil_div(a.M, 8 * NT), groups = ceil_div(a.s.strips, a.wf);
   a.clusters = (int)std::min<int64_t>(groups, std::max<int64_t>(1, sm_count() / S / row_tiles));
-  const int smem = warps * stages(NT, C) * stage_tiles(C) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
+  const int smem = warps * stages(C) * stage_tiles(C) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
   if (row_tiles * a.clusters * S > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: too many rows");
   auto run = [&](auto kernel) {
     return kv::launch(kernel, (unsigned)(row_tiles * a.clusters * S), 32 * warps, smem, S, s, "matmul_nbits", a);
@@ -422,14 +364,12 @@ int run_block(Args& a, int S, cudaStream_t s) {
 
 int run_product(Args& a, int type, cudaStream_t s) {
   const int64_t chunks = a.s.chunks;
-  const int most = type == I8Q_F32 ? 1 : 4;  // chunks of one tile of rows that a warp's registers hold
-  int nt = type == I8Q_F32 || a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
-  while (nt > 1 && ceil_div(chunks, (int64_t)kWarps * kMostCtas) > most / nt) nt /= 2;
-  const int room = most / nt;
+  // chunks of the rows that a warp's registers hold (two stages of four of the largest tiles would not fit)
+  const int room = type == I8Q_F32 ? 1 : a.s.tile_bytes > 1408 ? 2 : 4;
   // Warps along k: as many as there are chunks; where strips go round for
   // several at a time in a CTA, no more than hold k in their registers.
   a.wk = (int)std::min<int64_t>(kWarps, chunks);
-  const int64_t fewest = std::max<int64_t>(1, ceil_div(chunks, room));
+  const int64_t fewest = ceil_div(chunks, room);
   if (fewest < a.wk && a.s.strips * fewest >= (int64_t)sm_count() * kWarps) a.wk = (int)fewest;
   a.wf = (int)std::max<int64_t>(1, std::min<int64_t>(kWarps / a.wk, ceil_div(a.s.strips, sm_count())));
   int S = 1;
@@ -441,8 +381,6 @@ int run_product(Args& a, int type, cudaStream_t s) {
   if (type == I8Q_F32) return held ? run_block<float, 1, 1>(a, S, s) : run_block<float, 1, 0>(a, S, s);
   using B = __nv_bfloat16;
   if (!held) return run_block<B, 1, 0>(a, S, s);
-  if (nt == 4) return run_block<B, 4, 1>(a, S, s);
-  if (nt == 2) return share() == 1 ? run_block<B, 2, 1>(a, S, s) : run_block<B, 2, 2>(a, S, s);
   return share() <= 2 ? run_block<B, 1, 2>(a, S, s) : run_block<B, 1, 4>(a, S, s);
 }
 
@@ -470,6 +408,8 @@ extern "C" int i8q_matmul_nbits_pack(int64_t N, int64_t K, int64_t block_size, c
     return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: packed must be 16-byte aligned");
   if (packed_bytes < (size_t)s.strips * (size_t)s.chunks * (size_t)s.tile_bytes)
     return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits_pack: packed is smaller than matmul_nbits_packed_size");
+  // (allocated here, so that the product's first call may be a captured one)
+  if (!device_status_word()) return fail(I8Q_ERR_CUDA, "matmul_nbits_pack: no status word");
   I8Q_PROF("matmul_nbits_pack", as_stream(stream));
   const int64_t blocks = std::min<int64_t>(s.strips * s.chunks, 64 * (int64_t)sm_count());
   pack_kernel<<<(unsigned)blocks, 256, 0, as_stream(stream)>>>(s, B, scales, zero_points, static_cast<uint8_t*>(packed));
@@ -499,5 +439,6 @@ extern "C" int i8q_matmul_nbits(const void* A, int type, int64_t M, int64_t lda,
   a.a_aligned = reinterpret_cast<uintptr_t>(A) % (4 * es) == 0 && (M == 1 || lda % 4 == 0);
   cudaStream_t s = as_stream(stream);
   I8Q_PROF("matmul_nbits", s);
-  return run_product(a, type, s);
+  // more than one tile of 8 rows: 4096 -> 14336 by 16 rows 15.6 us there, 20 here; by 8 rows 17 and 11
+  return type == I8Q_BF16 && M > 8 && tc_takes(a) ? run_tc(a, s) : run_product(a, type, s);
 }

@@ -110,6 +110,21 @@ def test_deep_products_by_clusters(dev, M, K, type):
     check(dev, M, 60, K, 64, type, seed=K)
 
 
+@pytest.mark.parametrize("M", [9, 16, 17, 33, 64, 65, 200])
+@pytest.mark.parametrize("N,K,block", [(128, 128, 128), (100, 200, 16), (1000, 384, 32), (3000, 640, 64), (20000, 384, 128),
+                                       (2433, 4096, 32), (500, 14336, 64), (130, 33000, 128), (40, 70000, 256)])
+def test_many_rows(dev, M, N, K, block):
+    """The tcgen05 kernel: 16, 32 and 64 rows at a time, each block, odd and even numbers of chunks a CTA,
+    activations that stay and that are sent for again, clusters of each size."""
+    check(dev, M, N, K, block, scales="f32" if M % 2 else "bf16", zero=block != 64, bias=M == 33, seed=M)
+
+
+def test_many_rows_unaligned(dev):
+    check(dev, 20, 300, 1000, 32, pad=1)
+    check(dev, 20, 300, 1000, 32, offset=3, pad=5)
+    check(dev, 20, 300, 1000, 32, pad=8)
+
+
 def test_many_strips_of_a_cluster(dev):
     """More groups of strips than a cluster joins at once."""
     check(dev, 3, 16 * 700, 14336, 128, seed=1)
@@ -131,21 +146,23 @@ def test_large_and_small_activations(dev):
 
 @pytest.mark.parametrize("type", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
-def test_a_row_that_is_not_finite_stays_alone(dev, type, bad):
+@pytest.mark.parametrize("R", [3, 20])
+def test_a_row_that_is_not_finite_stays_alone(dev, R, type, bad):
     g = gen(3)
     N, K, block = 40, 256, 32
     B, s, z = weights(g, N, K, block, "f32", False)
     s = s.abs() + 0.01
-    A = torch.randn((3, K), generator=g)
+    rows = [0] + list(range(2, R))
+    A = torch.randn((R, K), generator=g)
     A[1, 77] = bad
     A = A.to(TYPES[type])
     m = q.MatMulNBits(B.to(dev), s.to(dev), K, block)
-    Y = torch.empty((3, N), dtype=A.dtype, device=dev)
+    Y = torch.empty((R, N), dtype=A.dtype, device=dev)
     m.forward(A.to(dev), Y)
     q.sync_status()
     w, sc = dense(B, s, None, K, block)
     y = Y.cpu().float()
-    assert torch.isfinite(y[[0, 2]]).all()
+    assert torch.isfinite(y[rows]).all()
     c = w[:, 77]
     if bad != bad:
         assert torch.isnan(y[1]).all()
@@ -184,7 +201,8 @@ def test_no_rows(dev):
     q.sync_status()
 
 
-def test_repeats_streams_and_graphs(dev):
+@pytest.mark.parametrize("rows", [3, 9, 50])
+def test_repeats_streams_and_graphs(dev, rows):
     g = gen(5)
     N, K = 300, 14336
     B, s, z = (t.to(dev) for t in weights(g, N, K, 32))
@@ -193,8 +211,8 @@ def test_repeats_streams_and_graphs(dev):
     m = q.MatMulNBits(B, s, K, 32, zero_points=z, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     B.fill_(0), s.fill_(0), z.fill_(0)  # not read again
-    A = torch.randn((9, K), generator=g).to(torch.bfloat16).to(dev)
-    one, two, three = (torch.empty((9, N), dtype=torch.bfloat16, device=dev) for _ in range(3))
+    A = torch.randn((rows, K), generator=g).to(torch.bfloat16).to(dev)
+    one, two, three = (torch.empty((rows, N), dtype=torch.bfloat16, device=dev) for _ in range(3))
     m.forward(A, one)
     m.forward(A, two)
     side.wait_stream(torch.cuda.current_stream())
