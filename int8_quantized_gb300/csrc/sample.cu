@@ -149,23 +149,25 @@ struct Args {
 };
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kDigit = 11, kMostCtas = 8;
+constexpr int kFine = 64, kGroups = kBins / kFine;  // bins of a group: one for each lane
+static_assert(kGroups == 32 && kMostCtas * kFine == kThreads, "");
 
 struct Shared {
   float2 powers[kSteps + 1];
-  uint32_t lo[kBins], hi[kBins];  // of this CTA
-  uint64_t total[kBins];          // of the row
+  uint32_t lo[2][kBins], hi[2][kBins];        // of this CTA, two histograms in turn
+  uint64_t group[2][kMostCtas][kGroups];      // sums of their groups, of all CTAs
+  uint64_t fine[kMostCtas][kFine];            // one group's bins, of all CTAs
   uint64_t warp_sum[kWarps];
   uint64_t best[kMostCtas];              // of each CTA of the cluster
   uint64_t mass[kMostCtas][kWarps];      // kept weight of each warp's tokens, of all CTAs
   uint32_t ties[kMostCtas][kWarps];      // and its tokens of the border's key
-  uint64_t before;
-  uint32_t bin;
+  Scale scale;
 };
 
-__device__ __forceinline__ void add(Shared& sh, uint32_t bin, uint64_t w) {
-  const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
+__device__ __forceinline__ void add(Shared& sh, int which, uint32_t bin, uint64_t w) {
+  const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[which][bin], low);
   const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
-  if (high) atomicAdd(&sh.hi[bin], high);
+  if (high) atomicAdd(&sh.hi[which][bin], high);
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
@@ -223,22 +225,27 @@ sample_kernel(const __grid_constant__ Args a) {
     }
   };
 
+  // f(first token, logits) of each of this lane's vectors, two on their way
+  auto each = [&](auto f) {
+    for (int v = v0 + lane; v < v1; v += 64) {
+      float y[kVec], z[kVec];
+      load(v, y), load(v + 32, z);
+      f(v * kVec - skew, y);
+      if (v + 32 < v1) f((v + 32) * kVec - skew, z);
+    }
+  };
+
   // ---- the largest logit, and its first place ----
   const float temperature = a.temperature ? a.temperature[row] : 1.0f, u = a.random[row];
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   int top_k = a.top_k ? a.top_k[row] : 0;
   if (top_k <= 0 || top_k > a.V) top_k = a.V;
   uint64_t best = 0;
-  for (int v = v0 + lane; v < v1; v += 32) {
-    float y[kVec];
-    load(v, y);
+  each([&](int first, const float (&y)[kVec]) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int i = v * kVec - skew + j;
-      if (i < 0 || i >= a.V) continue;
-      best = max(best, (uint64_t)K::of(y[j]) << 32 | (uint32_t)~i);
-    }
-  }
+    for (int j = 0; j < kVec; ++j)
+      if (first + j >= 0 && first + j < a.V) best = max(best, (uint64_t)K::of(y[j]) << 32 | (uint32_t)~(first + j));
+  });
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
   if (lane == 0) sh.warp_sum[warp] = best;
@@ -261,109 +268,105 @@ sample_kernel(const __grid_constant__ Args a) {
     }
     return;
   }
-  const Scale scale = make_scale(largest, temperature);
+  // (fp64 has two lanes a cycle: one division, not 512)
+  if (threadIdx.x == 0) sh.scale = make_scale(largest, temperature);
+  __syncthreads();
+  const Scale scale = sh.scale;
 
   // ---- the border: kept are the keys above it and the first `ties` of its own ----
   uint32_t border = 0, ties = UINT32_MAX;
   bool cut = false;
-  // Counts (or weights) of the tokens within the border so far by their
-  // digit of key bits [shift, shift + kDigit), prefix: the bits above.
-  auto histogram = [&](bool by_weight, int shift, uint32_t prefix) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+  int which = 1;
+  // Counts (or weights) of the tokens within the border so far by their digit
+  // of `bits` key bits from `shift` on, prefix: the bits above.  The CTAs
+  // exchange the sums of groups of bins; `find` then reads one group's bins.
+  auto histogram = [&](bool by_weight, int shift, int bits, uint32_t prefix) {
+    which ^= 1;  // (the other one may still be read)
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[which][i] = sh.hi[which][i] = 0;
     __syncthreads();
-    const int above = shift + kDigit;
-    for (int v = v0 + lane; v < v1; v += 32) {
-      float y[kVec];
-      load(v, y);
+    const int above = shift + bits;
+    const uint32_t mask = (1u << bits) - 1;
+    each([&](int first, const float (&y)[kVec]) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         const uint32_t k = K::of(y[j]);
         if (above < 32 && k >> above != prefix) continue;
         if (!by_weight) {
-          const int i = v * kVec - skew + j;
-          if (i >= 0 && i < a.V) atomicAdd(&sh.lo[k >> shift & (kBins - 1)], 1u);
+          if (first + j >= 0 && first + j < a.V) atomicAdd(&sh.lo[which][k >> shift & mask], 1u);
         } else if (!cut || k > border) {
           const uint64_t w = weight(y[j], scale, sh.powers);
-          if (w) add(sh, k >> shift & (kBins - 1), w);
+          if (w) add(sh, which, k >> shift & mask, w);
         }
       }
-    }
+    });
     if (by_weight && cut && rank == 0 && threadIdx.x == 0 && (above >= 32 || border >> above == prefix))
-      add(sh, border >> shift & (kBins - 1), ties * weight(K::value(border), scale, sh.powers));
-    meet();
-    for (int i = threadIdx.x; i < kBins / S; i += kThreads) {
-      const int b = rank * (kBins / S) + i;
+      add(sh, which, border >> shift & mask, ties * weight(K::value(border), scale, sh.powers));
+    __syncthreads();
+    for (int g = warp; g < kGroups; g += kWarps) {
       uint64_t sum = 0;
-      for (int r = 0; r < S; ++r) {
-        const Shared* other = cluster.map_shared_rank(&sh, r);
-        sum += (uint64_t)other->hi[b] << 32 | other->lo[b];
-      }
-      for (int r = 0; r < S; ++r) cluster.map_shared_rank(&sh, r)->total[b] = sum;
+#pragma unroll
+      for (int b = g * kFine + lane; b < (g + 1) * kFine; b += 32) sum += (uint64_t)sh.hi[which][b] << 32 | sh.lo[which][b];
+      sum = warp_sum64(sum);
+      if (lane < S) cluster.map_shared_rank(&sh, lane)->group[which][rank][g] = sum;
     }
     meet();
   };
-  // The digit in whose bin the sum from the top reaches target, and the sum before it.
-  auto find = [&](uint64_t target, uint32_t& bin, uint64_t& before) {
-    constexpr int kEach = kBins / kThreads;
-    uint64_t t[kEach], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) t[i] = sh.total[kBins - 1 - (threadIdx.x * kEach + i)], sum += t[i];
-    const uint64_t inclusive = warp_scan64(sum, lane);
-    if (lane == 31) sh.warp_sum[warp] = inclusive;
-    __syncthreads();
-    uint64_t at = inclusive - sum;
-    for (int w = 0; w < warp; ++w) at += sh.warp_sum[w];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if (at < target && target <= at + t[i]) sh.bin = kBins - 1 - (threadIdx.x * kEach + i), sh.before = at;
-      at += t[i];
+  // The place, from the top, at which the running sum of a lane's two values
+  // (each lane's second below its first) reaches target: 2 lane + 0 or 1, and
+  // the sum before it.  All warps of the CTA work it out.
+  auto reached = [&](uint64_t first, uint64_t second, uint64_t target, uint64_t& before) {
+    const uint64_t upto = warp_scan64(first + second, lane), mine = upto - first - second;
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
+    const bool later = mine + first < target;
+    before = __shfl_sync(0xffffffffu, later ? mine + first : mine, at);
+    return 2 * at + (int)__shfl_sync(0xffffffffu, (unsigned)later, at);
+  };
+  auto group_sum = [&](int g) {
+    uint64_t sum = 0;
+    for (int r = 0; r < S; ++r) sum += sh.group[which][r][g];
+    return sum;
+  };
+  // The digit in whose bin the sum from the top reaches target (at most the
+  // whole sum), and the sum before it.
+  auto find = [&](uint64_t target, uint64_t& before) {
+    uint64_t inside;
+    const int group = kGroups - 1 - reached(group_sum(kGroups - 1 - lane), 0, target, before) / 2;
+    if ((int)threadIdx.x < S * kFine) {
+      const int r = threadIdx.x / kFine, b = threadIdx.x % kFine;
+      const Shared* other = cluster.map_shared_rank(&sh, r);
+      sh.fine[r][b] = (uint64_t)other->hi[which][group * kFine + b] << 32 | other->lo[which][group * kFine + b];
     }
     __syncthreads();
-    bin = sh.bin, before = sh.before;
-    __syncthreads();
+    uint64_t t[2] = {0, 0};
+    for (int r = 0; r < S; ++r) t[0] += sh.fine[r][kFine - 1 - 2 * lane], t[1] += sh.fine[r][kFine - 2 - 2 * lane];
+    const int bin = group * kFine + kFine - 1 - reached(t[0], t[1], target - before, inside);
+    before += inside;
+    return (uint32_t)bin;
   };
   constexpr int kFirst = K::kBits - kDigit;
+  // The first histogram is there: the key at which the sum reaches target, and what is missing before it.
   auto descend = [&](bool by_weight, uint64_t target, uint32_t& key, uint64_t& missing) {
-    // (the first histogram is there)
-    uint32_t bin;
     uint64_t before;
-    find(target, bin, before);
+    key = find(target, before);
     target -= before;
-    key = bin;
     for (int shift = kFirst; shift > 0;) {
       const int bits = min(kDigit, shift);
       shift -= bits;
-      // a last digit of fewer bits: the prefix's lowest bits lie in its bins too
-      const int lower = kDigit - bits;
-      histogram(by_weight, shift, key >> lower);
-      if (lower) {  // the bins that belong to the prefix
-        const uint32_t mine = key & ((1u << lower) - 1);
-        for (int i = threadIdx.x; i < kBins; i += kThreads)
-          if ((uint32_t)i >> bits != mine) sh.total[i] = 0;
-        __syncthreads();
-      }
-      find(target, bin, before);
+      histogram(by_weight, shift, bits, key);
+      key = key << bits | find(target, before);
       target -= before;
-      key = key << bits | (bin & ((1u << bits) - 1));
     }
     missing = target;
   };
   if (top_k < a.V) {
     uint64_t missing;
-    histogram(false, kFirst, 0);
+    histogram(false, kFirst, kDigit, 0);
     descend(false, (uint64_t)top_k, border, missing);
     ties = (uint32_t)missing, cut = true;
   }
   if (top_p < 1.0f) {
-    histogram(true, kFirst, 0);
-    uint64_t sum = 0;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sum += sh.total[i];
-    sum = warp_sum64(sum);
-    if (lane == 0) sh.warp_sum[warp] = sum;
-    __syncthreads();
-    sum = 0;
-    for (int w = 0; w < kWarps; ++w) sum += sh.warp_sum[w];
-    __syncthreads();
+    histogram(true, kFirst, kDigit, 0);
+    const uint64_t sum = warp_sum64(group_sum(lane));
     bool more;
     uint64_t target = share(top_p, sum, more), missing;
     target = max(target + more, (uint64_t)1);
@@ -382,9 +385,7 @@ sample_kernel(const __grid_constant__ Args a) {
   }();
   uint64_t mass = 0;
   uint32_t same = 0;
-  for (int v = v0 + lane; v < v1; v += 32) {
-    float y[kVec];
-    load(v, y);
+  each([&](int, const float (&y)[kVec]) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       const uint32_t k = K::of(y[j]);
@@ -395,7 +396,7 @@ sample_kernel(const __grid_constant__ Args a) {
       const uint64_t w = weight(y[j], scale, sh.powers);
       if (w >= least) mass += w;
     }
-  }
+  });
   mass = warp_sum64(mass);
   same = __reduce_add_sync(0xffffffffu, same);
   if (lane < S) {
@@ -405,21 +406,48 @@ sample_kernel(const __grid_constant__ Args a) {
   meet();
   uint64_t tie_weight = cut ? weight(K::value(border), scale, sh.powers) : 0;
   if (tie_weight < least) tie_weight = 0;
-  uint64_t sum = 0, before = 0;
-  uint32_t seen = 0, seen_before = 0;
-  for (int i = 0; i < parts; ++i) {
-    const uint32_t here = cut ? min(sh.ties[i / kWarps][i % kWarps], ties - seen) : 0;
-    if (i == part) before = sum, seen_before = seen;
-    sum += sh.mass[i / kWarps][i % kWarps] + here * tie_weight;
-    seen += here;
-    if (i == part) mass = sum;
+  // the running sums of the warps of the cluster, four to a lane (parts <= 128); each warp works them out
+  uint64_t part_mass[4], lane_mass = 0;
+  uint32_t part_ties[4], lane_ties = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int p = lane * 4 + i;
+    part_mass[i] = p < parts ? sh.mass[p / kWarps][p % kWarps] : 0;
+    part_ties[i] = p < parts && cut ? sh.ties[p / kWarps][p % kWarps] : 0;
+    lane_ties += part_ties[i];
   }
+  uint32_t seen = lane_ties;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint32_t w = __shfl_up_sync(0xffffffffu, seen, m);
+    if (lane >= m) seen += w;
+  }
+  seen -= lane_ties;
+  uint32_t part_seen[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    part_seen[i] = seen;
+    const uint32_t here = seen < ties ? min(part_ties[i], ties - seen) : 0;
+    seen += part_ties[i];
+    part_mass[i] += here * tie_weight;
+    lane_mass += part_mass[i];
+  }
+  const uint64_t upto = warp_scan64(lane_mass, lane), sum = __shfl_sync(0xffffffffu, upto, 31);
+  uint64_t before = upto - lane_mass;
+  uint32_t seen_before = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < (part & 3)) before += part_mass[i];
+    if (i == (part & 3)) mass = before + part_mass[i], seen_before = part_seen[i];
+  }
+  before = __shfl_sync(0xffffffffu, before, part / 4), mass = __shfl_sync(0xffffffffu, mass, part / 4);
+  seen_before = __shfl_sync(0xffffffffu, seen_before, part / 4);
   const uint64_t target = share(u, sum, more);  // taken: the first token up to which the sum is above it
   if (!(before <= target && target < mass)) return;
 
   // ---- the token, by the warp that has it ----
   uint64_t at = before;
-  uint32_t left = cut ? ties - seen_before : 0;
+  uint32_t left = cut && seen_before < ties ? ties - seen_before : 0;
   for (int vb = v0; vb < v1; vb += 32) {
     const int v = vb + lane;
     float y[kVec];

@@ -45,7 +45,7 @@ def kept_weights(x, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
 
 
 def rows_of(x, R, dtype, dev):
-    return torch.from_numpy(np.array(np.broadcast_to(x, (R, x.size)))).to(dtype).to(dev)
+    return torch.from_numpy(np.tile(x, (R, 1))).to(dtype).to(dev)
 
 
 def per_row(v, R, dtype, dev):
