@@ -149,6 +149,8 @@ struct Args {
 };
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kDigit = 11, kMostCtas = 8;
+constexpr int kList = 1024, kLists = 2048;  // keys of the border's bin: of a CTA, of all
+constexpr int kSmall = 6;                   // bits of a digit of those
 constexpr int kFine = 64, kGroups = kBins / kFine;  // bins of a group: one for each lane
 static_assert(kGroups == 32 && kMostCtas * kFine == kThreads, "");
 
@@ -158,6 +160,8 @@ struct Shared {
   uint64_t group[2][kMostCtas][kGroups];      // sums of their groups, of all CTAs
   uint64_t fine[kMostCtas][kFine];            // one group's bins, of all CTAs
   uint64_t warp_sum[kWarps];
+  uint32_t list[kList], keys[kLists];
+  uint32_t count;
   uint64_t best[kMostCtas];              // of each CTA of the cluster
   uint64_t mass[kMostCtas][kWarps];      // kept weight of each warp's tokens, of all CTAs
   uint32_t ties[kMostCtas][kWarps];      // and its tokens of the border's key
@@ -240,12 +244,20 @@ sample_kernel(const __grid_constant__ Args a) {
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   int top_k = a.top_k ? a.top_k[row] : 0;
   if (top_k <= 0 || top_k > a.V) top_k = a.V;
-  uint64_t best = 0;
+  float high = -INFINITY;
+  int place = 0x7fffffff;
   each([&](int first, const float (&y)[kVec]) {
+    float top = y[0];  // (fmaxf leaves NaN out; places outside the row are -infinity)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      if (first + j >= 0 && first + j < a.V) best = max(best, (uint64_t)K::of(y[j]) << 32 | (uint32_t)~(first + j));
+    for (int j = 1; j < kVec; ++j) top = fmaxf(top, y[j]);
+    if (top > high) {
+      high = top;
+#pragma unroll
+      for (int j = kVec - 1; j >= 0; --j)
+        if (y[j] == top) place = first + j;
+    }
   });
+  uint64_t best = (uint64_t)K::of(high) << 32 | (uint32_t)~place;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
   if (lane == 0) sh.warp_sum[warp] = best;
@@ -277,30 +289,31 @@ sample_kernel(const __grid_constant__ Args a) {
   uint32_t border = 0, ties = UINT32_MAX;
   bool cut = false;
   int which = 1;
-  // Counts (or weights) of the tokens within the border so far by their digit
-  // of `bits` key bits from `shift` on, prefix: the bits above.  The CTAs
-  // exchange the sums of groups of bins; `find` then reads one group's bins.
-  auto histogram = [&](bool by_weight, int shift, int bits, uint32_t prefix) {
+  // Counts (or weights) of the tokens within the border so far by their bins,
+  // bin(key, logit) (negative: left out).  The CTAs exchange the sums of groups
+  // of bins; `find` then reads one group's bins.
+  auto histogram = [&](bool by_weight, auto bin) {
     which ^= 1;  // (the other one may still be read)
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[which][i] = sh.hi[which][i] = 0;
     __syncthreads();
-    const int above = shift + bits;
-    const uint32_t mask = (1u << bits) - 1;
     each([&](int first, const float (&y)[kVec]) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         const uint32_t k = K::of(y[j]);
-        if (above < 32 && k >> above != prefix) continue;
+        const int b = bin(k, y[j]);
+        if (b < 0) continue;
         if (!by_weight) {
-          if (first + j >= 0 && first + j < a.V) atomicAdd(&sh.lo[which][k >> shift & mask], 1u);
+          if (first + j >= 0 && first + j < a.V) atomicAdd(&sh.lo[which][b], 1u);
         } else if (!cut || k > border) {
           const uint64_t w = weight(y[j], scale, sh.powers);
-          if (w) add(sh, which, k >> shift & mask, w);
+          if (w) add(sh, which, b, w);
         }
       }
     });
-    if (by_weight && cut && rank == 0 && threadIdx.x == 0 && (above >= 32 || border >> above == prefix))
-      add(sh, which, border >> shift & mask, ties * weight(K::value(border), scale, sh.powers));
+    if (by_weight && cut && rank == 0 && threadIdx.x == 0) {
+      const int b = bin(border, K::value(border));
+      if (b >= 0) add(sh, which, b, ties * weight(K::value(border), scale, sh.powers));
+    }
     __syncthreads();
     for (int g = warp; g < kGroups; g += kWarps) {
       uint64_t sum = 0;
@@ -343,29 +356,89 @@ sample_kernel(const __grid_constant__ Args a) {
     before += inside;
     return (uint32_t)bin;
   };
-  constexpr int kFirst = K::kBits - kDigit;
-  // The first histogram is there: the key at which the sum reaches target, and what is missing before it.
+  // The first bins are even steps of the exponent, 32 to a factor of 2 of the
+  // weight: logits spread over several hundred of them, where the keys' first
+  // digit has four to an octave, and a handful of addresses took all the adds
+  // (32000 tokens: 8 us a histogram).
+  auto step = [&](uint32_t, float y) {
+    const float d = y == scale.max ? 0.0f : __fmul_rn(__fadd_rn(scale.half, -0.5f * y), scale.ch);
+    return kBins - 1 - (d < 63.9f ? (int)(32.0f * d) : kBins - 1);  // (infinities and NaN: the last)
+  };
+  // After the first histogram: the key at which the sum from the top reaches target, and what is missing before it.
   auto descend = [&](bool by_weight, uint64_t target, uint32_t& key, uint64_t& missing) {
     uint64_t before;
-    key = find(target, before);
+    const int bin = (int)find(target, before);
     target -= before;
-    for (int shift = kFirst; shift > 0;) {
-      const int bits = min(kDigit, shift);
-      shift -= bits;
-      histogram(by_weight, shift, bits, key);
-      key = key << bits | find(target, before);
-      target -= before;
+    // the keys of that bin, where they are few, brought together in each CTA
+    if (threadIdx.x == 0) sh.count = 0;  // (read by others before the last meeting, at the latest)
+    __syncthreads();
+    each([&](int first, const float (&y)[kVec]) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t k = K::of(y[j]);
+        if (step(k, y[j]) != bin || first + j < 0 || first + j >= a.V || (by_weight && cut && k <= border)) continue;
+        const uint32_t at = atomicAdd(&sh.count, 1u);
+        if (at < kList) sh.list[at] = k;
+      }
+    });
+    meet();
+    uint32_t all = 0;
+    bool few = true;
+    for (int r = 0; r < S; ++r) {
+      const Shared* other = cluster.map_shared_rank(&sh, r);
+      const uint32_t n = other->count;
+      few = few && n <= kList && all + n <= kLists;
+      if (few)
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads) sh.keys[all + i] = other->list[i];
+      all += n;
+    }
+    key = 0;
+    if (few) {  // (the same in all CTAs)
+      const bool extra = by_weight && cut && step(border, K::value(border)) == bin;  // the border's ties, as one
+      for (int shift = K::kBits; shift > 0;) {
+        const int bits = min(kSmall, shift);
+        shift -= bits;
+        if (threadIdx.x < 1 << kSmall) sh.lo[which ^ 1][threadIdx.x] = sh.hi[which ^ 1][threadIdx.x] = 0;
+        __syncthreads();
+        auto count = [&](uint32_t k, uint32_t times) {
+          if (shift + bits < 32 && k >> (shift + bits) != key) return;
+          add(sh, which ^ 1, k >> shift & ((1u << bits) - 1), times * (by_weight ? weight(K::value(k), scale, sh.powers) : 1));
+        };
+        for (uint32_t i = threadIdx.x; i < all; i += kThreads) count(sh.keys[i], 1);
+        if (extra && threadIdx.x == 0) count(border, ties);
+        __syncthreads();
+        const int top = (1 << kSmall) - 1 - 2 * lane;
+        const uint32_t* lo = sh.lo[which ^ 1];
+        const uint32_t* hi = sh.hi[which ^ 1];
+        uint64_t inside;
+        const int at = reached((uint64_t)hi[top] << 32 | lo[top], (uint64_t)hi[top - 1] << 32 | lo[top - 1], target, inside);
+        key = key << bits | (uint32_t)((1 << kSmall) - 1 - at);
+        target -= inside;
+        __syncthreads();
+      }
+    } else {  // (many equal logits, say) digits of the keys, from the top
+      for (int shift = K::kBits; shift > 0;) {
+        const int bits = min(kDigit, shift);
+        shift -= bits;
+        const uint32_t prefix = key, mask = (1u << bits) - 1;
+        const int above = shift + bits, low = shift;
+        histogram(by_weight, [&](uint32_t k, float y) {
+          return step(k, y) != bin || (above < 32 && k >> above != prefix) ? -1 : (int)(k >> low & mask);
+        });
+        key = key << bits | find(target, before);
+        target -= before;
+      }
     }
     missing = target;
   };
   if (top_k < a.V) {
     uint64_t missing;
-    histogram(false, kFirst, kDigit, 0);
+    histogram(false, step);
     descend(false, (uint64_t)top_k, border, missing);
     ties = (uint32_t)missing, cut = true;
   }
   if (top_p < 1.0f) {
-    histogram(true, kFirst, kDigit, 0);
+    histogram(true, step);
     const uint64_t sum = warp_sum64(group_sum(lane));
     bool more;
     uint64_t target = share(top_p, sum, more), missing;
