@@ -312,3 +312,47 @@ def test_no_rows_and_refusals(dev):
             q.sample(x, u, t, **kw)
     torch.cuda.synchronize()
     assert (t == 5).all()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(T=0.7, top_p=0.8), dict(T=0.5, top_k=3000, top_p=0.9, min_p=0.001), dict(top_k=33000 - 5)])
+def test_many_long_rows_of_odd_values(dev, kw):
+    """Rows whose weights come from a table, and what the table does not hold:
+    zeros, numbers below 2^-16 and from 2^7 on, infinities, NaN, masks, and runs
+    of equal logits longer than a list."""
+    R, V = 160, 33000
+    x = torch.from_numpy(logits_of(R * V, 2.0, 9).reshape(R, V))
+    g = torch.Generator()
+    g.manual_seed(2)
+    some = torch.rand((R, V), generator=g)
+    x[0:20][some[0:20] < 0.5] = 0.0
+    x[20:40] *= 1e-6
+    x[40:60] *= 100.0
+    x[60:80][some[60:80] < 0.9] = -math.inf
+    x[80:100][some[80:100] < 0.3] = math.nan
+    x[100:120] = 2.0
+    x[120:130, 5::7] = math.inf
+    x[130:140] = x[130:140].round()
+    x[140:150][some[140:150] < 0.5] = torch.finfo(torch.bfloat16).min
+    x[150] = -math.inf
+    x = x.to(torch.bfloat16)
+    u = torch.rand((R,), generator=g)
+    tokens, logp = call(dev, x.to(dev), u.to(dev), **kw)
+    q.sync_status()
+    T = float(np.float32(kw.get("T", 1.0)))
+    for r in range(0, 151, 3):
+        if r == 150:
+            assert int(tokens[r]) == -1
+            continue
+        w = kept_weights(x[r].float().numpy(), T, kw.get("top_k", 0), kw.get("top_p", 1.0), kw.get("min_p", 0.0))
+        c = np.cumsum(w)
+        assert int(tokens[r]) == int(np.searchsorted(c, np.float64(u[r]) * c[-1], side="right")), r
+
+
+@pytest.mark.parametrize("T", [1e-5, 3e-4, 1e-2])
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_sharp_temperatures_of_large_logits(dev, type, T):
+    """Logits so near each other, and so far from 0, that a step of the histogram is below one of theirs."""
+    rng = np.random.default_rng(3)
+    x = (100.0 + rng.integers(-40, 40, 9000) * 2.0 ** -17).astype(np.float32)
+    check(dev, x, type, T=T, top_p=0.9, most=100)
+    check(dev, x, type, T=T, top_k=500, top_p=0.7, most=100)
