@@ -396,6 +396,8 @@ class MatMulNBits:
         if size == 0:
             raise I8QError(_lib.ERR_UNSUPPORTED, "matmul_nbits_packed_size")
         self.packed = _workspace(size, B.device, stream)
+        if stream is not None:  # (belongs to that stream, and is read on others)
+            self.packed.record_stream(torch.cuda.current_stream())
         check(_L().i8q_matmul_nbits_pack(N, K, block_size, ptrs[0], ptrs[1], self._scale_type, ptrs[2],
                                          self.packed.data_ptr(), size, _stream(stream)), "matmul_nbits_pack")
         self._args = (self.packed.data_ptr(), size, N, K, block_size, self._scale_type, self._zero, ptrs[3])
@@ -413,6 +415,8 @@ class MatMulNBits:
         if (one != 1 and self.K > 1) or (also != 1 and self.N > 1):
             raise ValueError("A and Y must have contiguous rows")
         _on_current(A, "A")
+        if stream is not None:
+            self.packed.record_stream(stream)
         check(_L().i8q_matmul_nbits(A.data_ptr(), _float_type(A), A.shape[0], lda, *self._args, Y.data_ptr(), ldy,
                                     _stream(stream)), "matmul_nbits")
         return Y
