@@ -39,7 +39,8 @@ pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ sca
             uint8_t* __restrict__ packed) {
   kv::wait_previous_kernel();
   const int64_t blocks = (s.K + s.block - 1) / s.block;
-  const int64_t row_bytes = blocks * (s.block / 2), zero_bytes = (blocks + 1) / 2;
+  const int64_t row_bytes = blocks * (s.block / 2), zero_bytes = (blocks + 1) / 2;  // (rows of 8 bytes or more, all even)
+  const bool even = reinterpret_cast<uintptr_t>(B) % 2 == 0;
   for (int64_t tile = blockIdx.x; tile < s.strips * s.chunks; tile += gridDim.x) {
     const int64_t strip = tile / s.chunks, chunk = tile - strip * s.chunks;
     uint8_t* to = packed + tile * s.tile_bytes;
@@ -47,13 +48,18 @@ pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ sca
       const int b = threadIdx.x / 64, t = threadIdx.x % 4;
       const int64_t n = strip * kTileN + threadIdx.x / 4 % 16;
       uint32_t word = 0;
-      for (int st = 0; st < 2; ++st)
-        for (int j = 0; j < 4; ++j) {
-          const int64_t k = chunk * kTileK + 32 * b + 16 * st + 4 * t + j;
-          // past the matrix: code 0, which no activation or a scale of 0 meets
-          const uint32_t code = n < s.N && k < s.K ? B[n * row_bytes + k / 2] >> (4 * (k & 1)) & 15u : 0u;
-          word |= code << 4 * (st + 2 * (j / 2) + 4 * (j % 2));
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int64_t k = chunk * kTileK + 32 * b + 16 * st + 4 * t;
+        uint32_t four = 0;  // codes k .. k + 3; past the matrix 0, which no activation or a scale of 0 meets
+        if (n < s.N && k + 4 <= s.K && even) {
+          four = *reinterpret_cast<const uint16_t*>(B + n * row_bytes + k / 2);
+        } else {
+          for (int j = 0; j < 4; ++j)
+            if (n < s.N && k + j < s.K) four |= (B[n * row_bytes + (k + j) / 2] >> (4 * (j & 1)) & 15u) << 4 * j;
         }
+        word |= ((four & 15u) | (four >> 4 & 15u) << 16 | (four >> 8 & 15u) << 8 | (four >> 12) << 24) << 4 * st;
+      }
       reinterpret_cast<uint32_t*>(to)[threadIdx.x] = word;
     }
     for (int i = threadIdx.x; i < kTileN * s.per; i += blockDim.x) {

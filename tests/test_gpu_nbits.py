@@ -194,6 +194,16 @@ def test_values_near_each_other_cancel_exactly(dev):
     assert (Y == 21.0).all()
 
 
+def test_codes_at_an_odd_address(dev):
+    g = torch.Generator()
+    g.manual_seed(4)
+    B, s, z = weights(g, 50, 300, 32)
+    odd = torch.empty(B.numel() + 1, dtype=torch.uint8, device=dev)[1:]
+    odd.copy_(B.flatten())
+    a, b = (q.MatMulNBits(t, s.to(dev), 300, 32, zero_points=z.to(dev)) for t in (odd.view(B.shape), B.to(dev)))
+    assert torch.equal(a.packed, b.packed)
+
+
 def test_no_rows(dev):
     B, s, z = weights(gen(0), 20, 64, 32)
     m = q.MatMulNBits(B.to(dev), s.to(dev), 64, 32, zero_points=z.to(dev))
