@@ -361,6 +361,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
 // 128: 76 us, against 82 with 128 threads and 130 with 256).  The sums of two
 // products are scalar: the compiler fuses a paired sum with its products.
 constexpr int kUnitThreads = 64;
+// NORM: 16384 tokens of 40 normed rows of 128 123 us, without norms into the same
+// bf16 pages 76: 150 instructions more a lane and row.
 template <class T, bool S8, int L, bool NORM>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,

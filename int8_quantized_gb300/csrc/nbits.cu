@@ -170,6 +170,12 @@ struct Fragment<float> {
 // and enter the row's sum by a rounded fma with the block's scale (the pipe
 // cuts sums instead of rounding them; for fp32 activations only one step's 16
 // products are left to it).
+// Measured: 1 x 4096 -> 128000 63 us, 4.5 TB/s (the bytes take 42), 1 x 4096 ->
+// 14336 10 (4.5), 8 x 14336 -> 4096 16 (5.1).  Bound by issue slots, 178
+// instructions for the 2048 weights of a tile of which 88 turn codes into bf16,
+// and in short calls by the start and the strips' meetings.  More tiles of a
+// strip for each meeting pay (C 4 instead of 2 with all 16 warps along k: 63
+// and 75 us), more tiles on their way do not.
 template <class T, int NT, int C, int G, class ST>
 __global__ void __launch_bounds__(512, 1)
 nbits_kernel(const __grid_constant__ Args a) {
