@@ -218,6 +218,8 @@ sample_kernel(const __grid_constant__ Args a) {
   const int row = blockIdx.x / S, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const auto meet = [&] { S > 1 ? cluster.sync() : __syncthreads(); };
   kv::next_kernel_may_start();
+  // another CTA's memory may be written once that CTA has started: waited for before the first exchange
+  if (S > 1) cluster.barrier_arrive();
   for (int i = threadIdx.x; i <= kSteps; i += kThreads) sh.powers[i] = make_float2(g_powers.hi[i], g_powers.lo[i]);
   kv::wait_previous_kernel();
 
@@ -275,6 +277,7 @@ sample_kernel(const __grid_constant__ Args a) {
   for (int m = 1; m < 32; m <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
   if (lane == 0) sh.warp_sum[warp] = best;
   __syncthreads();
+  if (S > 1) cluster.barrier_wait();
   if (threadIdx.x < S) {
     for (int w = 0; w < kWarps; ++w) best = max(best, sh.warp_sum[w]);
     cluster.map_shared_rank(sh.best, threadIdx.x)[rank] = best;

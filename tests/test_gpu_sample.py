@@ -356,3 +356,26 @@ def test_sharp_temperatures_of_large_logits(dev, type, T):
     x = (100.0 + rng.integers(-40, 40, 9000) * 2.0 ** -17).astype(np.float32)
     check(dev, x, type, T=T, top_p=0.9, most=100)
     check(dev, x, type, T=T, top_k=500, top_p=0.7, most=100)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [8192, 8193, 16384, 20000, 32768, 33000])
+def test_the_shortest_shares_of_a_cluster(dev, V, type):
+    """2, 4 and 8 CTAs with 4096 tokens or few more each, call behind call: a
+    CTA may not hand its largest logit to one that has not started."""
+    R = 5
+    x = torch.from_numpy(logits_of(R * V, 2.0, V).reshape(R, V)).to(TYPES[type])
+    u = torch.from_numpy(np.random.default_rng(V).random(R).astype(np.float32))
+    T = torch.full((R,), 0.9)
+    T[3] = 0.0
+    want = []
+    for r in range(R):
+        w = kept_weights(x[r].float().numpy(), float(T[r]) or 1.0)
+        c = np.cumsum(w)
+        want.append(int(np.argmax(w)) if T[r] == 0 else int(np.searchsorted(c, np.float64(u[r]) * c[-1], side="right")))
+    x, u, T = x.to(dev), u.to(dev), T.to(dev)
+    tokens = torch.full((100, R), -7, dtype=torch.int32, device=dev)
+    for out in tokens:
+        q.sample(x, u, out, temperature=T)
+    q.sync_status()
+    assert (tokens.cpu() == torch.tensor(want, dtype=torch.int32)).all()
