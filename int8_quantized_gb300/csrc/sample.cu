@@ -79,7 +79,8 @@ __device__ __forceinline__ uint64_t weight(float x, const Scale& s, const float2
   constexpr float kC2 = (float)(kLn2 * kLn2 / 2), kC3 = (float)(kLn2 * kLn2 * kLn2 / 6);
   const float p1 = __fmul_rn(r, kLh);
   const float e1 = __fmaf_rn(r, kLl, __fmaf_rn(r, kLh, -p1));
-  const float t2 = __fmaf_rn(vl, kLh, __fmaf_rn(__fmul_rn(r, r), __fmaf_rn(r, kC3, kC2), e1));
+  // (2^(r + vl): vl, 2^-26 at most, meets 1 + r ln2)
+  const float t2 = __fmaf_rn(vl, __fmaf_rn(p1, kLh, kLh), __fmaf_rn(__fmul_rn(r, r), __fmaf_rn(r, kC3, kC2), e1));
   const float2 pw = powers[j + kSteps / 2];
   const float m = __fmul_rn(pw.x, p1);
   const float low = __fadd_rn(__fmaf_rn(pw.x, t2, __fmaf_rn(pw.x, p1, -m)), __fmaf_rn(pw.y, p1, pw.y));

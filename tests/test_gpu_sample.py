@@ -7,6 +7,7 @@ left out.  A kept set's border is met by a top_p or min_p that is 1e-9 from no
 prefix's share.  Log-probabilities: the logarithm of a ratio rounded thrice
 (3 2^-24) and of its own rounding, 2 units in its last place."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -379,3 +380,51 @@ def test_the_shortest_shares_of_a_cluster(dev, V, type):
         q.sample(x, u, out, temperature=T)
     q.sync_status()
     assert (tokens.cpu() == torch.tensor(want, dtype=torch.int32)).all()
+
+
+def weight_bounds(x, top, T):
+    """2^42 exp((x - top) / T), below and above by what fp64's exponential (2^-52) and its argument (60 2^-53) leave open."""
+    w = math.exp(float((Fraction(float(x)) - Fraction(float(top))) / Fraction(float(T)))) * 2.0 ** 42
+    slack = Fraction(w * 2.0 ** -46)
+    return Fraction(w) - slack, Fraction(w) + slack
+
+
+def check_weights(dev, T, top, depths, seed=0):
+    """A token's weight to one step of 2^-42, by whether the token is taken.
+
+    Of three tokens (x, the largest, z) of weights w, 2^42 and t the first is
+    taken where w > u (w + 2^42 + t).  For an fp32 u the logit z is the last
+    one by whose weight the first token has to be taken, or the first by which
+    it must not be, for every w and t less than 1 from their values."""
+    T, top, rng = np.float32(T), np.float32(top), np.random.default_rng(seed)
+    rows, want = [], []
+    for depth in depths:
+        x = np.float32(float(top) - depth * float(T))
+        if not (x < top and np.isfinite(x)):
+            continue
+        lo, hi = weight_bounds(x, top, T)
+        if lo < 8:
+            continue
+        # (a step of w moves the border by 1 / u - 1 of t, and u's own rounding by up to 2^19)
+        t = 2.0 ** 20 * (1 + rng.random()) + 2.0 ** 44 / float(lo)
+        u = np.float32(float(lo) / (float(lo) + 2.0 ** 42 + t))
+        U = Fraction(float(u))
+        sure = (lo - 1) * (1 - U) / U - 2 ** 42 - 1   # taken for all t up to this
+        never = (hi + 1) * (1 - U) / U - 2 ** 42 + 1  # ... and not from this on
+        for border, taken in ((sure, True), (never, False)):
+            z = np.float32(float(top) + math.log(float(border) / 2.0 ** 42) * float(T))
+            step = np.float32(-np.inf if taken else np.inf)
+            while (weight_bounds(z, top, T)[1] > border) if taken else (weight_bounds(z, top, T)[0] < border):
+                z = np.nextafter(z, step)
+            rows.append((x, top, z, u)), want.append(taken)
+    rows = torch.tensor(np.array(rows, np.float32))
+    assert len(want) > 100
+    tokens, _ = call(dev, rows[:, :3].contiguous().to(dev), rows[:, 3].contiguous().to(dev), T=float(T))
+    q.sync_status()
+    assert np.array_equal(tokens.cpu().numpy() == 0, np.array(want))
+
+
+@pytest.mark.parametrize("T,top", [(1.0, 0.0), (1.0, 20.0), (0.7, -3.0), (1e-3, 0.5), (50.0, 100.0), (2e9, 1e9)])
+def test_weights_are_off_by_less_than_their_step(dev, T, top):
+    rng = np.random.default_rng(int(T * 10))
+    check_weights(dev, T, top, np.concatenate((rng.uniform(0, 27, 800), rng.uniform(0, 2, 400), 10 ** rng.uniform(-6, 0, 100))))
