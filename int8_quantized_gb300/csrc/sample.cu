@@ -48,22 +48,31 @@ struct PowerTable {  // 2^(j / 512), j = -256 .. 256, in two parts
 __device__ const PowerTable g_powers = PowerTable();
 
 struct Scale {
-  float max, half;  // the row's largest logit and its half (halves: a difference does not overflow)
-  float ch, cl;     // 2 log2(e) / T in two parts
+  float max, part;  // the row's largest logit, and f times it
+  float minus;      // -f
+  float ch, cl;     // log2(e) / (f T) in two parts
 };
 
+// Differences are those of logits times f, a power of two: a half, so that
+// they do not overflow, but for a T by which log2(e) / (f T) would leave the
+// range in which fp32 holds both its parts, or the logits that T tells apart
+// have no half.  (A product with 2^60 that overflows is of a logit whose
+// neighbours lie many times T from it: they weigh nothing.  Products are
+// rounded before the sum: infinities of opposite signs give NaN, an infinity
+// of the wrong sign never comes.)
 __device__ __forceinline__ Scale make_scale(float max, float temperature) {
-  const double c = 2.0 / kLn2 / (double)temperature;
+  const float f = temperature > 0x1p60f ? 0x1p-61f : temperature < 0x1p-60f ? 0x1p60f : 0.5f;
+  const double c = 1.0 / kLn2 / (double)temperature / (double)f;
   const float ch = (float)c;
-  return Scale{max, 0.5f * max, ch, isinf(ch) ? 0.0f : (float)(c - (double)ch)};
+  return Scale{max, f * max, -f, ch, (float)(c - (double)ch)};
 }
 
 // powers: the table in shared memory.  0 for -infinity and NaN.
 __device__ __forceinline__ uint64_t weight(float x, const Scale& s, const float2* powers) {
   if (x == s.max) return kWhole;
-  const float xh = -0.5f * x;
-  const float h = __fadd_rn(s.half, xh), hv = __fsub_rn(h, s.half);
-  const float hl = __fadd_rn(__fsub_rn(s.half, __fsub_rn(h, hv)), __fsub_rn(xh, hv));
+  const float xh = __fmul_rn(s.minus, x);
+  const float h = __fadd_rn(s.part, xh), hv = __fsub_rn(h, s.part);
+  const float hl = __fadd_rn(__fsub_rn(s.part, __fsub_rn(h, hv)), __fsub_rn(xh, hv));
   const float p = __fmul_rn(h, s.ch);
   if (!(p >= 0.0f && p < 43.5f)) return 0;
   const float pl = __fmaf_rn(hl, s.ch, __fmaf_rn(h, s.cl, __fmaf_rn(h, s.ch, -p)));
@@ -397,7 +406,7 @@ sample_kernel(const __grid_constant__ Args a) {
   // digit has four to an octave, and a handful of addresses took all the adds
   // (32000 tokens: 8 us a histogram).
   auto step = [&](float y) {
-    const float d = y == scale.max ? 0.0f : __fmul_rn(__fadd_rn(scale.half, -0.5f * y), scale.ch);
+    const float d = y == scale.max ? 0.0f : __fmul_rn(__fadd_rn(scale.part, __fmul_rn(scale.minus, y)), scale.ch);
     return kBins - 1 - (d < 63.9f ? (int)(32.0f * d) : kBins - 1);  // (infinities and NaN: the last)
   };
   // After the first histogram: the key at which the sum from the top reaches target, and what is missing before it.
@@ -408,7 +417,7 @@ sample_kernel(const __grid_constant__ Args a) {
     // the keys of that bin, where they are few, brought together in each CTA
     // (a range that holds the bin, where T is not below what fp32 tells apart near the largest, spares most the step)
     const float wide = (float)kLn2 / 32.0f * temperature;
-    const bool plain = wide > 0x1p-18f * fabsf(scale.max) && wide < 1e30f && bin > 1;
+    const bool plain = wide > 0x1p-18f * fabsf(scale.max) && wide > 1e-30f && wide < 1e30f && bin > 1;
     const float least_y = plain ? scale.max - (float)(kBins + 1 - bin) * wide : -INFINITY;
     const float most_y = plain ? scale.max - (float)(kBins - 3 - bin) * wide : INFINITY;
     if (threadIdx.x == 0) sh.count = 0;  // (read by others before the last meeting, at the latest)

@@ -428,3 +428,29 @@ def check_weights(dev, T, top, depths, seed=0):
 def test_weights_are_off_by_less_than_their_step(dev, T, top):
     rng = np.random.default_rng(int(T * 10))
     check_weights(dev, T, top, np.concatenate((rng.uniform(0, 27, 800), rng.uniform(0, 2, 400), 10 ** rng.uniform(-6, 0, 100))))
+
+
+@pytest.mark.parametrize("T,top", [(1e37, 3e38), (1e37, 0.0), (2e18, 1e18), (1e-37, 0.0), (1e-38, 1e-36), (1e-39, 0.0), (1e-42, 0.0),
+                                   (5e-44, 1e-42), (1e-19, 1e-18), (9e-19, 0.0)])
+def test_weights_of_temperatures_at_the_ends_of_fp32(dev, T, top):
+    rng = np.random.default_rng(8)
+    check_weights(dev, T, top, np.concatenate((rng.uniform(0, 27, 800), rng.uniform(0, 2, 400))))
+
+
+@pytest.mark.parametrize("kw", [{}, dict(top_p=0.9), dict(top_k=900, top_p=0.9), dict(top_k=900, min_p=0.01)])
+@pytest.mark.parametrize("T", [1e-44, 1e-40, 1e-30, 8e-19, 1e-18, 2e18, 1e30, 3e38])
+def test_large_and_small_logits_at_any_temperature(dev, T, kw):
+    """Logits that T tells apart, and such as lie far beyond what it does, of either sign."""
+    z = logits_of(2500, seed=12).astype(np.float64)
+    few = dict(most=50, T=T, **kw)
+    x = np.clip(z * T, -3e38, 3e38)
+    check(dev, x, **few)
+    for far in (1e25, -1e25, 3e38, -1e38):
+        if abs(far) < 1e6 * T:
+            continue
+        y = x.copy()
+        y[::5] = far * (1 + np.arange(500) / 1000.0) if abs(far) < 1e38 else far
+        if far < 0:
+            y[1::5] = far
+        check(dev, y, **few)
+        check(dev, np.abs(y) * np.sign(far), **few)
