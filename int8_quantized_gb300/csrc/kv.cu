@@ -446,6 +446,7 @@ append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const i
   };
   auto normed = [&](float (&y)[8], const float (&w)[8]) {  // by all lanes of a row
     const float inverse = inverse_rms<L>(y, c.dim, norm.eps, lanes);
+    if (!in_row) return;  // (0 stays 0 where the factor is an infinity or a NaN: put() looks at all lanes)
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(y[j], inverse), w[j]);
   };

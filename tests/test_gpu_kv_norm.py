@@ -172,3 +172,40 @@ def test_refusals(dev):
         q.kv_append(c, table, seq, index, xk, xv, q_norm=good)
     torch.cuda.synchronize()
     assert torch.equal(c.k, before) and (out == 5.0).all()
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 112, 128, 144, 192])
+def test_a_key_that_is_not_finite_leaves_its_value_alone(dev, D, strided, type):
+    """Where a row has fewer elements than its lanes hold, the lanes past its
+    end take the norm's factor too: an infinity (a zero row, eps 0) or a NaN.
+    The values' codes and scales are those of the call without norms."""
+    T, Hq, H = 20, 4, 2
+    g = gen(D)
+    table, pages, _ = make_table(g, dev, [T], 16)
+    c, d = (make_cache(gen(7), dev, pages, H, 16, D, "s8") for _ in range(2))
+    x = torch.randn((T, Hq + 2 * H, D), generator=g)
+    x[0, :-H] = 0.0
+    x[1, :-H, 3] = float("nan")
+    x[2, :-H, D - 1] = float("inf")
+    x[3, :-H] = 1e-30
+    x[4] = 0.0
+    x = x.to(TYPES[type])
+    rows = torch.zeros((T, Hq + 2 * H, D + 3 * strided), dtype=x.dtype, device=dev)[..., 3 * strided:]
+    rows.copy_(x)
+    xq, xk, xv = rows.split((Hq, H, H), 1)
+    w = torch.full((D,), 0.5, device=dev)
+    seq, index = torch.zeros(T, dtype=torch.int32, device=dev), torch.arange(T, dtype=torch.int32, device=dev)
+    out = torch.empty((T, Hq, D), dtype=x.dtype, device=dev)
+    for which in (dict(k_norm=w), dict(q_norm=w, k_norm=w)):
+        q.kv_append(c, table, seq, index, xk, xv, q=xq, q_out=out, norm_eps=0.0, **which)
+        q.kv_append(d, table, seq, index, xk, xv, q=xq, q_out=torch.empty_like(out))
+        q.sync_status()
+        assert torch.isfinite(c.v_scale).all()
+        assert torch.equal(c.v, d.v) and torch.equal(c.v_scale, d.v_scale)
+        k_back, v_back = (torch.empty((T, H, D), device=dev) for _ in range(2))
+        q.kv_gather(c, table, seq, index, k_back, v_back)
+        most = x[:, -H:].float().abs().amax(-1, keepdim=True)
+        assert ((v_back.cpu() - x[:, -H:].float()).abs() <= 0.501 / 127 * most).all()
+        assert torch.isnan(k_back[1]).all()
