@@ -371,7 +371,10 @@ class MatMulNBits:
     codes to a byte; scales fp32 or bf16 [N, blocks] (or flat); zero_points
     uint8 [N, ceil(blocks / 2)] (or flat), two to a byte, or None (8); bias
     fp32 [N] or None.  The matrix is laid out once, here (on `stream`, or the
-    current one); afterwards B, scales and zero_points may go."""
+    current one); afterwards B, scales and zero_points may go, and after a
+    call the handle may: torch's allocator keeps their memory until the stream
+    that reads it is done.  A call on another stream than the matrix was laid
+    out on has to be ordered behind it by the caller."""
 
     def __init__(self, B, scales, K, block_size, zero_points=None, bias=None, stream=None):
         N, blocks = B.shape[0], -(-K // block_size)
@@ -396,10 +399,14 @@ class MatMulNBits:
         if size == 0:
             raise I8QError(_lib.ERR_UNSUPPORTED, "matmul_nbits_packed_size")
         self.packed = _workspace(size, B.device, stream)
-        if stream is not None:  # (belongs to that stream, and is read on others)
-            self.packed.record_stream(torch.cuda.current_stream())
+        self._read = (self.packed,) if bias is None else (self.packed, bias)  # by the calls
+        self._streams = set()
         check(_L().i8q_matmul_nbits_pack(N, K, block_size, ptrs[0], ptrs[1], self._scale_type, ptrs[2],
                                          self.packed.data_ptr(), size, _stream(stream)), "matmul_nbits_pack")
+        used = torch.cuda.current_stream() if stream is None else stream
+        for t in (B, scales, zero_points):
+            if t is not None:
+                t.record_stream(used)
         self._args = (self.packed.data_ptr(), size, N, K, block_size, self._scale_type, self._zero, ptrs[3])
 
     def forward(self, A, Y, stream=None):
@@ -415,10 +422,13 @@ class MatMulNBits:
         if (one != 1 and self.K > 1) or (also != 1 and self.N > 1):
             raise ValueError("A and Y must have contiguous rows")
         _on_current(A, "A")
-        if stream is not None:
-            self.packed.record_stream(stream)
-        check(_L().i8q_matmul_nbits(A.data_ptr(), _float_type(A), A.shape[0], lda, *self._args, Y.data_ptr(), ldy,
-                                    _stream(stream)), "matmul_nbits")
+        on = _stream(stream)
+        check(_L().i8q_matmul_nbits(A.data_ptr(), _float_type(A), A.shape[0], lda, *self._args, Y.data_ptr(), ldy, on),
+              "matmul_nbits")
+        if on.value not in self._streams:  # (once is enough: a block keeps the streams that read it)
+            self._streams.add(on.value)
+            for t in self._read:
+                t.record_stream(torch.cuda.current_stream() if stream is None else stream)
         return Y
 
 
