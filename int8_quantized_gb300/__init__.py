@@ -592,7 +592,7 @@ def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions
     rot = None
     if cos is not None:
         rot = ctypes.byref(_rotary(positions, cos, sin, pair_axis, interleaved, tokens))
-    norm = None if q_norm is None and k_norm is None else ctypes.byref(_head_norm(q_norm, k_norm, norm_eps, D))
+    norm = None if q_norm is None and k_norm is None else ctypes.byref(_head_norm(q_norm, k_norm, norm_eps, D, k.device))
     qs, qo, heads = (None, 0, 0), (None, 0, 0), 0
     if q is not None:
         heads = q.shape[1]
@@ -604,19 +604,22 @@ def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions
     return q_out
 
 
-def _head_norm(q_norm, k_norm, eps, dim):
+def _head_norm(q_norm, k_norm, eps, dim, device):
     dtypes = set()
     for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is None:
             continue
         if not isinstance(t, _Tensor) or not t.is_cuda or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous CUDA tensor")
+        if t.device != device:
+            raise TypeError(f"{name} must be a tensor beside k")
         if t.shape != (dim,):
             raise ValueError(f"{name} must be [{dim}]")
         dtypes.add(t.dtype)
         kind = _float_type(t)
     if len(dtypes) > 1:
         raise TypeError("q_norm and k_norm must have one dtype")
+    _on_current(q_norm if k_norm is None else k_norm, "k")  # (beside which both lie)
     return _lib.HeadNormStruct(*(None if t is None else t.data_ptr() for t in (q_norm, k_norm)), kind, eps)
 
 

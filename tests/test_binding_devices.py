@@ -38,3 +38,21 @@ def test_sample_settings_beside_the_logits(second, monkeypatch):
     x, t = second(torch.zeros((2, 50))), second(torch.zeros(2, dtype=torch.int32))
     with pytest.raises(TypeError, match="temperature must be"):
         q.sample(x, second(torch.zeros(2)), t, temperature=on(torch.zeros(2), torch.device("cuda:0")))
+
+
+@pytest.mark.parametrize("name", ["q_norm", "k_norm"])
+def test_norms_of_the_heads(second, monkeypatch, name):
+    cache = type("Cache", (), {"_ref": None, "shape": (1, 1, 16, 64)})()
+    i, x, w = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 1, 64)), torch.ones(64)
+
+    def call(place, norm):
+        to = lambda t: on(t, torch.device(place))
+        q.kv_append(cache, to(torch.zeros((1, 1), dtype=torch.int32)), to(i), to(i), to(x), to(x), q=to(x), q_out=to(x.clone()),
+                    **{name: norm})
+
+    with pytest.raises(TypeError, match=f"{name} must be a tensor beside k"):
+        call("cuda:0", second(w))
+    with pytest.raises(ValueError, match="not the current device"):
+        call("cuda:1", second(w))
+    with pytest.raises(AssertionError, match="the library was called"):
+        call("cuda:0", on(w, torch.device("cuda:0")))
