@@ -572,7 +572,7 @@ def _rotary(positions, cos, sin, pair_axis, interleaved, tokens):
 
 
 def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions=None, cos=None, sin=None,
-              pair_axis=None, interleaved=False, q_norm=None, k_norm=None, norm_eps=1e-6, stream=None):
+              pair_axis=None, interleaved=False, stream=None, q_norm=None, k_norm=None, norm_eps=1e-6):
     """Write tokens into the cache: token t becomes token index[t] of
     sequence seq[t] (int32; seq < 0: left out).  k, v [tokens, kv_heads,
     head_dim] fp32 or bf16, any token and head strides; q, q_out [tokens,

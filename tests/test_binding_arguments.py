@@ -159,3 +159,22 @@ def test_cache_with_an_axis_of_one_place(dev, axis, cache):
     q.sync_status()
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_kv_append_takes_its_stream_where_it_did(monkeypatch):
+    """The norms came after the stream's place."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args[-2:])) or 0
+
+    monkeypatch.setattr(q, "_L", lambda: Library())
+    monkeypatch.setattr(q, "_page_table", lambda t, *a: q._lib.PageTableStruct())
+    monkeypatch.setattr(q, "_rows", lambda *a: (None, 0, 0))
+    monkeypatch.setattr(q, "_i32", lambda *a: None)
+    monkeypatch.setattr(q, "_stream", lambda s=None: s)
+    cache = type("Cache", (), {"_ref": None, "shape": (1, 1, 16, 64)})()
+    k = torch.zeros((2, 1, 64))
+    q.kv_append(cache, None, None, None, k, k, None, None, None, None, None, None, False, "side")
+    assert seen == [("i8q_kv_append_norm", (None, "side"))]
