@@ -413,10 +413,13 @@ int i8q_matmul_nbits_pack(int64_t N, int64_t K, int64_t block_size, const uint8_
  * few rows: it reads the matrix again for every 64 of bf16 (8 where A is not
  * 16-byte aligned or lda no multiple of 8), and for every 8 of fp32.
  * Weights and activations enter the products exactly (fp32 activations in
- * three parts of 8 bits), a block's products are summed by the tensor pipe
- * (for fp32, 16 of them) and blocks in fp32, rounded; the order does not
- * depend on the run.  Y is rounded once at the end.  A row that holds an
- * infinity or a NaN gives such values in that row alone.  No workspace.
+ * three parts of 8 bits; what of one lies below 2^-133 is cut off), a block's
+ * products are summed by the tensor pipe (for fp32, 16 of them) and blocks in
+ * fp32, rounded; the order does not depend on the run.  Sums are held at 2^-12
+ * of their value: neither a block's products before their scale nor a row's
+ * sum on its way leave fp32's range where Y does not, and what of a row's sum
+ * lies below 2^-137 is lost.  Y is rounded once at the end.  A row that holds
+ * an infinity or a NaN gives such values in that row alone.  No workspace.
  * Errors: INVALID_ARG, UNSUPPORTED (block_size), CUDA. */
 int i8q_matmul_nbits(const void* A, int type, int64_t M, int64_t lda, const void* packed, size_t packed_bytes, int64_t N,
                      int64_t K, int64_t block_size, int scale_type, int has_zero, const float* bias, void* Y, int64_t ldy,

@@ -96,15 +96,6 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
 
-// Two codes at nibbles 0 and 4 of w as bf16 numbers less their zero point:
-// 0x43 over a byte c < 128 is 128 + c, and 128 + z is subtracted exactly.
-__device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t zero) {
-  uint32_t v, r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
-  return r;
-}
-
 // A fragment of activations: four neighbours of row m from k on, as bf16
 // pairs; fp32 in three parts of 8 bits cut off one after the other, which are
 // all of its 24 (an infinity or a NaN in the first part alone).
@@ -274,7 +265,8 @@ nbits_kernel(const __grid_constant__ Args a) {
     for (int st = 0; st < 8; ++st) {
       const int i = st * 16 / G;
       const uint32_t v0 = w0[st / 2] >> (4 * (st & 1)), v1 = w1[st / 2] >> (4 * (st & 1));
-      const uint32_t f[4] = {pair(v0, z0.pair(i)), pair(v1, z1.pair(i)), pair(v0 >> 8, z0.pair(i)), pair(v1 >> 8, z1.pair(i))};
+      const uint32_t f[4] = {code_pair(v0, z0.pair(i)), code_pair(v1, z1.pair(i)), code_pair(v0 >> 8, z0.pair(i)),
+                             code_pair(v1 >> 8, z1.pair(i))};
       const bool first = kParts > 1 || st * 16 % G == 0, last = kParts > 1 || (st + 1) * 16 % G == 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -300,6 +292,7 @@ nbits_kernel(const __grid_constant__ Args a) {
     const int m = rows0 + e / 16;
     const int64_t n = ((int64_t)(c0 + group * a.clusters) * a.wf + strip) * kTileN + e % 16;
     if (n >= a.s.N) return;
+    v = __fmul_rn(v, kUnit);
     if (a.bias) v = __fadd_rn(v, a.bias[n]);
     store(Y + (int64_t)m * a.ldy + n, v);
   };

@@ -83,10 +83,25 @@ struct Row {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
     else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
-  __device__ __forceinline__ uint32_t pair(int i) const {  // 128 + zero point twice, as bf16
-    return __byte_perm(w[i / 4], 0x43434343u, 0x4040u + (i & 3) * 0x0101u);
+  __device__ __forceinline__ uint32_t pair(int i) const {  // a zero point twice, as code_pair() takes it
+    return __byte_perm(w[i / 4], 0x3d3d3d3du, 0x4040u + (i & 3) * 0x0101u);
   }
 };
+
+// Codes enter the products as bf16 numbers of 2^-12, and sums keep that unit:
+// a block's products of the largest activations (128 of them, by up to 15)
+// stay within fp32, however small its scale.
+constexpr float kUnit = 4096.0f;
+
+// Two codes at nibbles 0 and 4 of w as bf16 numbers less their zero point:
+// 0x3d over a byte c < 128 is 2^-5 + c 2^-12, and the zero point's number is
+// subtracted exactly.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x3d003d00, 0xea;" : "=r"(v) : "r"(w));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+  return r;
+}
 
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }

@@ -95,13 +95,6 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {  // as nbits.cu's pair()
-  uint32_t v, r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
-  return r;
-}
-
 // A cluster has a unit (a tile of outputs by a tile of rows) at a time, its
 // CTAs a share of k each; their sums meet in shared memory, each CTA adding up
 // and writing a share of the rows.
@@ -292,6 +285,7 @@ tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TcArg
       __nv_bfloat16* const Y = static_cast<__nv_bfloat16*>(a.Y) + n;
       const float bias = a.bias && n < a.s.N ? a.bias[n] : 0.0f;
       auto put = [&](int m, float v) {
+        v = __fmul_rn(v, kUnit);
         if (row0 + m < a.M && n < a.s.N) store(Y + (int64_t)(row0 + m) * a.ldy, a.bias ? __fadd_rn(v, bias) : v);
       };
       if (S == 1) {

@@ -267,3 +267,70 @@ def test_refusals(dev):
             m.forward(a, y)
     torch.cuda.synchronize()
     assert (Y == 5.0).all()
+
+
+def products(dev, A, B, s, z, K, block, bias=None):
+    """Y and, in 64 bits, what it should be and the sum of its terms' sizes."""
+    up = lambda t: None if t is None else t.to(dev)
+    m = q.MatMulNBits(up(B), up(s), K, block, zero_points=up(z), bias=up(bias))
+    Y = torch.empty((A.shape[0], B.shape[0]), dtype=A.dtype, device=dev)
+    m.forward(A.to(dev), Y)
+    q.sync_status()
+    w, sc = dense(B, s, z, K, block)
+    want = A.double() @ (w * sc).t() + (0 if bias is None else bias.double())
+    return Y.cpu().double(), want, A.double().abs() @ (w * sc).abs().t()
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 40, 70])
+@pytest.mark.parametrize("block", [16, 128, 256])
+@pytest.mark.parametrize("type,scales", [("bf16", "bf16"), ("f32", "f32")])
+def test_products_beyond_fp32_before_their_scale(dev, M, block, type, scales):
+    """Activations as large as the type has them: a block's products pass fp32's range, Y does not."""
+    g = gen(M)
+    N, K = 70, 700
+    B, s, z = weights(g, N, K, block, scales)
+    A = ((torch.rand((M, K), generator=g) * 0.5 + 0.5) * torch.randint(0, 2, (M, K), generator=g).mul(2).sub(1))
+    A = (A.double() * torch.finfo(TYPES[type]).max).to(TYPES[type])
+    A[0] = torch.finfo(TYPES[type]).max
+    bias = torch.randn((N,), generator=g) * 1e33
+    s = (s.float() * 2.0 ** -12).to(s.dtype)
+    got, want, size = products(dev, A, B, s, z, K, block, bias)
+    assert want.abs().max() < 3e38 and torch.isfinite(A).all()
+    tol = tolerance(size, want, K, block, type, bias)
+    assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("share", [1.0, 0.5])
+@pytest.mark.parametrize("M", [2, 20])
+@pytest.mark.parametrize("type", ["bf16", "f32"])
+def test_a_sum_beyond_fp32_on_its_way(dev, M, type, share):
+    K, block = 256, 32
+    B = torch.full((16, K // block, block // 2), 0xFF, dtype=torch.uint8)  # 7 after the zero point
+    B[:, 4:] = 0x11                                                       # -7
+    B[:, 7, 0] = 0x12                                                     # and one of -6
+    A = torch.full((M, K), torch.finfo(TYPES[type]).max * share).to(TYPES[type])
+    got, want, size = products(dev, A, B, torch.ones((16, K // block)), None, K, block)
+    assert (want == A[0, 0].double()).all()
+    tol = tolerance(size, want, K, block, type, None)
+    # (the tolerance is that of the sum before its rounding to the type: Y = fp32's largest number, plus a part of the
+    # 1792 times as large sum of the terms' sizes, may round to an infinity; half of it, off by 0.007 of it, may not)
+    beyond = torch.isposinf(got) & (want + tol > torch.finfo(torch.float32).max)
+    assert not beyond.any() or (type, share) == ("f32", 1.0)
+    assert ((got - want).abs().le(tol) | beyond).all()
+
+
+@pytest.mark.parametrize("M", [3, 20])
+@pytest.mark.parametrize("type", ["bf16", "f32"])
+def test_smallest_activations_and_largest_scales(dev, M, type):
+    """Subnormal activations, whole multiples of 2^-133, by scales of 2^90; what of a row's sum lies below 2^-137 (of
+    its blocks' and warps' parts: (K / 16 + 32) of them) is lost."""
+    g = gen(M)
+    N, K, block = 40, 400, 32
+    B, s, z = weights(g, N, K, block, "f32")
+    A = torch.randint(-3000, 3001, (M, K), generator=g).double() * 2.0 ** -133
+    A = A.to(TYPES[type])
+    got, want, size = products(dev, A, B, s * 2.0 ** 90, z, K, block)
+    assert want.abs().max() > 0 and ((got - want).abs() <= tolerance(size, want, K, block, type, None)).all()
+    got, want, size = products(dev, A, B, s, z, K, block)
+    tol = tolerance(size, want, K, block, type, None) - 1e-37 + (K / 16 + 32) * 2.0 ** -137
+    assert ((got - want).abs() <= tol + (2.0 ** -133 if type == "bf16" else 2.0 ** -149)).all()
