@@ -334,3 +334,16 @@ def test_smallest_activations_and_largest_scales(dev, M, type):
     got, want, size = products(dev, A, B, s, z, K, block)
     tol = tolerance(size, want, K, block, type, None) - 1e-37 + (K / 16 + 32) * 2.0 ** -137
     assert ((got - want).abs() <= tol + (2.0 ** -133 if type == "bf16" else 2.0 ** -149)).all()
+
+
+@pytest.mark.parametrize("type,M,K,ctas,rounds", [("f32", 3, 4096, 2, 17), ("f32", 40, 4096, 2, 33), ("bf16", 40, 14336, 2, 17),
+                                                  ("bf16", 20, 14336, 2, 35), ("bf16", 30, 33000, 8, 18), ("f32", 24, 33000, 8, 33),
+                                                  ("bf16", 33, 70000, 8, 17)])
+def test_more_strips_than_a_cluster_joins_at_once(dev, type, M, K, ctas, rounds):
+    """A cluster's CTAs hold the sums of 16 groups of strips between two
+    meetings; these have 17 to 35, so that what they hold is written anew.
+    (Rows of bf16 at an odd place go 8 at a time, as fp32's do, and each 8 have
+    a share of the clusters.)"""
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    clusters = sms // ctas // -(-M // 8)
+    check(dev, M, 16 * ((rounds - 1) * clusters + clusters // 2 + 1) - 3, K, 128, type, offset=1, pad=2, seed=rounds)
