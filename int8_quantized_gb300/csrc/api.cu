@@ -72,19 +72,29 @@ int smem_attr(const void* func, int bytes) {
   }, &a);
 }
 
+// 256 zeros.  The call that needs them may be a captured one, whose stream's
+// capture an allocation and a copy on the default stream would end: the
+// allocation is made in the thread's relaxed mode, the zeros are written on a
+// stream of their own.
+static uint32_t* zeroed() {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+  uint32_t* p = nullptr;
+  cudaStream_t s = nullptr;
+  bool ok = cudaMalloc(&p, 256) == cudaSuccess;
+  ok = ok && cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+  ok = ok && cudaMemsetAsync(p, 0, 256, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  if (s) cudaStreamDestroy(s);
+  if (!ok && p) cudaFree(p), p = nullptr;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return p;
+}
+
 uint32_t* device_status_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_dev_mu);
-  if (!g_status[dev]) {
-    uint32_t* p = nullptr;
-    if (cudaMalloc(&p, 256) != cudaSuccess) return nullptr;
-    if (cudaMemset(p, 0, 256) != cudaSuccess) {
-      cudaFree(p);
-      return nullptr;
-    }
-    g_status[dev] = p;
-  }
+  if (!g_status[dev]) g_status[dev] = zeroed();
   return g_status[dev];
 }
 
