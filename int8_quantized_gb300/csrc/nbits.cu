@@ -37,7 +37,6 @@ int check_shape(int64_t N, int64_t K, int64_t block, int scale_type, bool has_ze
 __global__ void __launch_bounds__(256)
 pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ scales, const uint8_t* __restrict__ zeros,
             uint8_t* __restrict__ packed) {
-  kv::wait_previous_kernel();
   const int64_t blocks = (s.K + s.block - 1) / s.block;
   const int64_t row_bytes = blocks * (s.block / 2), zero_bytes = (blocks + 1) / 2;  // (rows of 8 bytes or more, all even)
   const bool even = reinterpret_cast<uintptr_t>(B) % 2 == 0;
@@ -75,6 +74,8 @@ pack_kernel(Shape s, const uint8_t* __restrict__ B, const void* __restrict__ sca
     }
   }
 }
+
+constexpr int kRows = 8, kOut = kRows * kTileN;  // of a product, and its outputs
 
 // A warp's ring: stages of its tiles of one strip (or of one tile, where it
 // has no fixed number of them), one of which is read while the others arrive.
@@ -156,7 +157,7 @@ struct Fragment<float> {
 // and streams the tiles of one strip of 16 outputs after the other through a
 // ring of its own in shared memory, each lane copying what it will read.  The
 // warps of a strip add their sums up in shared memory, those of a cluster's
-// CTAs through it.  NT: tiles of 8 rows.  G: the block, at most 128.  S: the
+// CTAs through it.  Rows: 8 at a time.  G: the block, at most 128.  ST: the
 // scales' type.  The products of a block are summed by the tensor pipe from 0
 // and enter the row's sum by a rounded fma with the block's scale (the pipe
 // cuts sums instead of rounding them; for fp32 activations only one step's 16
@@ -167,17 +168,17 @@ struct Fragment<float> {
 // and in short calls by the start and the strips' meetings.  More tiles of a
 // strip for each meeting pay (C 4 instead of 2 with all 16 warps along k: 63
 // and 75 us), more tiles on their way do not.
-template <class T, int NT, int C, int G, class ST>
+template <class T, int C, int G, class ST>
 __global__ void __launch_bounds__(512, 1)
 nbits_kernel(const __grid_constant__ Args a) {
-  constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G, kOut = NT * 128;
+  constexpr int kParts = Fragment<T>::kParts, kPer = kTileK / G;
   constexpr int kStages = stages(C), kTiles = stage_tiles(C);
   extern __shared__ __align__(16) uint8_t smem[];
   const int S = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane & 3;
   const int wk = warp % a.wk, wf = warp / a.wk;
-  const int cluster = blockIdx.x / S, rows0 = cluster / a.clusters * (8 * NT), c0 = cluster % a.clusters;
-  const int rows = min(8 * NT, a.M - rows0);
+  const int cluster = blockIdx.x / S, rows0 = cluster / a.clusters * kRows, c0 = cluster % a.clusters;
+  const int rows = min(kRows, a.M - rows0);
   const int chunks = (int)a.s.chunks, strips = (int)a.s.strips, tile_bytes = a.s.tile_bytes;
   const int parts = a.wk * S, part = rank * a.wk + wk;
   const int c_begin = (int)((int64_t)part * chunks / parts), cw = (int)((int64_t)(part + 1) * chunks / parts) - c_begin;
@@ -223,16 +224,12 @@ nbits_kernel(const __grid_constant__ Args a) {
   for (int i = 0; i < kStages - 1; ++i) send();
 
   const T* const A = static_cast<const T*>(a.A);
-  Fragment<T> x[C ? C : 1][8][NT];
+  Fragment<T> x[C ? C : 1][8];
   auto load_x = [&](int slot, int c) {
 #pragma unroll
     for (int st = 0; st < 8; ++st)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int m = nt * 8 + g;
-        x[slot][st][nt].load(A + (int64_t)(rows0 + m) * a.lda, (c_begin + c) * kTileK + st * 16 + 4 * t, (int)a.s.K,
-                             c < cw && m < rows, a.a_aligned);
-      }
+      x[slot][st].load(A + (int64_t)(rows0 + g) * a.lda, (c_begin + c) * kTileK + st * 16 + 4 * t, (int)a.s.K,
+                       c < cw && g < rows, a.a_aligned);
   };
 #pragma unroll
   for (int c = 0; c < C; ++c) load_x(c, c);
@@ -247,7 +244,7 @@ nbits_kernel(const __grid_constant__ Args a) {
     __syncwarp();  // the scales and zero points were copied by other lanes, and all have read the stage before
     send();
   };
-  auto tile = [&](const Fragment<T> (&xc)[8][NT], const uint8_t* at, float (&y)[NT][4]) {
+  auto tile = [&](const Fragment<T> (&xc)[8], const uint8_t* at, float (&y)[4]) {
     uint32_t w0[4], w1[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -260,7 +257,7 @@ nbits_kernel(const __grid_constant__ Args a) {
       z0 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g);
       z1 = Row<uint8_t, kPer>(at + kCodeBytes + kTileN * kPer * sizeof(ST), g + 8);
     }
-    float acc[NT][4];
+    float acc[4];
 #pragma unroll
     for (int st = 0; st < 8; ++st) {
       const int i = st * 16 / G;
@@ -269,20 +266,14 @@ nbits_kernel(const __grid_constant__ Args a) {
                              code_pair(v1 >> 8, z1.pair(i))};
       const bool first = kParts > 1 || st * 16 % G == 0, last = kParts > 1 || (st + 1) * 16 % G == 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int p = kParts - 1; p >= 0; --p) {
-          if (first && p == kParts - 1) mma_first(acc[nt], f, xc[st][nt].b[p]);
-          else mma(acc[nt], f, xc[st][nt].b[p]);
-        }
+      for (int p = kParts - 1; p >= 0; --p) {
+        if (first && p == kParts - 1) mma_first(acc, f, xc[st].b[p]);
+        else mma(acc, f, xc[st].b[p]);
       }
       if (last) {
         const float u0 = s0.value(i), u1 = s1.value(i);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          y[nt][0] = __fmaf_rn(acc[nt][0], u0, y[nt][0]), y[nt][1] = __fmaf_rn(acc[nt][1], u0, y[nt][1]);
-          y[nt][2] = __fmaf_rn(acc[nt][2], u1, y[nt][2]), y[nt][3] = __fmaf_rn(acc[nt][3], u1, y[nt][3]);
-        }
+        y[0] = __fmaf_rn(acc[0], u0, y[0]), y[1] = __fmaf_rn(acc[1], u0, y[1]);
+        y[2] = __fmaf_rn(acc[2], u1, y[2]), y[3] = __fmaf_rn(acc[3], u1, y[3]);
       }
     }
   };
@@ -298,7 +289,7 @@ nbits_kernel(const __grid_constant__ Args a) {
   };
 
   for (int gi = 0; gi < ng; ++gi) {
-    float y[NT][4] = {};
+    float y[4] = {};
     if (gi < live) {
       arrived();
       if constexpr (C > 0) {
@@ -317,14 +308,11 @@ nbits_kernel(const __grid_constant__ Args a) {
     }
     // the sums of a strip's warps, two buffers in turn
     float* const mine = partial + ((gi & 1) * a.wf + wf) * a.wk * kOut;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (nt * 8 + 2 * t < rows)
-        *reinterpret_cast<float4*>(mine + wk * kOut + nt * 128 + lane * 4) = make_float4(y[nt][0], y[nt][1], y[nt][2], y[nt][3]);
+    if (2 * t < rows) *reinterpret_cast<float4*>(mine + wk * kOut + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
     asm volatile("bar.sync %0, %1;\n" ::"r"(wf), "r"(a.wk * 32) : "memory");
     for (int e = wk * 32 + lane; e < rows * 16; e += a.wk * 32) {
       const int m = e / 16, f = e % 16;
-      const float* p = mine + m / 8 * 128 + ((f & 7) * 4 + (m & 7) / 2) * 4 + (m & 1) + 2 * (f / 8);
+      const float* p = mine + ((f & 7) * 4 + m / 2) * 4 + (m & 1) + 2 * (f / 8);
       float v = 0.0f;
 #pragma unroll 4
       for (int w = 0; w < a.wk; ++w) v = __fadd_rn(v, p[w * kOut]);
@@ -345,12 +333,12 @@ nbits_kernel(const __grid_constant__ Args a) {
   }
 }
 
-template <class T, int NT, int C>
+template <class T, int C>
 int run_block(Args& a, int S, cudaStream_t s) {
   const int warps = a.wk * a.wf;
-  const int64_t row_tiles = ceil_div(a.M, 8 * NT), groups = ceil_div(a.s.strips, a.wf);
+  const int64_t row_tiles = ceil_div(a.M, kRows), groups = ceil_div(a.s.strips, a.wf);
   a.clusters = (int)std::min<int64_t>(groups, std::max<int64_t>(1, sm_count() / S / row_tiles));
-  const int smem = warps * stages(C) * stage_tiles(C) * a.s.tile_bytes + 2 * warps * NT * 512 + (S > 1 ? kRound * a.wf * NT * 512 : 0);
+  const int smem = warps * stages(C) * stage_tiles(C) * a.s.tile_bytes + 2 * warps * kOut * 4 + (S > 1 ? kRound * a.wf * kOut * 4 : 0);
   if (row_tiles * a.clusters * S > INT32_MAX) return fail(I8Q_ERR_INVALID_ARG, "matmul_nbits: too many rows");
   auto run = [&](auto kernel) {
     return kv::launch(kernel, (unsigned)(row_tiles * a.clusters * S), 32 * warps, smem, S, s, "matmul_nbits", a);
@@ -358,10 +346,10 @@ int run_block(Args& a, int S, cudaStream_t s) {
   auto scaled = [&](auto scale) {
     using ST = decltype(scale);
     switch (a.s.per) {
-      case 8: return run(nbits_kernel<T, NT, C, 16, ST>);
-      case 4: return run(nbits_kernel<T, NT, C, 32, ST>);
-      case 2: return run(nbits_kernel<T, NT, C, 64, ST>);
-      default: return run(nbits_kernel<T, NT, C, 128, ST>);
+      case 8: return run(nbits_kernel<T, C, 16, ST>);
+      case 4: return run(nbits_kernel<T, C, 32, ST>);
+      case 2: return run(nbits_kernel<T, C, 64, ST>);
+      default: return run(nbits_kernel<T, C, 128, ST>);
     }
   };
   return a.s.scale_size == 4 ? scaled(float()) : scaled(__nv_bfloat16());
@@ -383,10 +371,10 @@ int run_product(Args& a, int type, cudaStream_t s) {
   while (S < kMostCtas && a.s.strips * S * 2 <= sm_count() && chunks >= (int64_t)kWarps * S * 2) S *= 2;
   if (S > 1) a.wf = 1;
   const bool held = share() <= room;
-  if (type == I8Q_F32) return held ? run_block<float, 1, 1>(a, S, s) : run_block<float, 1, 0>(a, S, s);
+  if (type == I8Q_F32) return held ? run_block<float, 1>(a, S, s) : run_block<float, 0>(a, S, s);
   using B = __nv_bfloat16;
-  if (!held) return run_block<B, 1, 0>(a, S, s);
-  return share() <= 2 ? run_block<B, 1, 2>(a, S, s) : run_block<B, 1, 4>(a, S, s);
+  if (!held) return run_block<B, 0>(a, S, s);
+  return share() <= 2 ? run_block<B, 2>(a, S, s) : run_block<B, 4>(a, S, s);
 }
 
 }  // namespace

@@ -106,8 +106,8 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The products of bf16 activations on the tcgen05 pipe (nbits_tc.cu): whether
-// TMA can read them, and the launch.
+// The products of several rows of bf16 activations on the tcgen05 pipe
+// (nbits_tc.cu): whether TMA can read them, and the launch.
 bool tc_takes(const Args& a);
 int run_tc(Args& a, cudaStream_t stream);
 

@@ -444,7 +444,7 @@ int run_form(TcArgs& t, const CUtensorMap& map, cudaStream_t s) {
 }  // namespace
 
 bool tc_takes(const Args& a) {
-  return reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && (a.M == 1 || a.lda % 8 == 0) && a.lda <= (1LL << 36);
+  return reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && a.lda % 8 == 0 && a.lda <= (1LL << 36);
 }
 
 int run_tc(Args& a, cudaStream_t s) {
@@ -456,7 +456,7 @@ int run_tc(Args& a, cudaStream_t s) {
   t.units = (int)units, t.tiles = (int)tiles;
   CUtensorMap map;
   const cuuint64_t dims[2] = {(cuuint64_t)a.s.K, (cuuint64_t)a.M};
-  const cuuint64_t strides[1] = {(cuuint64_t)(a.M == 1 ? round_up(a.s.K, 8) : a.lda) * 2};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.lda * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)rows};
   const int rc = make_tensor_map(&map, a.A, 2, dims, strides, box, "matmul_nbits");
   if (rc != I8Q_OK) return rc;
