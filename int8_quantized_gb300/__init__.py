@@ -605,9 +605,10 @@ def kv_append(cache, page_table, seq, index, k, v, q=None, q_out=None, positions
 
 
 def _head_norm(q_norm, k_norm, eps, dim, device):
-    dtypes = set()
+    pointers, some = [], None
     for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is None:
+            pointers.append(None)
             continue
         if not isinstance(t, _Tensor) or not t.is_cuda or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous CUDA tensor")
@@ -615,12 +616,13 @@ def _head_norm(q_norm, k_norm, eps, dim, device):
             raise TypeError(f"{name} must be a tensor beside k")
         if t.shape != (dim,):
             raise ValueError(f"{name} must be [{dim}]")
-        dtypes.add(t.dtype)
-        kind = _float_type(t)
-    if len(dtypes) > 1:
-        raise TypeError("q_norm and k_norm must have one dtype")
-    _on_current(q_norm if k_norm is None else k_norm, "k")  # (beside which both lie)
-    return _lib.HeadNormStruct(*(None if t is None else t.data_ptr() for t in (q_norm, k_norm)), kind, eps)
+        if some is not None and t.dtype is not some.dtype:
+            raise TypeError("q_norm and k_norm must have one dtype")
+        some = t
+        pointers.append(t.data_ptr())
+    if device.index != torch.cuda.current_device():  # (on which the kernel runs)
+        raise ValueError(f"k lies on {device}, which is not the current device")
+    return _lib.HeadNormStruct(*pointers, _float_type(some), eps)
 
 
 def _float_type(t):
