@@ -377,6 +377,8 @@ class MatMulNBits:
     out on has to be ordered behind it by the caller."""
 
     def __init__(self, B, scales, K, block_size, zero_points=None, bias=None, stream=None):
+        if K < 1 or block_size < 1 or B.dim() < 1:
+            raise ValueError("K and block_size must be 1 or more, B a row of blocks for each output")
         N, blocks = B.shape[0], -(-K // block_size)
         if B.dtype != torch.uint8 or B.numel() != N * blocks * (block_size // 2):
             raise ValueError(f"B must be uint8 [{N}, {blocks}, {block_size // 2}]")
@@ -396,8 +398,9 @@ class MatMulNBits:
         self.N, self.K, self.block_size, self.bias = N, K, block_size, bias
         self._zero = int(zero_points is not None)
         size = int(_L().i8q_matmul_nbits_packed_size(N, K, block_size, self._scale_type, self._zero))
-        if size == 0:
-            raise I8QError(_lib.ERR_UNSUPPORTED, "matmul_nbits_packed_size")
+        if size == 0:  # (the sizes are refused: by which code and why)
+            check(_L().i8q_matmul_nbits_pack(N, K, block_size, None, None, self._scale_type, None, None, 0, None),
+                  "matmul_nbits_pack")
         self.packed = _workspace(size, B.device, stream)
         self._read = (self.packed,) if bias is None else (self.packed, bias)  # by the calls
         self._streams = set()

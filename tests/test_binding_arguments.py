@@ -178,3 +178,24 @@ def test_kv_append_takes_its_stream_where_it_did(monkeypatch):
     k = torch.zeros((2, 1, 64))
     q.kv_append(cache, None, None, None, k, k, None, None, None, None, None, None, False, "side")
     assert seen == [("i8q_kv_append_norm", (None, "side"))]
+
+
+@pytest.mark.parametrize("N,K,block,code,what", [(0, 64, 32, -1, "N and K must"), (2, 64, 8, -2, "block_size must"),
+                                                 (2, 96, 48, -2, "block_size must")])
+def test_the_sizes_of_a_matmul_nbits(monkeypatch, N, K, block, code, what):
+    """Sizes that the library refuses come with its code and reason."""
+    from int8_quantized_gb300 import build
+    build.build()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    at = torch.device("cuda:0")
+    B, s = on(torch.zeros((N, K // block, block // 2), dtype=torch.uint8), at), on(torch.zeros((N, K // block)), at)
+    with pytest.raises(q.I8QError, match=what) as e:
+        q.MatMulNBits(B, s, K, block)
+    assert e.value.code == code
+
+
+@pytest.mark.parametrize("K,block", [(0, 32), (-64, 32), (64, 0), (64, -32)])
+def test_a_matmul_nbits_of_nothing(K, block):
+    at = torch.device("cuda:0")
+    with pytest.raises(ValueError, match="K and block_size"):
+        q.MatMulNBits(on(torch.zeros((2, 2, 16), dtype=torch.uint8), at), on(torch.zeros((2, 2)), at), K, block)
