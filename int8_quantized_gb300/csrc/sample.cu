@@ -643,10 +643,14 @@ extern "C" int i8q_sample(const void* logits, int type, int64_t rows, int64_t vo
   if (rows > 1 && row_stride < vocabulary) return fail(I8Q_ERR_INVALID_ARG, "sample: rows overlap (row_stride below vocabulary)");
   const uintptr_t es = type == I8Q_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % es) return fail(I8Q_ERR_INVALID_ARG, "sample: logits are not aligned to their type");
-  uint32_t* status = device_status_word();
-  if (!status) return fail(I8Q_ERR_CUDA, "sample: no status word");
   const i8q_sampling none{};
   const i8q_sampling& p = sampling ? *sampling : none;
+  for (const void* of_rows : {(const void*)random, (const void*)p.temperature, (const void*)p.top_k, (const void*)p.top_p,
+                              (const void*)p.min_p, (const void*)tokens, (const void*)logprobs})
+    if (reinterpret_cast<uintptr_t>(of_rows) % 4)
+      return fail(I8Q_ERR_INVALID_ARG, "sample: random, a setting, tokens or logprobs are not aligned to their type");
+  uint32_t* status = device_status_word();
+  if (!status) return fail(I8Q_ERR_CUDA, "sample: no status word");
   Args a{logits, row_stride, (int)vocabulary, random, p.temperature, p.top_k, p.top_p, p.min_p, tokens, logprobs, status};
   // CTAs of a row: what two on each SM leave room for, of 4096 tokens at least
   int S = 1;

@@ -25,3 +25,13 @@ def test_refused(lib, what, kw):  # noqa: F811
 
 def test_no_rows(lib):  # noqa: F811
     assert call(lib, rows=0, logits=None) == 0
+
+
+@pytest.mark.parametrize("which", ["random", "temperature", "top_k", "top_p", "min_p", "tokens", "logprobs"])
+def test_rows_numbers_that_are_not_aligned(lib, which):  # noqa: F811
+    """The kernel would read or write at an address that a GPU faults at."""
+    from int8_quantized_gb300 import _lib
+    at = {n: 4098 if n == which else 4096 for n in ("random", "tokens", "logprobs")}
+    s = _lib.SamplingStruct(**{n: 4098 if n == which else 4096 for n in ("temperature", "top_k", "top_p", "min_p")})
+    assert lib.i8q_sample(P, 1, 3, 100, 100, at["random"], ctypes.byref(s), at["tokens"], at["logprobs"], None) == -1
+    assert b"aligned to their type" in lib.i8q_last_error()
