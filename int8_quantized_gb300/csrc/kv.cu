@@ -191,9 +191,11 @@ __device__ __forceinline__ float inverse_rms(const float (&x)[N], int dim, float
 }
 
 // Rows of any alignment: one warp per row of q, k or v, lane l turns pairs
-// l, l + 32, ...  (16384 tokens of 48 rows of 128: 484 us, where rows that can
-// be read four elements at a time take 76 below.)
-template <class T, bool S8>
+// l, l + 32, ...  (16384 tokens of 48 rows of 128, bf16 into int8 pages: 474 us,
+// with norms 703, where rows that can be read four elements at a time take 78
+// and 142 below.  NORM is a form of its own: a branch in the one kernel took the
+// calls without norms from 474 to 601.)
+template <class T, bool S8, bool NORM>
 __global__ void __launch_bounds__(256)
 append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int64_t tokens,
               Rows q, Rows qo, Rows k, Rows v, Rotary r, Norm norm, uint32_t* status) {
@@ -223,9 +225,22 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
     const Rows& in = which == 0 ? q : (which == 1 ? k : v);
     const T* src = static_cast<const T*>(in.p) + t * in.token + head * in.head;
     const int turned = which == 2 ? 0 : r.pairs;
-    float y[I8Q_KV_MAX_HEAD_DIM / 32] = {};
+    float y[I8Q_KV_MAX_HEAD_DIM / 32];
     int at[I8Q_KV_MAX_HEAD_DIM / 32];
     uint32_t most = 0;
+    auto turn_pair = [&](int u, int j) {
+      float x1 = y[2 * u], x2 = y[2 * u + 1];
+      if (j < turned) {
+        const int a = (r.axis[j >> 4] >> ((j & 15) * 2)) & 3;
+        const int64_t g = (int64_t)r.positions[a * r.position_stride + t] * r.pairs + j;
+        const float cs = r.cos[g], sn = r.sin[g];
+        const float y1 = __fsub_rn(__fmul_rn(x1, cs), __fmul_rn(x2, sn));
+        x2 = __fadd_rn(__fmul_rn(x2, cs), __fmul_rn(x1, sn));
+        x1 = y1;
+      }
+      y[2 * u] = x1, y[2 * u + 1] = x2;
+      most = max(most, max(__float_as_uint(fabsf(x1)), __float_as_uint(fabsf(x2))));
+    };
 #pragma unroll
     for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 64; ++u) {
       const int j = lane + 32 * u;
@@ -234,31 +249,22 @@ append_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t
         const int e1 = split ? j : 2 * j, e2 = split ? j + r.pairs : 2 * j + 1;
         y[2 * u] = load1(src + e1), y[2 * u + 1] = load1(src + e2);
         at[2 * u] = e1, at[2 * u + 1] = e2;
+        if constexpr (!NORM) turn_pair(u, j);
+      } else if (NORM) {
+        y[2 * u] = y[2 * u + 1] = 0.0f;
       }
     }
-    const void* weight = which == 0 ? norm.q : which == 1 ? norm.k : nullptr;
-    if (weight) {
-      const float inverse = inverse_rms<32>(y, c.dim, norm.eps, 0xffffffffu);
+    if constexpr (NORM) {
+      const void* weight = which == 0 ? norm.q : which == 1 ? norm.k : nullptr;
+      if (weight) {
+        const float inverse = inverse_rms<32>(y, c.dim, norm.eps, 0xffffffffu);
 #pragma unroll
-      for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 32; ++u)
-        if (lane + 32 * (u / 2) < half) y[u] = __fmul_rn(__fmul_rn(y[u], inverse), weight_at(norm, weight, at[u]));
-    }
-#pragma unroll
-    for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 64; ++u) {
-      const int j = lane + 32 * u;
-      if (j < half) {
-        float x1 = y[2 * u], x2 = y[2 * u + 1];
-        if (j < turned) {
-          const int a = (r.axis[j >> 4] >> ((j & 15) * 2)) & 3;
-          const int64_t g = (int64_t)r.positions[a * r.position_stride + t] * r.pairs + j;
-          const float cs = r.cos[g], sn = r.sin[g];
-          const float y1 = __fsub_rn(__fmul_rn(x1, cs), __fmul_rn(x2, sn));
-          x2 = __fadd_rn(__fmul_rn(x2, cs), __fmul_rn(x1, sn));
-          x1 = y1;
-        }
-        y[2 * u] = x1, y[2 * u + 1] = x2;
-        most = max(most, max(__float_as_uint(fabsf(x1)), __float_as_uint(fabsf(x2))));
+        for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 32; ++u)
+          if (lane + 32 * (u / 2) < half) y[u] = __fmul_rn(__fmul_rn(y[u], inverse), weight_at(norm, weight, at[u]));
       }
+#pragma unroll
+      for (int u = 0; u < I8Q_KV_MAX_HEAD_DIM / 64; ++u)
+        if (lane + 32 * u < half) turn_pair(u, lane + 32 * u);
     }
     const int64_t dst = kv::row_at(c, page, head, off);
     if (which == 0) {
@@ -722,8 +728,11 @@ extern "C" int i8q_kv_append_norm(const i8q_kv_cache* cache, const i8q_page_tabl
         return n.q || n.k ? run(append_units_kernel<T, S8, L, true>) : run(append_units_kernel<T, S8, L, false>);
       });
     const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (q_heads + 2 * c.heads), 8), (int64_t)sm_count() * 64);
-    append_kernel<T, decltype(s8)::value>
-        <<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rq, ro, rk, rv, r, n, status);
+    auto run = [&](auto norms) {
+      append_kernel<T, decltype(s8)::value, decltype(norms)::value>
+          <<<(unsigned)blocks, 256, 0, s>>>(c, tab, seq, index, tokens, rq, ro, rk, rv, r, n, status);
+    };
+    n.q || n.k ? run(std::true_type()) : run(std::false_type());
     I8Q_LAUNCH_CHECK("kv_append");
     return I8Q_OK;
   });
