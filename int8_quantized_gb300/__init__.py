@@ -414,7 +414,8 @@ class MatMulNBits:
 
     def forward(self, A, Y, stream=None):
         """Y [rows, N] = A [rows, K] times the matrix, both fp32 or both bf16,
-        rows of any stride.  Returns Y."""
+        rows at any distance that keeps them apart; Y is not part of A.  Returns
+        Y."""
         if not isinstance(A, _Tensor) or not isinstance(Y, _Tensor) or A.device != self.device or Y.device != self.device:
             raise TypeError(f"A and Y must be tensors on {self.device}")
         if Y.dtype != A.dtype:
@@ -706,7 +707,7 @@ def _per_row(t, name, rows, dtype, device):
 
 def sample(logits, random, tokens, logprobs=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
     """The next token of each row of logits [rows, vocabulary] (fp32 or bf16,
-    rows of any stride) by its number of random (fp32 [rows], in [0, 1)):
+    rows at any distance that keeps them apart) by its number of random (fp32 [rows], in [0, 1)):
     tokens int32 [rows], logprobs fp32 [rows] or None.  temperature, top_p,
     min_p: fp32 [rows], top_k int32 [rows], each None: off.  See i8q_sample.
     Returns tokens."""

@@ -368,7 +368,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
 // products are scalar: the compiler fuses a paired sum with its products.
 constexpr int kUnitThreads = 64;
 // NORM: 16384 tokens of 40 normed rows of 128 123 us, without norms into the same
-// bf16 pages 76: 150 instructions more a lane and row.
+// bf16 pages 80 (int8 pages 142 and 78; fp32 rows 154 and 134, 165 and 132): 150
+// instructions more a lane and row, 0.73 of the issue slots, and 80 registers for
+// 48, so that 22 warps an SM are there to hide a token's chain of loads (2.3 cycles
+// of it per issue).  Two forms of fp32 rows into int8 pages spill one register.
 template <class T, bool S8, int L, bool NORM>
 __global__ void __launch_bounds__(kUnitThreads)
 append_units_kernel(Cache c, Table tab, const int32_t* __restrict__ seq, const int32_t* __restrict__ index, int splits,

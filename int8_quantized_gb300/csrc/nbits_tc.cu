@@ -10,10 +10,15 @@
 //
 // The matrix's bytes take 4.8 us of 64 x 4096 -> 14336, this kernel 21 (32 rows
 // 17, 16 rows 15), mma.sync (nbits.cu) 57, which for up to 8 rows is the faster
-// (1 row 10 us and 14.4).  What bounds it is the line of waits of a chunk: about
-// 780 cycles, whatever the rows, of which the four summing warps' 1000 (a wait
-// for the scales 240, for the products 370 although they are there, the sums 220)
-// are the longest.  Tried at the same rate: two chunks at a time, two groups of
+// (1 row 10 us and 14.4).  There 112 CTAs have a tile of outputs each and the
+// whole k; by clock stamps of a CTA's summing warps, in cycles (blocks of 64; 16,
+// 32 and 64 rows): start and first chunk 5000, 4900 and 5200, each of the 31 other
+// chunks 650, 710 and 860, output 1420, 2710 and 5190, 27000, 29800 and 37500 in
+// all.  A chunk is a line of waits between the roles, with a wait for each 16
+// columns of sums in the summing warps (blocks of 128 of 64 rows 720, of 32
+// 1620); the output writes a row's elements of two bytes one after the other; 40
+// of the 152 SMs have no tile, and every split of k that uses them has the longer
+// line (share_k).  Tried at the same rate: two chunks at a time, two groups of
 // summing warps, blocks' sums twice in TMEM, twice the codes on their way.
 #include <cooperative_groups.h>
 

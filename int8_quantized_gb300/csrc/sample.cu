@@ -214,8 +214,9 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {
 // of the exponent, and the keys of the bin in which the border lies; the kept
 // weight of each warp; the warp in which the random number falls alone.  Bound
 // by the chain of these where rows are few (1 x 32000 bf16 with top-p 26 us, 12
-// without), by issue slots where they are many (128 x 128000: bf16 126 us, fp32
-// 198; without top-p 65 for bf16).
+// without), by issue slots where they are many (128 x 128000: bf16 121 us, fp32
+// 194; without top-p 65 for bf16).  Tokens kept in registers or shared memory
+// between the passes were not tried.
 template <class T, bool TABLE>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const __grid_constant__ Args a) {
